@@ -69,7 +69,8 @@ extern "C" {
 #define MLA_DEVERR_BAD_PAGE 1u   /* block_table entry outside [0, num_pages), *
                                   * or a length needing more page slots than *
                                   * block_table_stride                       */
-#define MLA_DEVERR_BAD_INDEX 2u  /* sparse index < -1 or >= s_kv              */
+#define MLA_DEVERR_BAD_INDEX 2u  /* sparse index < -1 or >= s_kv, or a token  *
+                                  * position without a rope_table row        */
 #define MLA_DEVERR_TIMEOUT 4u    /* an internal wait ran out (kernel bailed)  */
 #define MLA_DEVERR_METADATA 8u   /* metadata built for another shape (nothing *
                                   * was computed), or for other lengths      */
@@ -87,6 +88,12 @@ extern "C" {
                           * README, "FP8 / FP4 KV Cache Format").  Keys are 512  *
                           * wide and the value is the whole key: q is            *
                           * [batch, s_q, h_q, 512] and out keeps 512 columns.    */
+
+/* ------------------------------------------------ order of rotated pairs
+ * Which of the 64 rotated columns turn together: angle i of a position turns
+ * the pair (a, b) into (a cos - b sin, a sin + b cos). */
+#define MLA_ROPE_PAIRS 0  /* columns (2i, 2i + 1), i = 0 .. 31 */
+#define MLA_ROPE_HALVES 1 /* columns (i, i + 32),  i = 0 .. 31 */
 
 /* Human-readable name of a status code. Never NULL. */
 const char* mla_status_string(int status);
@@ -361,6 +368,138 @@ int mla_decode_noalloc(const void* q, const void* kv_cache, int kv_format, int64
 int mla_combine(const void* metadata, int batch, int s_q, int h_q, int num_sm_parts,
                 const void* workspace, const float* attn_sink, void* out, float* lse,
                 cudaStream_t stream);
+
+/* ======================================================== a step's tokens
+ *
+ * What a layer does with a step's new tokens around the attention calls
+ * above: their latent rows go into the cache (mla_append_kv), their queries
+ * are normalised and rotated (mla_query_norm_rope), and a layer with a sliding
+ * window attends through mla_window_decode.  No schedule and no host copy of
+ * the lengths is involved, so the three can be captured in a CUDA graph once
+ * and replayed while the lengths, which stay in device memory, grow.
+ *
+ * Positions, common to the three: the call has `s` token slots per request
+ * (s_new, s_q).
+ *   cache_seqlens [batch] int32  cached tokens per request, the new ones
+ *                 included (as for mla_decode);
+ *   new_lens      optional [batch] int32: how many of the request's slots, from
+ *                 the first, hold new tokens (clamped to [0, s]; NULL: all).
+ * Token slot j of request b is at position
+ *   cache_seqlens[b] - new_lens[b] + j.
+ * Slots j >= new_lens[b] and slots whose position would be negative are
+ * padding.  batch * s <= 2^24.
+ *
+ * Rotation, common to mla_append_kv and mla_query_norm_rope: rope_table is
+ * [rope_rows, 64] fp32, row p holding the 32 cosines, then the 32 sines of
+ * position p's angles (any scaling of the angles is the caller's); NULL with
+ * rope_rows = 0 leaves out the rotation.  A token whose position has no row
+ * sets MLA_DEVERR_BAD_INDEX and nothing is written for it.
+ *
+ * Norm: norm_eps > 0 multiplies a row by 1 / sqrt(mean(x^2) + norm_eps) and
+ * then by norm_weight (fp32, one per column; NULL: ones); norm_eps = 0 leaves
+ * out the norm (norm_weight is then NULL).  All arithmetic is fp32 and every
+ * value is rounded once, where it is written.
+ */
+
+/*
+ * Writes the new tokens' rows into the paged cache.
+ *
+ *  kv_new       token slot j of request b at (b * s_new + j) * token_stride
+ *               elements, bf16: the 512 latent columns, then the 64 position
+ *               columns (MLA_KV_FP8_528: 512 columns, the last 64 of which are
+ *               rotated).  token_stride is a multiple of 8, so the rows may
+ *               lie among other columns of a projection's output.
+ *  The norm is over the 512 latent columns (MLA_KV_FP8_528: before the
+ *  rotation); the 64 position columns of the 576-wide formats are rotated only.
+ *  kv_cache     as for mla_decode; token at position p goes to slot p mod 64 of
+ *               page block_table[b, p / 64].  Nothing else of the cache is
+ *               written.  FP8 formats: scale = absmax / 448 of each 128 columns
+ *               (1 where all are 0), or the smallest power of two at or above
+ *               that of each 32 columns; codes = column / scale rounded to
+ *               nearest even.  A non-finite column makes no more than its own
+ *               token's row non-finite.
+ *  Every new token needs a slot of its own: where two tokens of a call name the
+ *  same slot (a page shared by requests), what it holds afterwards may be a
+ *  mixture of both.  kv_new must not overlap the cache.
+ *  block_table  [batch] rows of max_pages int32 entries, block_table_stride
+ *               entries apart (>= max_pages).
+ *  A page entry outside [0, num_pages), or a page slot past a row's max_pages,
+ *  sets MLA_DEVERR_BAD_PAGE and nothing is written for that
+ *  token.  Padding slots are not read for their position and write nothing.
+ */
+int mla_append_kv(const void* kv_new, int64_t token_stride, const int32_t* cache_seqlens,
+                  const int32_t* new_lens, int batch, int s_new, const float* rope_table,
+                  int64_t rope_rows, int rope_style, const float* norm_weight, float norm_eps,
+                  void* kv_cache, int kv_format, int64_t num_pages, const int32_t* block_table,
+                  int64_t block_table_stride, int64_t max_pages, uint32_t* err,
+                  cudaStream_t stream);
+
+/*
+ * RMS norm of every query head over its d columns and rotation of the last 64.
+ *
+ *  q, out       bf16; head h of token slot j of request b at
+ *               (b * s_q + j) * token_stride + h * head_stride elements.
+ *               Strides are multiples of 8 and leave heads apart
+ *               (head_stride >= d, token_stride >= (h_q - 1) * head_stride + d).
+ *               out may be q itself with the same strides; otherwise the two
+ *               must not overlap.  With the 576-wide absorbed queries of
+ *               mla_decode this is the rotation of columns 512 .. 575; before
+ *               absorption d is the head's own width.
+ *  d            64 .. 576, a multiple of 64.  Any h_q >= 1;
+ *               batch * s_q * h_q < 2^31.
+ *  Rows of padding slots (and of tokens without a table row) stay as they were
+ *  in out.
+ */
+int mla_query_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const int32_t* cache_seqlens, const int32_t* new_lens, int batch, int s_q,
+                        int h_q, int d, const float* rope_table, int64_t rope_rows, int rope_style,
+                        const float* norm_weight, float norm_eps, void* out,
+                        int64_t out_token_stride, int64_t out_head_stride, uint32_t* err,
+                        cudaStream_t stream);
+
+/*
+ * Size in bytes of mla_window_decode's workspace for these arguments: 0, or
+ * batch * s_q * pieces rows of fp32 partial outputs and LSEs when the call cuts
+ * every token's keys into several pieces (few tokens, long windows).  One
+ * workspace serves one call at a time.
+ */
+int mla_window_workspace_size(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts,
+                              size_t* bytes);
+
+/*
+ * Paged decode with a sliding window: the token at position p attends to the
+ * keys t <= p with
+ *     t > p - window   or   t < sinks
+ * (the last `window` tokens, itself included, and the request's first `sinks`
+ * tokens).  window >= 1, sinks >= 0; a window of at least the length is plain
+ * causal attention.  One token a request is a decode step; any s_q with
+ * batch * s_q <= 2^24 is accepted, so a chunk of a prompt goes through the same
+ * call (its keys appended first).
+ *
+ *  q, kv_cache, kv_format, num_pages, softmax_scale, out, lse: as for
+ *               mla_decode.
+ *  block_table  as for mla_append_kv; only the entries of pages that hold a
+ *               visible key are read, so pages that the window has left (and
+ *               that hold none of the first tokens) may have been given away.
+ *               A bad entry, or one past max_pages, sets
+ *               MLA_DEVERR_BAD_PAGE; the outputs of tokens that need it are
+ *               then unspecified.
+ *  Cache slots that a token does not see may hold anything, NaN included.
+ *  Lengths above 2^30 count as 2^30.
+ *  attn_sink    optional [h_q] fp32, as for mla_sparse_decode.
+ *  num_sm_parts from mla_num_sm_parts (any value >= 1 gives the same result up
+ *               to rounding).
+ *  workspace    mla_window_workspace_size() bytes, 16-byte aligned; NULL when
+ *               that is 0.
+ *  A token that sees no key (padding slots among them) gets out = 0,
+ *  lse = -inf.
+ */
+int mla_window_decode(const void* q, const void* kv_cache, int kv_format, int64_t num_pages,
+                      const int32_t* block_table, int64_t block_table_stride, int64_t max_pages,
+                      const int32_t* cache_seqlens, const int32_t* new_lens, int batch, int s_q,
+                      int h_q, int window, int sinks, float softmax_scale, const float* attn_sink,
+                      int num_sm_parts, void* workspace, void* out, float* lse, uint32_t* err,
+                      cudaStream_t stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

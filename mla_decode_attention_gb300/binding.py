@@ -8,6 +8,7 @@ first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -21,6 +22,8 @@ LIB_PATH = os.path.join(HERE, "libmla_decode.so")
 MLA_KV_BF16 = 0
 MLA_KV_FP8_656 = 1
 MLA_KV_FP8_528 = 2
+MLA_ROPE_PAIRS = 0
+MLA_ROPE_HALVES = 1
 MLA_DEVERR_BAD_PAGE = 1
 MLA_DEVERR_BAD_INDEX = 2
 MLA_DEVERR_TIMEOUT = 4
@@ -59,6 +62,13 @@ _SIGS = {
                                 _vp, _vp]),
     "mla_combine": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
     "mla_check_wait_timeout": (_i, [_vp, _vp]),
+    "mla_append_kv": (_i, [_vp, _i64, _vp, _vp, _i, _i, _vp, _i64, _i, _vp, _f, _vp, _i, _i64, _vp,
+                           _i64, _i64, _vp, _vp]),
+    "mla_query_norm_rope": (_i, [_vp, _i64, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i64, _i, _vp, _f,
+                                 _vp, _i64, _i64, _vp, _vp]),
+    "mla_window_workspace_size": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "mla_window_decode": (_i, [_vp, _vp, _i, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp,
+                               _i, _vp, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -325,6 +335,184 @@ def mla_combine(metadata: torch.Tensor, batch: int, s_q: int, h_q: int, num_sm_p
                              _ptr(attn_sink), _ptr(out), _ptr(lse), _stream(stream)))
 
 
+# ---------------------------------------------------------------- a step's tokens
+
+def _call_on(name, device, stream, *tensors):
+    """Checks that every given tensor is on ``device``; returns (function, raw
+    stream, context): the call is made with that device current, on its
+    current stream unless one is given."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: tensors are on {t.device} and {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    here = device.index == torch.cuda.current_device()
+    return getattr(_lib or lib(), name), raw, (contextlib.nullcontext() if here else torch.cuda.device(device))
+
+
+def _vector(t, dtype, n, name):
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
+
+
+def _block_table(block_table, batch):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch \
+            or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table must be an int32 tensor [batch, max_pages] with unit column stride")
+    return block_table.stride(0), block_table.shape[1]
+
+
+def _cache(kv_cache, kv_format):
+    if kv_format not in _FORMATS:
+        raise ValueError(f"unknown kv_format {kv_format}")
+    d_qk, token_bytes = _FORMATS[kv_format]
+    want = torch.bfloat16 if kv_format == MLA_KV_BF16 else torch.uint8
+    if kv_cache.dtype != want or kv_cache.dim() != 3 or kv_cache.shape[1:] != (64, token_bytes or 576) \
+            or not kv_cache.is_contiguous():
+        raise ValueError(f"kv_format {kv_format} needs a contiguous {want} kv_cache [pages, 64, {token_bytes or 576}]")
+    return d_qk
+
+
+def _rope(rope_table):
+    if rope_table is None:
+        return 0
+    if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or rope_table.shape[1] != 64 \
+            or not rope_table.is_contiguous():
+        raise ValueError("rope_table must be a contiguous float32 tensor [positions, 64]")
+    return rope_table.shape[0]
+
+
+def mla_append_kv(kv_new: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, block_table: torch.Tensor,
+                  cache_seqlens: torch.Tensor, rope_table: Optional[torch.Tensor] = None,
+                  rope_style: int = MLA_ROPE_PAIRS, norm_weight: Optional[torch.Tensor] = None,
+                  norm_eps: float = 0.0, new_lens: Optional[torch.Tensor] = None,
+                  err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Writes the new tokens' latent rows kv_new [b, s_new, 576] bf16 ([b, s_new,
+    512] for MLA_KV_FP8_528; unit column stride, token slots evenly spaced) into
+    kv_cache, normalised (norm_eps > 0; norm_weight [512] float32) and rotated
+    (rope_table [positions, 64] float32: 32 cosines, 32 sines).  cache_seqlens
+    [b] int32 counts the new tokens; new_lens [b] int32 says how many of the
+    s_new slots hold one (all of them when None)."""
+    dev = kv_cache.device
+    fn, raw, on = _call_on("mla_append_kv", dev, stream, kv_new, block_table, cache_seqlens, rope_table, norm_weight,
+                           new_lens, err)
+    d = _cache(kv_cache, kv_format)
+    if kv_new.dtype != torch.bfloat16 or kv_new.dim() != 3 or kv_new.shape[2] != d or kv_new.stride(2) != 1:
+        raise ValueError(f"kv_new must be a bfloat16 tensor [batch, s_new, {d}] with unit column stride")
+    b, s, _ = kv_new.shape
+    token = kv_new.stride(1) if s > 1 else kv_new.stride(0) if b > 1 else max(d, kv_new.stride(1) & ~7)
+    if b > 1 and s > 1 and kv_new.stride(0) != s * token:
+        raise ValueError("kv_new's token slots must be evenly spaced over the batch")
+    _vector(cache_seqlens, torch.int32, b, "cache_seqlens")
+    if new_lens is not None:
+        _vector(new_lens, torch.int32, b, "new_lens")
+    if norm_weight is not None:
+        _vector(norm_weight, torch.float32, 512, "norm_weight")
+    if err is not None:
+        _vector(err, torch.int32, 1, "err")
+    bt = _block_table(block_table, b)
+    rows = _rope(rope_table)
+    with on:
+        _check("mla_append_kv", fn(
+            kv_new.data_ptr(), token, cache_seqlens.data_ptr(), _ptr(new_lens), b, s, _ptr(rope_table), rows,
+            rope_style, _ptr(norm_weight), norm_eps, kv_cache.data_ptr(), kv_format, kv_cache.shape[0],
+            block_table.data_ptr(), *bt, _ptr(err), raw))
+
+
+def mla_query_norm_rope(q: torch.Tensor, out: torch.Tensor, cache_seqlens: torch.Tensor,
+                        rope_table: Optional[torch.Tensor] = None, rope_style: int = MLA_ROPE_PAIRS,
+                        norm_weight: Optional[torch.Tensor] = None, norm_eps: float = 0.0,
+                        new_lens: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """RMS norm of every head of q [b, s_q, h, d] bf16 (norm_eps > 0; norm_weight
+    [d] float32) and rotation of its last 64 columns, into out (q itself, or a
+    tensor of the same shape that does not overlap it).  Rows of padding slots
+    stay as they were in out.  cache_seqlens, new_lens, rope_table: as for
+    mla_append_kv."""
+    dev = q.device
+    fn, raw, on = _call_on("mla_query_norm_rope", dev, stream, out, cache_seqlens, rope_table, norm_weight, new_lens,
+                           err)
+    if q.dim() != 4 or q.shape != out.shape:
+        raise ValueError("q and out must be [batch, s_q, h_q, d]")
+    b, s, h, d = q.shape
+    strides = []
+    for t, name in ((q, "q"), (out, "out")):
+        if t.dtype != torch.bfloat16 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a bfloat16 tensor with unit column stride")
+        sb, ss, sh, _ = t.stride()
+        head = sh if h > 1 else d
+        token = ss if s > 1 else sb if b > 1 else h * head
+        if b > 1 and s > 1 and sb != s * token:
+            raise ValueError(f"{name}'s token slots must be evenly spaced over the batch")
+        strides += [token, head]
+    _vector(cache_seqlens, torch.int32, b, "cache_seqlens")
+    if new_lens is not None:
+        _vector(new_lens, torch.int32, b, "new_lens")
+    if norm_weight is not None:
+        _vector(norm_weight, torch.float32, d, "norm_weight")
+    if err is not None:
+        _vector(err, torch.int32, 1, "err")
+    rows = _rope(rope_table)
+    with on:
+        _check("mla_query_norm_rope", fn(
+            q.data_ptr(), strides[0], strides[1], cache_seqlens.data_ptr(), _ptr(new_lens), b, s, h, d,
+            _ptr(rope_table), rows, rope_style, _ptr(norm_weight), norm_eps, out.data_ptr(), strides[2], strides[3],
+            _ptr(err), raw))
+
+
+def mla_window_workspace_size(batch: int, s_q: int, h_q: int, window: int, sinks: int, num_sm_parts: int) -> int:
+    n = _sz()
+    _check("mla_window_workspace_size",
+           lib().mla_window_workspace_size(batch, s_q, h_q, window, sinks, num_sm_parts, ctypes.byref(n)))
+    return n.value
+
+
+def mla_window_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, block_table: torch.Tensor,
+                      cache_seqlens: torch.Tensor, softmax_scale: float, window: int, sinks: int, num_sm_parts: int,
+                      workspace: Optional[torch.Tensor], out: torch.Tensor, lse: torch.Tensor,
+                      err: Optional[torch.Tensor] = None, stream=None, attn_sink: Optional[torch.Tensor] = None,
+                      new_lens: Optional[torch.Tensor] = None) -> None:
+    """Paged decode over the last ``window`` cached tokens of every query token
+    and the request's first ``sinks``: q [b, s_q, h, 576] bf16 ([.., 512] for
+    MLA_KV_FP8_528), caches and block_table as for mla_decode; out [b, s_q, h,
+    512] bf16, lse [b, h, s_q] float32 (0 and -inf for a token that sees no key).
+    attn_sink: optional [h] float32.  cache_seqlens, new_lens: as for
+    mla_append_kv.  workspace: mla_window_workspace_size() bytes (None when
+    that is 0), float32."""
+    dev = q.device
+    fn, raw, on = _call_on("mla_window_decode", dev, stream, kv_cache, block_table, cache_seqlens, workspace, out, lse,
+                           err, attn_sink, new_lens)
+    d = _cache(kv_cache, kv_format)
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[3] != d or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous bfloat16 tensor [batch, s_q, h_q, {d}]")
+    b, s, h, _ = q.shape
+    if out.dtype != torch.bfloat16 or out.shape != (b, s, h, 512) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bfloat16 tensor [batch, s_q, h_q, 512]")
+    _vector(lse, torch.float32, b * h * s, "lse")
+    _vector(cache_seqlens, torch.int32, b, "cache_seqlens")
+    if new_lens is not None:
+        _vector(new_lens, torch.int32, b, "new_lens")
+    if attn_sink is not None:
+        _vector(attn_sink, torch.float32, h, "attn_sink")
+    if err is not None:
+        _vector(err, torch.int32, 1, "err")
+    need = _sz()
+    _check("mla_window_workspace_size",
+           _lib.mla_window_workspace_size(b, s, h, window, sinks, num_sm_parts, ctypes.byref(need)))
+    if need.value and (workspace is None or workspace.numel() * workspace.element_size() < need.value
+                       or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor of at least {need.value} bytes")
+    bt = _block_table(block_table, b)
+    with on:
+        _check("mla_window_decode", fn(
+            q.data_ptr(), kv_cache.data_ptr(), kv_format, kv_cache.shape[0], block_table.data_ptr(), *bt,
+            cache_seqlens.data_ptr(), _ptr(new_lens), b, s, h, window, sinks, softmax_scale, _ptr(attn_sink),
+            num_sm_parts, _ptr(workspace) if need.value else None, out.data_ptr(), lse.data_ptr(), _ptr(err), raw))
+
+
 def mla_check_wait_timeout(err: torch.Tensor, stream=None) -> None:
     """Runs the library's bounded wait on a barrier nothing completes; the
     kernel ORs MLA_DEVERR_TIMEOUT into err (uint32 device word) after ~2 s."""
@@ -349,6 +537,21 @@ class DecodeBuffers:
         wbytes = mla_workspace_size(batch, s_q, h_q, self.num_sm_parts)
         self.metadata = torch.zeros(mbytes // 4, dtype=torch.int32, device=dev)
         self.workspace = torch.empty(wbytes // 4, dtype=torch.float32, device=dev)
+        self.out = torch.empty(batch, s_q, h_q, 512, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(batch, h_q, s_q, dtype=torch.float32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+class WindowBuffers:
+    """Device buffers of mla_window_decode for one shape: workspace (None when
+    the shape needs none), out, lse, err."""
+
+    def __init__(self, batch: int, s_q: int, h_q: int, window: int, sinks: int, device="cuda", num_sm_parts=None):
+        dev = torch.device(device)
+        idx = dev.index if dev.index is not None else torch.cuda.current_device()
+        self.num_sm_parts = num_sm_parts or mla_num_sm_parts(idx, h_q)
+        nbytes = mla_window_workspace_size(batch, s_q, h_q, window, sinks, self.num_sm_parts)
+        self.workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=dev) if nbytes else None
         self.out = torch.empty(batch, s_q, h_q, 512, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(batch, h_q, s_q, dtype=torch.float32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)

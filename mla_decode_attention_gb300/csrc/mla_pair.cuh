@@ -119,6 +119,7 @@ struct Bars {
   uint64_t p_full[2];                              // output CTA, completed by bulk copies
   uint64_t pv_done[2], o_full, o_free, o_drained, o_rescaled;  // output CTA
   uint64_t side_read[2];                           // output CTA: row threads read P's side data
+  uint64_t v_clean;                                // output CTA, windowed: rows of keys not seen are zero
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -167,7 +168,7 @@ __device__ __forceinline__ int issuer_index(int warp) { return warp == 0 ? 0 : (
 // query rows as [9 chunks][rows][64 columns] with [2 x 128 x 64] boxes (a
 // quarter of the latent part of one token's 128 rows), tm_qr as [rows][576]
 // with [128 x 64] boxes (its RoPE part).
-template <bool kSparse>
+template <bool kSparse, bool kWindow = false>
 __global__ void __maxnreg__(kSparse ? 128 : 224)
     mla_pair_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_qa,
                     const __grid_constant__ CUtensorMap tm_qb, const __grid_constant__ CUtensorMap tm_ql,
@@ -211,6 +212,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
     mbar_init(smem_u32(&bars->o_free), 4);
     mbar_init(smem_u32(&bars->o_drained), 1);
     mbar_init(smem_u32(&bars->o_rescaled), 4);
+    mbar_init(smem_u32(&bars->v_clean), 4);
     bars->abort = 0;
     fence_mbarrier_init();
     if (rank == 1) {  // both P buffers start empty and armed for their first copy
@@ -232,8 +234,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
   // whole-sequence schedule is walked) start towards L2 before the wait: a
   // prefetch only warms L2, so rows a preceding kernel is still writing are
   // read for real after the wait all the same.
-  if (rank == 0 && threadIdx.x == 32 * 2 && part < p.batch * p.s_q)
-    prefetch_l2(p.q + static_cast<int64_t>(part) * kRows * kDqk, kRows * kDqk * 2);
+  if (rank == 0 && threadIdx.x == 32 * 2 && part < p.batch * p.s_q * (kWindow ? p.n_split : 1))
+    prefetch_l2(p.q + static_cast<int64_t>(kWindow ? part / p.n_split : part) * kRows * kDqk, kRows * kDqk * 2);
   pdl_wait_primary();
   pdl_launch_dependents();  // the combine may launch now; it waits for this grid to finish
   // Schedule B (whole sequences) is walked when it is at most kSplitPenalty
@@ -242,9 +244,10 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
   // better balance; a sparse tile takes about twice as long.
   constexpr int kSplitPenalty = kSparse ? 5 : 11;
   // The metadata must describe this call; otherwise nothing is read or written.
-  const bool meta_ok = meta_header_matches(p.meta, p.batch, p.s_q, p.num_parts, p.topk, p.causal);
-  const int32_t* meta = meta_ok ? schedule_for(p.meta, kSplitPenalty) : p.meta;
-  if (blockIdx.x == 0 && threadIdx.x == blockDim.x - 1) {  // a thread with no work at the start
+  // (A windowed call has none.)
+  const bool meta_ok = kWindow || meta_header_matches(p.meta, p.batch, p.s_q, p.num_parts, p.topk, p.causal);
+  const int32_t* meta = !kWindow && meta_ok ? schedule_for(p.meta, kSplitPenalty) : p.meta;
+  if (!kWindow && blockIdx.x == 0 && threadIdx.x == blockDim.x - 1) {  // a thread with no work at the start
     // read by the combine after this grid: the schedule walked, or -1 when
     // the metadata was rejected (the combine then writes nothing), and
     // whether that schedule left anything to merge or fill
@@ -269,8 +272,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         constexpr int kIssuers = kSparse ? kKIssuersSparse : 2;
         const int pw = issuer_index(warp);
         const uint64_t pol = l2_policy_evict_first();
-        PartCursor cur = walked_part_cursor(p.meta, meta, part);
-        int q, t0, t1, split;
+        Pieces<kWindow> pc(p, meta, part);
         uint32_t tc = 0;
         int32_t issued[kKGroups];  // ring round of this issuer's last load per group slot
         for (int i = 0; i < kKGroups; ++i) issued[i] = -1;
@@ -290,18 +292,19 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           }
           q_issued = true;
         };
-        while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+        while (pc.next()) {
+          const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
           if (first) {
             first = false;
             if (pw == 0 && lane == 0) issue_first_q(q);
           }
           int32_t nid[4];  // sparse: the next tile's indices, requested one tile ahead
-          const int32_t keys = meta_seq(meta, p.num_parts, q)[kSKeys];
+          const int32_t keys = pc.keys();
           const int32_t* idx_row = p.indices + static_cast<int64_t>(q) * p.topk;
           const int32_t* bt_row = kSparse ? nullptr : bt_row_of(p, q);
           int32_t fallback = -2;  // sparse: first row the query names, found when a tile names none
           if constexpr (kSparse) load_idx4(p, q, t0, lane, keys, nid);
-          else if (pw == 0) check_seq_keys(p, q, keys);
+          else if (!kWindow && pw == 0) check_seq_keys(p, q, keys);
           for (int t = t0; t < t1; ++t, ++tc) {
             if (!ok) continue;
             int32_t y[4];
@@ -314,7 +317,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             } else {
 #pragma unroll
               for (int h2 = 0; h2 < 2; ++h2) {
-                int32_t blk = page_of(p, bt_row, keys, 2 * t + h2);
+                int32_t blk = page_of(p, bt_row, keys, pc.page(2 * t + h2));
                 if (blk < 0) {
                   if (p.err && pw == 0) atomicOr(p.err, MLA_DEVERR_BAD_PAGE);
                   blk = static_cast<int32_t>(p.num_pages);  // out of range: TMA fills zeros
@@ -368,12 +371,12 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
     } else if (warp == 1) {
       // ---------------------------------------------------- S = Q . K^T
       if (lane == 0) {
-        PartCursor cur = walked_part_cursor(p.meta, meta, part);
-        int q, t0, t1, split;
+        Pieces<kWindow> pc(p, meta, part);
         uint32_t tc = 0, item = 0, qtma_n = 0, qcp_n = 0;  // completed phases of q_tma, q_cp
         bool ok = true, q_pending = false;  // q_pending: a query box is in flight
         const uint64_t qpol = l2_policy_evict_first();
-        while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+        while (pc.next()) {
+          const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
           if (item > 0) {
             // a later piece's query rows: the RoPE part into kQRope and the
             // latent part two chunks at a time through the P staging buffer
@@ -485,20 +488,18 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       const uint32_t stage = base + kStage;
       const uint32_t prow = stage + (r >> 3) * 1024 + (r & 7) * 128;
       const float sc = p.scale_log2;
-      PartCursor cur = walked_part_cursor(p.meta, meta, part);
-      int q, t0, t1, split;
+      Pieces<kWindow> pc(p, meta, part);
       uint32_t tc = 0, item = 0;
       bool ok = true;
-      while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
-        const int32_t* srec = meta_seq(meta, p.num_parts, q);
-        const int32_t keys = srec[kSKeys];
+      while (pc.next()) {
+        const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
+        const int32_t keys = pc.keys();
         // the piece's query rows come by TMA and tcgen05.cp (QK issuer); the
         // next piece's rows (147 KB, contiguous) start towards L2
         if (r == 0) {
-          PartCursor nc = cur;
-          int nq, nt0, nt1, nsplit;
-          if (next_piece(meta, p.num_parts, &nc, &nq, &nt0, &nt1, &nsplit))
-            prefetch_l2(p.q + static_cast<int64_t>(nq) * kRows * kDqk, kRows * kDqk * 2);
+          Pieces<kWindow> npc = pc;
+          if (npc.next())
+            prefetch_l2(p.q + static_cast<int64_t>(npc.q) * kRows * kDqk, kRows * kDqk * 2);
         }
         float m_use = 0.f, lsum = 0.f, bsum = 0.f;
         for (int t = t0; t < t1; ++t, ++tc) {
@@ -522,8 +523,13 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             for (int k = 0; k < 4; ++k)
               vm[k] = __ballot_sync(0xffffffffu, sid[k] >= 0 && static_cast<int64_t>(sid[k]) < p.s_kv);
           }
+          if constexpr (kWindow) {
+            const WindowSpan span = pc.span();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) vm[k] = span.mask32(kPage * span.page(2 * t + (k >> 1)) + 32 * (k & 1));
+          }
           const int n_valid = keys - t * kTileTokens;  // >= 1; < 128 only on the last tile
-          const bool full = kSparse || n_valid >= kTileTokens;
+          const bool full = kSparse || (kWindow ? (vm[0] & vm[1] & vm[2] & vm[3]) == ~0u : n_valid >= kTileTokens);
           // Row max of the raw scores (the scale is positive) over the tile's
           // keys.  The first tile of a piece takes its reference from it.  A
           // later tile needs it only when its probabilities against the current
@@ -537,11 +543,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               float v[32];
               tmem_ld32(t_s + 32 * i, v);
               tmem_wait_ld();
-              if (!full) {
+              if (!kWindow && !full) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 32 * i + j < n_valid ? v[j] : -INFINITY;
               }
-              if constexpr (kSparse) {
+              if (kSparse || (kWindow && !full)) {
                 const uint32_t w = vm[0] * (i == 0) | vm[1] * (i == 1) | vm[2] * (i == 2) | vm[3] * (i == 3);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = (w >> j) & 1u ? v[j] : -INFINITY;
@@ -576,11 +582,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               float v[32];
               tmem_ld32(t_s + 32 * i, v);
               tmem_wait_ld();
-              if (!full) {  // keys past the end: s = -inf, p = 2^-inf = 0
+              if (!kWindow && !full) {  // keys past the end: s = -inf, p = 2^-inf = 0
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 32 * i + j < n_valid ? v[j] : -INFINITY;
               }
-              if constexpr (kSparse) {  // slots without a pool row: p = 0
+              if (kSparse || (kWindow && !full)) {  // slots without a pool row, keys not seen: p = 0
                 const uint32_t w = vm[0] * (i == 0) | vm[1] * (i == 1) | vm[2] * (i == 2) | vm[3] * (i == 3);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = (w >> j) & 1u ? v[j] : -INFINITY;
@@ -631,7 +637,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           if (t == t1 - 1) {
             float inv_l = bsum > 0.f ? 1.f / bsum : 0.f;
             // attention sink: applied with 1/l to a final row, by the combine to a split row
-            if (kSparse && p.attn_sink && srec[kSNSplits] == 1) {
+            if ((kSparse || kWindow) && p.attn_sink && pc.whole()) {
               const float lse_t = (lsum > 0.f && bsum > 0.f) ? (m_use + __log2f(lsum)) * 0.69314718055994531f
                                                              : -INFINITY;
               inv_l *= attn_sink_factor(lse_t, p.attn_sink[r]);
@@ -660,11 +666,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         const float lse_v = (lsum > 0.f && bsum > 0.f) ? (m_use + __log2f(lsum)) * 0.69314718055994531f
                                                        : -INFINITY;
         if (ok) {
-          if (srec[kSNSplits] == 1) {
+          if (pc.whole()) {
             const int b = q / p.s_q, j = q % p.s_q;
             p.lse[(static_cast<int64_t>(b) * kRows + r) * p.s_q + j] = lse_v;
           } else {
-            p.ws_lse[static_cast<int64_t>(srec[kSSplitOff] + split) * kRows + r] = lse_v;
+            p.ws_lse[pc.split_row() * kRows + r] = lse_v;
           }
         }
         ++item;
@@ -672,11 +678,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       if (kSparse && r == 0) bulk_wait_all();  // the last copy has landed in the peer
     } else if (warp == 3 && !kSparse) {
       // ---------------------------------------------------- P transfers (dense)
-      PartCursor cur = walked_part_cursor(p.meta, meta, part);
-      int q, t0, t1, split;
+      Pieces<kWindow> pc(p, meta, part);
       uint32_t tc = 0;
       bool ok = true;
-      while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+      while (pc.next()) {
+        const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
         for (int t = t0; t < t1; ++t, ++tc) {
           if (lane == 0 && tc > 0) bulk_wait_read_all();
           __syncwarp();
@@ -712,15 +718,15 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         constexpr int kIssuers = kSparse ? kVIssuersSparse : 2;
         const int pw = issuer_index(warp);
         const uint64_t pol = l2_policy_evict_first();
-        PartCursor cur = walked_part_cursor(p.meta, meta, part);
-        int q, t0, t1, split;
+        Pieces<kWindow> pc(p, meta, part);
         uint32_t tc = 0;
         int32_t issued[kVGroups];
         for (int i = 0; i < kVGroups; ++i) issued[i] = -1;
         bool ok = true;
-        while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+        while (pc.next()) {
+          const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
           int32_t nid[4];  // sparse: the next tile's indices, requested one tile ahead
-          const int32_t keys = meta_seq(meta, p.num_parts, q)[kSKeys];
+          const int32_t keys = pc.keys();
           const int32_t* idx_row = p.indices + static_cast<int64_t>(q) * p.topk;
           const int32_t* bt_row = kSparse ? nullptr : bt_row_of(p, q);
           int32_t fallback = -2;
@@ -737,7 +743,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             } else {
 #pragma unroll
               for (int h2 = 0; h2 < 2; ++h2) {
-                int32_t blk = page_of(p, bt_row, keys, 2 * t + h2);
+                int32_t blk = page_of(p, bt_row, keys, pc.page(2 * t + h2));
                 if (blk < 0) blk = static_cast<int32_t>(p.num_pages);
                 y[h2] = blk * kPage;
               }
@@ -782,11 +788,12 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
     } else if (warp == 1) {
       // ---------------------------------------------------- O += P . V
       if (lane == 0) {
-        PartCursor cur = walked_part_cursor(p.meta, meta, part);
-        int q, t0, t1, split;
+        Pieces<kWindow> pc(p, meta, part);
         uint32_t tc = 0, item = 0, rc = 0;
+        [[maybe_unused]] uint32_t vc = 0;  // windowed: tiles with keys not seen
         bool ok = true;
-        while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+        while (pc.next()) {
+          const int t0 = pc.t0, t1 = pc.t1;
           for (int t = t0; t < t1; ++t, ++tc) {
             if (!ok) continue;
             const uint32_t b = tc & 1;
@@ -805,6 +812,14 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             }
             if (!ok) continue;
             tc_fence_after();
+            if constexpr (kWindow) {
+              if (!pc.span().full_tile(t)) {  // the row warps have zeroed the rows of keys not seen
+                ok = mbar_wait(smem_u32(&bars->v_clean), vc & 1, abort_flag, p.err);
+                ++vc;
+                if (!ok) continue;
+                tc_fence_after();
+              }
+            }
             const uint64_t pdesc = sw128_desc(pbuf, 16, 1024);
             if constexpr (!kSparse) {
               // paged: V half hf (N = 256: 64-column blocks 1 KB apart, 8-token
@@ -848,16 +863,33 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       // ---------------------------------------------------- rescale, epilogue
       const int r = threadIdx.x - 128;
       const uint32_t t_o = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16);
-      PartCursor cur = walked_part_cursor(p.meta, meta, part);
-      int q, t0, t1, split;
+      Pieces<kWindow> pc(p, meta, part);
       uint32_t tc = 0, item = 0, rc = 0;
       bool ok = true;
-      while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
-        const int32_t* srec = meta_seq(meta, p.num_parts, q);
+      while (pc.next()) {
+        const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
         float inv_l = 0.f;
         for (int t = t0; t < t1; ++t, ++tc) {
           const uint32_t b = tc & 1;
           const uint32_t side = base + kPBuf0 + b * kPBufStride;
+          if constexpr (kWindow) {
+            if (!pc.span().full_tile(t)) {
+              // The rows of keys not seen become zeros before P.V reads them:
+              // their weight 0 times what is there could be NaN.  Thread r =
+              // key r of the tile.
+              for (int hf = 0; hf < 2; ++hf)
+                if (ok) ok = mbar_wait(smem_u32(&bars->vfull[hf]), tc & 1, abort_flag, p.err);
+              if (ok && !pc.sees(t, r)) {
+                const uint32_t row = base + (r >> 6) * kHalfPage + ((r & 63) >> 3) * 4096 + (r & 7) * 128;
+#pragma unroll 1
+                for (int u = 0; u < 64; ++u)
+                  st_shared_v4(row + (u >> 5) * 2 * kHalfPage + ((u >> 3) & 3) * 1024 + (((u + lane) & 7) << 4), 0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&bars->v_clean));
+            }
+          }
           if (ok) ok = mbar_wait_cluster(smem_u32(&bars->p_full[b]), (tc >> 1) & 1, abort_flag, p.err);
           ok = __all_sync(0xffffffffu, ok);
           float alpha = 1.f;
@@ -913,8 +945,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           // Thread r holds row r of O; each 128-byte slice of the warp's 32 rows
           // goes through a swizzled 4 KB staging area so that every global
           // store instruction writes four whole 128-byte row segments.
-          const bool final_out = srec[kSNSplits] == 1;
-          const int64_t row0 = (final_out ? static_cast<int64_t>(q) : static_cast<int64_t>(srec[kSSplitOff] + split)) *
+          const bool final_out = pc.whole();
+          const int64_t row0 = (final_out ? static_cast<int64_t>(q) : pc.split_row()) *
                                    kRows + 32 * (warp - 4);
           const uint32_t stg = base + kEpi + (warp - 4) * 4096;
           const int rr0 = lane >> 3, uu = lane & 7;
@@ -977,13 +1009,22 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));
         ++item;
       }
+      if constexpr (kWindow) {  // tokens that see no key: out = 0, lse = -inf
+        Pieces<true> e(p, nullptr, part);
+        while (pc.passed_empty && e.template next<true>()) {
+          const int b = e.q / p.s_q, j = e.q % p.s_q;
+          uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(e.q) * kRows * kDv);
+          for (int i = r; i < kRows * kDv / 8; i += kRowThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+          p.lse[(static_cast<int64_t>(b) * kRows + r) * p.s_q + j] = -INFINITY;
+        }
+      }
     } else if (warp == 3 && !kSparse) {
       // ---------------------------------------------------- P buffer hand-back
-      PartCursor cur = walked_part_cursor(p.meta, meta, part);
-      int q, t0, t1, split;
+      Pieces<kWindow> pc(p, meta, part);
       uint32_t tc = 0;
       bool ok = true;
-      while (next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+      while (pc.next()) {
+        const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
         for (int t = t0; t < t1; ++t, ++tc) {
           if (lane == 0 && ok) {
             const uint32_t b = tc & 1;

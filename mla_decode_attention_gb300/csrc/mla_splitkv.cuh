@@ -46,6 +46,7 @@
 #include "mla_internal.h"
 #include "mla_ptx.cuh"
 #include "mla_schedule.cuh"
+#include "mla_window.cuh"
 
 namespace mla {
 
@@ -111,7 +112,8 @@ struct SplitParams {
   const int32_t* meta;     // schedule metadata (read-only)
   int32_t* ws_ctrl;        // workspace control words: [0] = the schedule walked (for the combine)
   const int32_t* block_table;
-  int64_t bt_stride;       // dense: int32 entries per block-table row (page slots of a request)
+  int64_t bt_stride;       // dense: int32 entries from one block-table row to the next
+  int64_t bt_width;        // dense: entries of a row (page slots of a request)
   int64_t num_pages;       // dense: pages in the cache
   const int32_t* cache_seqlens;  // dense: [batch] lengths, checked against the metadata's key counts
   const int32_t* indices;  // sparse: [n_seq, topk]
@@ -135,6 +137,83 @@ struct SplitParams {
   int n_hblk;
   int rows;                // query rows loaded per CTA (min(h, 64))
   float scale_log2;        // softmax_scale * log2(e)
+  // windowed attention (no metadata): see mla_window.cuh
+  const int32_t* new_lens; // optional [batch]
+  int window, sinks;
+  int n_split;             // pieces that each query token's tiles are cut into
+};
+
+// The pieces that part `part` walks: next() moves to a piece (tiles [t0, t1) of
+// query token q, split `split`); page(e) is the logical page of tile list
+// entry e (tile t holds entries 2t, 2t + 1), whole() whether the token's tiles
+// are all in this piece, split_row() the piece's row of the split workspace.
+// By the schedule metadata:
+template <bool kWindow>
+struct Pieces {
+  const SplitParams& p;
+  const int32_t* meta;
+  PartCursor cur;
+  int q, t0, t1, split;
+  __device__ __forceinline__ Pieces(const SplitParams& prm, const int32_t* walked, int part)
+      : p(prm), meta(walked), cur(walked_part_cursor(prm.meta, walked, part)) {}
+  __device__ __forceinline__ bool next() { return next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split); }
+  __device__ __forceinline__ const int32_t* rec() const { return meta_seq(meta, p.num_parts, q); }
+  __device__ __forceinline__ int32_t keys() const { return rec()[kSKeys]; }
+  __device__ __forceinline__ int32_t page(int32_t e) const { return e; }
+  __device__ __forceinline__ bool whole() const { return rec()[kSNSplits] == 1; }
+  __device__ __forceinline__ int64_t split_row() const { return static_cast<int64_t>(rec()[kSSplitOff] + split); }
+};
+
+// By the token's position and window.  Only the position is kept: what follows
+// from it is computed where it is used, since the softmax threads of the one-SM
+// kernel have no registers to hold it through a tile (they spilled).
+template <>
+struct Pieces<true> {
+  const SplitParams& p;
+  int item, q, t0, t1;
+  int32_t end;
+  bool passed_empty = false;  // a token that sees no key was passed over
+  __device__ __forceinline__ Pieces(const SplitParams& prm, const int32_t*, int part) : p(prm), item(part) {}
+  // Moves to the next piece; with kEmpty to the next token that sees no key
+  // instead (these have no piece).
+  template <bool kEmpty = false>
+  __device__ __forceinline__ bool next() {
+    const int items = p.batch * p.s_q * p.n_split;
+    while (item < items) {
+      q = item / p.n_split;
+      const int split = item - q * p.n_split;
+      item += p.num_parts;
+      const int b = q / p.s_q;
+      end = window_end(p.cache_seqlens, p.new_lens, p.s_q, b, q - b * p.s_q);
+      const int tiles = window_span(end, p.window, p.sinks).tiles;
+      if (kEmpty) {
+        if (tiles == 0 && split == 0) return true;
+        continue;
+      }
+      passed_empty |= tiles == 0;
+      const int pieces = window_pieces(tiles, p.n_split);
+      if (split >= pieces) continue;
+      window_piece(tiles, pieces, split, &t0, &t1);
+      return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ WindowSpan span() const {
+    int32_t e = end;
+    asm volatile("" : "+r"(e));  // not to be computed ahead of its use
+    return window_span(e, p.window, p.sinks);
+  }
+  // whether the token sees key i of tile t
+  __device__ __forceinline__ bool sees(int t, int i) const {
+    const WindowSpan w = span();
+    return w.sees(kPage * w.page(2 * t + (i >> 6)) + (i & 63));
+  }
+  __device__ __forceinline__ int32_t keys() const { return end; }
+  __device__ __forceinline__ int32_t page(int32_t e) const { return span().page(e); }
+  __device__ __forceinline__ bool whole() const { return window_pieces(span().tiles, p.n_split) == 1; }
+  __device__ __forceinline__ int64_t split_row() const {  // q * n_split + split: the item itself
+    return static_cast<int64_t>(item) - p.num_parts;
+  }
 };
 
 struct SmemSmall {
@@ -246,14 +325,14 @@ __device__ __forceinline__ void load_bcast32(const float* src, float (&dst)[32])
 
 // Physical page of logical page `pg` of a sequence with `keys` keys whose
 // block-table row is `bt_row`, or -1 when there is none: the entry is outside
-// [0, num_pages), or the page slot lies past the row's bt_stride entries
+// [0, num_pages), or the page slot lies past the row's bt_width entries
 // (more keys than the row can address).  Pages past the last one of the
 // sequence (the second page of a tile's last 64-key half) map to the last.
 __device__ __forceinline__ int32_t page_of(const SplitParams& p, const int32_t* bt_row, int32_t keys,
                                            int pg) {
   const int last = (keys - 1) / kPage;
   const int slot = pg < last ? pg : last;
-  if (static_cast<int64_t>(slot) >= p.bt_stride) return -1;
+  if (static_cast<int64_t>(slot) >= p.bt_width) return -1;
   const int32_t blk = bt_row[slot];
   return (blk < 0 || static_cast<int64_t>(blk) >= p.num_pages) ? -1 : blk;
 }
@@ -323,7 +402,7 @@ __device__ __forceinline__ void sparse_rows4(const SplitParams& p, const int32_t
 // their fp32 scale, rounded to bf16, into the chunk's 128-byte-swizzled row
 // `row` (shared memory).  Kept out of line: inlined into the softmax loop it
 // pushed that loop past the 96 registers a thread of this kernel may hold.
-__device__ __noinline__ void convert_unit(uint32_t row, int dq_r, int dq_u, uint4 codes, float sc) {
+static __device__ __noinline__ void convert_unit(uint32_t row, int dq_r, int dq_u, uint4 codes, float sc) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const uint32_t w0 = half ? codes.z : codes.x, w1 = half ? codes.w : codes.y;
@@ -337,7 +416,7 @@ __device__ __noinline__ void convert_unit(uint32_t row, int dq_r, int dq_u, uint
   }
 }
 
-template <KvMode kMode>
+template <KvMode kMode, bool kWindow = false>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_splitkv_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_kv,
@@ -355,12 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int part = blockIdx.x / p.n_hblk;
   const int hb = blockIdx.x % p.n_hblk;
   // The metadata must describe this call; otherwise nothing is read or written.
-  const bool meta_ok = meta_header_matches(p.meta, p.batch, p.s_q, p.num_parts, p.topk, p.causal);
+  // (A windowed call has no metadata.)
+  const bool meta_ok = kWindow || meta_header_matches(p.meta, p.batch, p.s_q, p.num_parts, p.topk, p.causal);
   // Schedule B (whole sequences) only when nearly balanced: a tile of this
   // kernel takes ~3-6 us, so the ~26 us that splitting costs is ~4 tiles.
   constexpr int kSplitPenalty = 4;
-  const int32_t* meta = meta_ok ? schedule_for(p.meta, kSplitPenalty) : p.meta;
-  if (blockIdx.x == 0 && threadIdx.x == 32 * kSoftmaxWarp0) {  // a softmax thread: nothing to do yet
+  const int32_t* meta = !kWindow && meta_ok ? schedule_for(p.meta, kSplitPenalty) : p.meta;
+  if (!kWindow && blockIdx.x == 0 && threadIdx.x == 32 * kSoftmaxWarp0) {  // a softmax thread: nothing to do yet
     // read by the combine after this grid: the schedule walked, or -1 when
     // the metadata was rejected (the combine then writes nothing), and
     // whether that schedule left anything to merge or fill
@@ -441,12 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int own0 = share ? hb : 0, own_step = share ? 2 : 1;
       const int n_own = (kChunks - 1) / own_step;
       const int n_req = kMode == KvMode::kPagedFp8V41 ? n_own : n_own + 1;  // + the RoPE chunk
-      PartCursor cur = walked_part_cursor(p.meta, meta, part);
-      int q, t0, t1, split;
+      Pieces<kWindow> pc(p, meta, part);
       uint32_t tile_ctr = 0, item_ctr = 0;
       bool ok = true;
       const uint64_t pol = l2_policy_evict_first();
-      while (ok && next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+      while (ok && pc.next()) {
+        const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
         ok = mbar_wait(smem_u32(&sm->q_empty), (item_ctr & 1) ^ 1, abort_flag, p.err);
         if (!ok) break;
         mbar_arrive_expect_tx(smem_u32(&sm->q_full), kQk * p.rows * 128);
@@ -454,14 +534,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kQk; ++c)
           tma_load_2d(q_base + c * kQChunkBytes, &tm_q, c * 64, q_row, smem_u32(&sm->q_full),
                       l2_policy_evict_last());
-        const int32_t keys = meta_seq(meta, p.num_parts, q)[kSKeys];
+        const int32_t keys = pc.keys();
         const int32_t* bt_row = bt_row_of(p, q);
-        check_seq_keys(p, q, keys);
+        if constexpr (!kWindow) check_seq_keys(p, q, keys);
         for (int t = t0; t < t1 && ok; ++t) {
           const uint32_t par = (tile_ctr & 1) ^ 1;
           int32_t blk[2];
           for (int h2 = 0; h2 < 2; ++h2) {
-            blk[h2] = page_of(p, bt_row, keys, 2 * t + h2);
+            blk[h2] = page_of(p, bt_row, keys, pc.page(2 * t + h2));
             if (blk[h2] < 0) {
               if (p.err) atomicOr(p.err, MLA_DEVERR_BAD_PAGE);
               blk[h2] = 0;  // read a valid page; the bad page's keys are wrong but finite
@@ -534,13 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Lane L gathers rows 4L..4L+3 of each 128-row tile with one tile::gather4
     // per column chunk; lane 0 owns the barriers.  Invalid slots (-1, out of
     // range, past topk) fetch pool row 0 and are masked by the softmax.
-    PartCursor cur = walked_part_cursor(p.meta, meta, part);
-    int q, t0, t1, split;
+    Pieces<kWindow> pc(p, meta, part);
     uint32_t tile_ctr = 0, item_ctr = 0;
     int32_t issued[kChunks];  // tile counter of each slot's latest gather, -1 = none
     for (int c = 0; c < kChunks; ++c) issued[c] = -1;
     bool ok = true;
-    while (ok && next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+    while (ok && pc.next()) {
+      const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
       if (lane == 0) {
         ok = mbar_wait(smem_u32(&sm->q_empty), (item_ctr & 1) ^ 1, abort_flag, p.err);
         if (ok) {
@@ -554,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       const int32_t* idx_row = p.indices + static_cast<int64_t>(q) * p.topk;
-      const int32_t n_slots = meta_seq(meta, p.num_parts, q)[kSKeys];  // topk or topk_length
+      const int32_t n_slots = pc.keys();  // topk or topk_length
       int32_t fallback = -2;  // first row the query names, found when a tile names none
       for (int t = t0; t < t1 && ok; ++t) {
         int32_t id[4], rid[4];
@@ -595,13 +675,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint64_t pol_kv = l2_policy_evict_first();
       const uint64_t pol_q = l2_policy_evict_last();
-      PartCursor cur = walked_part_cursor(p.meta, meta, part);
-      int q, t0, t1, split;
+      Pieces<kWindow> pc(p, meta, part);
       uint32_t tile_ctr = 0, item_ctr = 0;
       int32_t issued[kChunks];  // tile counter of each slot's latest load, -1 = none
       for (int c = 0; c < kChunks; ++c) issued[c] = -1;
       bool ok = true;
-      while (ok && next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+      while (ok && pc.next()) {
+        const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
         // Q rows of this block: 9 boxes of [rows x 64 columns]
         ok = mbar_wait(smem_u32(&sm->q_empty), (item_ctr & 1) ^ 1, abort_flag, p.err);
         if (!ok) break;
@@ -610,20 +690,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kChunks; ++c)
           tma_load_2d(q_base + c * kQChunkBytes, &tm_q, c * 64, q_row, smem_u32(&sm->q_full), pol_q);
         {  // the next piece's query rows into L2
-          PartCursor nc = cur;
-          int nq, nt0, nt1, ns;
-          if (next_piece(meta, p.num_parts, &nc, &nq, &nt0, &nt1, &ns))
-            prefetch_l2(p.q + (static_cast<int64_t>(nq) * p.h + hb * kRowsPerCta) * p.d_qk,
+          Pieces<kWindow> npc = pc;
+          if (npc.next())
+            prefetch_l2(p.q + (static_cast<int64_t>(npc.q) * p.h + hb * kRowsPerCta) * p.d_qk,
                         p.rows * p.d_qk * 2);
         }
-        const int32_t keys = meta_seq(meta, p.num_parts, q)[kSKeys];
+        const int32_t keys = pc.keys();
         const int32_t* bt_row = bt_row_of(p, q);
-        check_seq_keys(p, q, keys);
+        if constexpr (!kWindow) check_seq_keys(p, q, keys);
         for (int t = t0; t < t1 && ok; ++t) {
           int32_t y[2];
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
-            int32_t blk = page_of(p, bt_row, keys, 2 * t + h2);
+            int32_t blk = page_of(p, bt_row, keys, pc.page(2 * t + h2));
             if (blk < 0) {
               if (p.err) atomicOr(p.err, MLA_DEVERR_BAD_PAGE);
               blk = static_cast<int32_t>(p.num_pages);  // out of range: TMA fills zeros
@@ -659,12 +738,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ===================================================== MMA issuer
     if (lane == 0) {
-      PartCursor cur = walked_part_cursor(p.meta, meta, part);
-      int q, t0, t1, split;
+      Pieces<kWindow> pc(p, meta, part);
       uint32_t tile_ctr = 0, item_ctr = 0;
       bool ok = true;
       const uint32_t p_base = kv_base + 8 * kChunkBytes;
-      while (ok && next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
+      while (ok && pc.next()) {
+        const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
         ok = mbar_wait(smem_u32(&sm->q_full), item_ctr & 1, abort_flag, p.err);
         if (!ok) break;
         for (int t = t0; t < t1 && ok; ++t) {
@@ -749,13 +828,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* red_w = &sm->red_max[g][wq][0];
     float* bc_m = &sm->bcast[g][wq][0];
     float* bc_a = &sm->bcast2[g][wq][0];
-    PartCursor cur = walked_part_cursor(p.meta, meta, part);
-    int q, t0, t1, split;
+    Pieces<kWindow> pc(p, meta, part);
     uint32_t tile_ctr = 0, item_ctr = 0;
     bool ok = true;
-    while (ok && next_piece(meta, p.num_parts, &cur, &q, &t0, &t1, &split)) {
-      const int32_t* srec = meta_seq(meta, p.num_parts, q);
-      const int32_t keys = srec[kSKeys];
+    while (ok && pc.next()) {
+      const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
+      const int32_t keys = pc.keys();
       const int32_t* idx_row = (kMode == KvMode::kSparseBf16)
                                    ? p.indices + static_cast<int64_t>(q) * p.topk : nullptr;
       float m_true = NEG_INF;  // running max of row R*g + (lane & 15) (-inf: no key yet)
@@ -764,23 +842,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       float lsum = 0.f;        // sum p of row R*g + (lane & 15) over this warp's tokens
       float bsum = 0.f;        // sum bf16(p) of the same row
       for (int t = t0; t < t1; ++t) {
+        // windowed: whether the token sees the key of this thread's row
+        [[maybe_unused]] bool seen = true;
+        if constexpr (kWindow) seen = pc.sees(t, r);
         if constexpr (is_fp8(kMode)) {
           // ---- FP8: convert this tile's owned latent chunks in place.  Thread
           // = (token dq_r, 16-code unit dq_u); reads of the staging finish at
           // the named barrier before any bf16 write lands on it.  Every exit
           // is decided at a barrier, so all 16 warps leave together.
           const int own0 = share ? hb : 0, own_step = share ? 2 : 1;
+          [[maybe_unused]] bool seen_dq = true;  // windowed: the same for the key that it converts
+          if constexpr (kWindow) seen_dq = pc.sees(t, dq_r);
 #pragma unroll 1
           for (int c = own0; c < kChunks - 1; c += own_step) {
             if (lane == 0 && ok) ok = mbar_wait(smem_u32(&sm->raw_full[c]), tile_ctr & 1, abort_flag, p.err);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             const uint32_t slot = kv_base + c * kChunkBytes;
-            const uint4 codes = ld_shared_v4(slot + kRawCodeOff + dq_r * 64 + dq_u * 16);
+            uint4 codes = ld_shared_v4(slot + kRawCodeOff + dq_r * 64 + dq_u * 16);
             // the unit's scale: fp32 per 128 codes (656-byte cache), or e8m0
             // per 32 codes, 2^(byte - 127) (528-byte cache)
-            const float sc = kMode == KvMode::kPagedFp8V41
-                                 ? e8m0_to_f32(ld_shared_u8(slot + kRawScaleOff + dq_r * 16 + 2 * c + (dq_u >> 1)))
-                                 : ld_shared_f32(slot + kRawScaleOff + dq_r * 16 + (c >> 1) * 4);
+            float sc = kMode == KvMode::kPagedFp8V41
+                           ? e8m0_to_f32(ld_shared_u8(slot + kRawScaleOff + dq_r * 16 + 2 * c + (dq_u >> 1)))
+                           : ld_shared_f32(slot + kRawScaleOff + dq_r * 16 + (c >> 1) * 4);
+            if constexpr (kWindow) {  // keys not seen become zeros: their weight 0 times what is there could be NaN
+              if (!seen_dq) {
+                codes = make_uint4(0u, 0u, 0u, 0u);
+                sc = 0.f;
+              }
+            }
             ok = !named_barrier_or(kDequantBarrier, 128 * kSoftmaxGroups, !ok);
             if (!ok) break;
             convert_unit(slot + dq_r * 128, dq_r, dq_u, codes, sc);
@@ -799,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(t_s, x);
         tmem_wait_ld();
         const int tok = t * kTileTokens + r;
-        bool valid = tok < keys;
+        bool valid = kWindow ? seen : tok < keys;
         if (kMode == KvMode::kSparseBf16 && valid) {
           const int32_t id = idx_row[tok];
           valid = id >= 0 && static_cast<int64_t>(id) < p.s_kv;
@@ -884,6 +973,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t unit = static_cast<uint32_t>((2 * g + cu) ^ (r & 7));
           st_shared_v4(prow + unit * 16, pk[0], pk[1], pk[2], pk[3]);
         }
+        if constexpr (kWindow && !is_fp8(kMode)) {
+          // the rows of keys not seen become zeros before P.V reads them (Q.K^T
+          // has): their weight 0 times what is there could be NaN
+          if (!seen) {
+            const uint32_t row = kv_base + 2 * g * kChunkBytes + r * 128;
+#pragma unroll 1
+            for (uint32_t u = lane; u < lane + 8u; ++u) {
+              st_shared_v4(row + ((u & 7) << 4), 0u, 0u, 0u, 0u);
+              st_shared_v4(row + kChunkBytes + ((u & 7) << 4), 0u, 0u, 0u, 0u);
+            }
+          }
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -910,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const bool has = lsum > 0.f && bsum > 0.f;
-      const bool final_out = srec[kSNSplits] == 1;
+      const bool final_out = pc.whole();
       float inv_l = has ? 1.f / bsum : 0.f;
       const float lse_v = has ? (m_use + __log2f(lsum)) * 0.69314718055994531f : NEG_INF;
       // attention sink: applied here to a final row, by the combine to a split row
@@ -920,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       const volatile float* il = bc_a;  // 1 / sum of row i, read per store (broadcast)
       const int row0 = hb * kRowsPerCta + R * g;  // first head of this warpgroup
-      const int split_row = srec[kSSplitOff] + split;
+      const int64_t split_row = pc.split_row();
       const int b = q / p.s_q, j = q % p.s_q;
       // h is a multiple of 16, so a warpgroup's 16 rows are all heads or all padding
       if (row0 < p.h) {
@@ -940,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[i * kDv] = __float2bfloat16_rn(f != 0.f ? o[i] * f : 0.f);
             }
           } else {
-            float* dst = p.ws_o + (static_cast<int64_t>(split_row) * p.h + row0) * kDv + d;
+            float* dst = p.ws_o + (split_row * p.h + row0) * kDv + d;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
               const float f = il[i];
@@ -953,9 +1054,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (final_out)
           p.lse[(static_cast<int64_t>(b) * p.h + row0 + lane) * p.s_q + j] = lse_v;
         else
-          p.ws_lse[static_cast<int64_t>(split_row) * p.h + row0 + lane] = lse_v;
+          p.ws_lse[split_row * p.h + row0 + lane] = lse_v;
       }
       ++item_ctr;
+    }
+    if constexpr (kWindow) {  // tokens that see no key: out = 0, lse = -inf
+      Pieces<true> e(p, nullptr, part);
+      while (pc.passed_empty && e.template next<true>()) {
+        const int b = e.q / p.s_q, j = e.q % p.s_q, row0 = hb * kRowsPerCta;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(e.q) * p.h + row0) * kDv);
+        for (int i = threadIdx.x; i < p.rows * kDv / 8; i += 128 * kSoftmaxGroups) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (static_cast<int>(threadIdx.x) < p.rows)
+          p.lse[(static_cast<int64_t>(b) * p.h + row0 + threadIdx.x) * p.s_q + j] = NEG_INF;
+      }
     }
   }
 

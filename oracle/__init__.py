@@ -366,3 +366,88 @@ def sparse_prefill(q, kv_pool, indices, softmax_scale, tokens=None, attn_sink=No
     out, lse = sparse_decode(q[:, None], pool, idx, softmax_scale, rows=rows, attn_sink=attn_sink,
                              topk_length=tl)
     return out[:, 0], lse[:, :, 0]
+
+
+# ------------------------------------------------------------ a step's tokens
+#
+# Positions, norm and rotation of new tokens, and attention over a sliding
+# window with the first tokens visible, from their definitions.
+
+def token_positions(cache_seqlens, new_lens, s: int) -> np.ndarray:
+    """Position of token slot j of request b [b, s]: L_b - n_b + j; -1 for
+    padding (j >= n_b, or a negative position).  n_b = s without new_lens."""
+    L = np.asarray(cache_seqlens, dtype=np.int64)
+    n = np.full_like(L, s) if new_lens is None else np.clip(np.asarray(new_lens, dtype=np.int64), 0, s)
+    pos = (L - n)[:, None] + np.arange(s)[None]
+    ok = (np.arange(s)[None] < n[:, None]) & (pos >= 0) & (L[:, None] > 0)
+    return np.where(ok, pos, -1)
+
+
+def rms_norm(x: np.ndarray, weight, eps: float) -> np.ndarray:
+    """x / sqrt(mean(x^2) + eps) * weight over the last axis; x itself for eps = 0."""
+    if eps == 0.0:
+        return x
+    y = x / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps)
+    return y if weight is None else y * weight
+
+
+def rotate(x: np.ndarray, table_rows: np.ndarray, halves: bool) -> np.ndarray:
+    """x [..., 64] with pair i turned by the angle whose cosine and sine are
+    table_rows[..., i] and [..., 32 + i]: (a, b) -> (a c - b s, a s + b c).
+    Pair i is columns (2i, 2i + 1), or with ``halves`` (i, i + 32)."""
+    c, s = table_rows[..., :32], table_rows[..., 32:]
+    out = np.empty_like(x)
+    ia, ib = (np.arange(32), np.arange(32) + 32) if halves else (2 * np.arange(32), 2 * np.arange(32) + 1)
+    a, b = x[..., ia], x[..., ib]
+    out[..., ia] = a * c - b * s
+    out[..., ib] = a * s + b * c
+    return out
+
+
+def latent_rows(x, pos, table, halves, weight, eps, v41: bool) -> np.ndarray:
+    """Rows to be cached of the new tokens x [n, 576] (v41: [n, 512]) at
+    positions pos [n], before the format's rounding: the 512 latent columns
+    normalised, the last 64 columns rotated."""
+    y = x.copy()
+    y[:, :512] = rms_norm(x[:, :512], weight, eps)
+    if table is not None:
+        y[:, -64:] = rotate(y[:, -64:], table[pos], halves)
+    assert y.shape[1] == (512 if v41 else 576)
+    return y
+
+
+def query_rows(q, pos, table, halves, weight, eps) -> np.ndarray:
+    """Query heads q [n, h, d] at positions pos [n]: normalised over d, the last
+    64 columns rotated."""
+    y = rms_norm(q, weight, eps).copy()
+    if table is not None:
+        y[..., -64:] = rotate(y[..., -64:], table[pos][:, None], halves)
+    return y
+
+
+def window_keys(pos: int, window: int, sinks: int) -> np.ndarray:
+    """Positions that the token at ``pos`` sees: t <= pos with t > pos - window
+    or t < sinks."""
+    t = np.arange(pos + 1)
+    return t[(t > pos - window) | (t < sinks)]
+
+
+def window_decode(q, kv_rows, block_table, cache_seqlens, new_lens, softmax_scale, window, sinks, attn_sink=None):
+    """Windowed decode: q [b, s, h, d] float64, kv_rows [pages, 64, d] float64
+    keys (value: the first 512 columns).  Returns out [b, s, h, 512], lse
+    [b, h, s]."""
+    b, s, h, _ = q.shape
+    pos = token_positions(cache_seqlens, new_lens, s)
+    out = np.zeros((b, s, h, 512))
+    lse = np.full((b, h, s), -np.inf)
+    for bi in range(b):
+        for j in range(s):
+            if pos[bi, j] < 0:
+                continue
+            t = window_keys(int(pos[bi, j]), window, sinks)
+            keys = kv_rows[block_table[bi, t // 64], t % 64]
+            o, l = attend(q[bi, j], keys, softmax_scale)
+            if attn_sink is not None:
+                o = o * sink_factor(l, np.asarray(attn_sink, dtype=np.float64))[:, None]
+            out[bi, j], lse[bi, :, j] = o, l
+    return out, lse
