@@ -876,7 +876,12 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             if (!pc.span().full_tile(t)) {
               // The rows of keys not seen become zeros before P.V reads them:
               // their weight 0 times what is there could be NaN.  Thread r =
-              // key r of the tile.
+              // key r of the tile.  The previous tile's P.V is waited for first:
+              // without it the V barriers could still be a phase behind, and
+              // their parity would pass for this tile's (P(tc - 1) has come, so
+              // pv_done is at most that one phase behind; and neither can run
+              // ahead, since this tile's P.V waits for these rows).
+              if (ok && tc > 0) ok = mbar_wait(smem_u32(&bars->pv_done[(tc - 1) & 1]), ((tc - 1) >> 1) & 1, abort_flag, p.err);
               for (int hf = 0; hf < 2; ++hf)
                 if (ok) ok = mbar_wait(smem_u32(&bars->vfull[hf]), tc & 1, abort_flag, p.err);
               if (ok && !pc.sees(t, r)) {

@@ -112,6 +112,14 @@ def test_few_tokens_are_cut_into_pieces(fmt, h):
         check(c, *run(c, parts))
 
 
+@pytest.mark.parametrize("fmt,h", [(BF16, 128), (BF16, 64), (FP8_656, 64), (FP8_528, 128)])
+@pytest.mark.parametrize("parts", [1, 2, 5])
+def test_long_windows_one_after_the_other(fmt, h, parts):
+    """Every part walks several tokens with many tiles all of whose keys are
+    seen between the tiles at the window's ends, which have keys that are not."""
+    parity(fmt, [1100, 1900, 1333, 1500, 1920], 2, h, 1000, 70, seed=12, parts=parts)
+
+
 @pytest.mark.parametrize("fmt,h", [(BF16, 128), (BF16, 16), (FP8_656, 64), (FP8_528, 128)])
 def test_a_chunk_of_a_prompt(fmt, h):
     """Many tokens a request: every part walks several pieces."""
