@@ -524,12 +524,27 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               vm[k] = __ballot_sync(0xffffffffu, sid[k] >= 0 && static_cast<int64_t>(sid[k]) < p.s_kv);
           }
           if constexpr (kWindow) {
-            const WindowSpan span = pc.span();
+            // Scores of keys not seen become -inf in TMEM before the passes read
+            // them: only the tiles at the runs' ends have any.
+            const WindowSpan& span = pc.span;
+            if (ok && span.edge(t)) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t m = span.mask32(kPage * span.page(2 * t + (i >> 1)) + 32 * (i & 1));
+                if (m == ~0u) continue;
+                float v[32];
+                tmem_ld32(t_s + 32 * i, v);
+                tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) vm[k] = span.mask32(kPage * span.page(2 * t + (k >> 1)) + 32 * (k & 1));
+                for (int j = 0; j < 32; ++j) v[j] = (m >> j) & 1u ? v[j] : -INFINITY;
+                tmem_st32(t_s + 32 * i, v);
+              }
+              tmem_wait_st();
+            }
           }
           const int n_valid = keys - t * kTileTokens;  // >= 1; < 128 only on the last tile
-          const bool full = kSparse || (kWindow ? (vm[0] & vm[1] & vm[2] & vm[3]) == ~0u : n_valid >= kTileTokens);
+          const bool full = kSparse || kWindow || n_valid >= kTileTokens;
           // Row max of the raw scores (the scale is positive) over the tile's
           // keys.  The first tile of a piece takes its reference from it.  A
           // later tile needs it only when its probabilities against the current
@@ -543,11 +558,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               float v[32];
               tmem_ld32(t_s + 32 * i, v);
               tmem_wait_ld();
-              if (!kWindow && !full) {
+              if (!full) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 32 * i + j < n_valid ? v[j] : -INFINITY;
               }
-              if (kSparse || (kWindow && !full)) {
+              if constexpr (kSparse) {
                 const uint32_t w = vm[0] * (i == 0) | vm[1] * (i == 1) | vm[2] * (i == 2) | vm[3] * (i == 3);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = (w >> j) & 1u ? v[j] : -INFINITY;
@@ -582,11 +597,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               float v[32];
               tmem_ld32(t_s + 32 * i, v);
               tmem_wait_ld();
-              if (!kWindow && !full) {  // keys past the end: s = -inf, p = 2^-inf = 0
+              if (!full) {  // keys past the end: s = -inf, p = 2^-inf = 0
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 32 * i + j < n_valid ? v[j] : -INFINITY;
               }
-              if (kSparse || (kWindow && !full)) {  // slots without a pool row, keys not seen: p = 0
+              if constexpr (kSparse) {  // slots without a pool row: p = 0
                 const uint32_t w = vm[0] * (i == 0) | vm[1] * (i == 1) | vm[2] * (i == 2) | vm[3] * (i == 3);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = (w >> j) & 1u ? v[j] : -INFINITY;
@@ -813,7 +828,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             if (!ok) continue;
             tc_fence_after();
             if constexpr (kWindow) {
-              if (!pc.span().full_tile(t)) {  // the row warps have zeroed the rows of keys not seen
+              if (pc.span.edge(t)) {  // the row warps have zeroed the rows of keys not seen
                 ok = mbar_wait(smem_u32(&bars->v_clean), vc & 1, abort_flag, p.err);
                 ++vc;
                 if (!ok) continue;
@@ -873,7 +888,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           const uint32_t b = tc & 1;
           const uint32_t side = base + kPBuf0 + b * kPBufStride;
           if constexpr (kWindow) {
-            if (!pc.span().full_tile(t)) {
+            if (pc.span.edge(t)) {
               // The rows of keys not seen become zeros before P.V reads them:
               // their weight 0 times what is there could be NaN.  Thread r =
               // key r of the tile.  The previous tile's P.V is waited for first:

@@ -164,14 +164,13 @@ struct Pieces {
   __device__ __forceinline__ int64_t split_row() const { return static_cast<int64_t>(rec()[kSSplitOff] + split); }
 };
 
-// By the token's position and window.  Only the position is kept: what follows
-// from it is computed where it is used, since the softmax threads of the one-SM
-// kernel have no registers to hold it through a tile (they spilled).
+// By the token's position and window.
 template <>
 struct Pieces<true> {
   const SplitParams& p;
   int item, q, t0, t1;
   int32_t end;
+  WindowSpan span;
   bool passed_empty = false;  // a token that sees no key was passed over
   __device__ __forceinline__ Pieces(const SplitParams& prm, const int32_t*, int part) : p(prm), item(part) {}
   // Moves to the next piece; with kEmpty to the next token that sees no key
@@ -185,7 +184,8 @@ struct Pieces<true> {
       item += p.num_parts;
       const int b = q / p.s_q;
       end = window_end(p.cache_seqlens, p.new_lens, p.s_q, b, q - b * p.s_q);
-      const int tiles = window_span(end, p.window, p.sinks).tiles;
+      span = window_span(end, p.window, p.sinks);
+      const int tiles = span.tiles;
       if (kEmpty) {
         if (tiles == 0 && split == 0) return true;
         continue;
@@ -198,19 +198,22 @@ struct Pieces<true> {
     }
     return false;
   }
-  __device__ __forceinline__ WindowSpan span() const {
+  // Whether the token sees key i of tile t.  `span` is computed again from the
+  // position: the softmax threads of the one-SM kernel have no registers to
+  // hold it through a tile (they spilled).
+  __device__ __forceinline__ bool sees(int t, int i) const {
     int32_t e = end;
     asm volatile("" : "+r"(e));  // not to be computed ahead of its use
-    return window_span(e, p.window, p.sinks);
-  }
-  // whether the token sees key i of tile t
-  __device__ __forceinline__ bool sees(int t, int i) const {
-    const WindowSpan w = span();
+    const WindowSpan w = window_span(e, p.window, p.sinks);
     return w.sees(kPage * w.page(2 * t + (i >> 6)) + (i & 63));
   }
   __device__ __forceinline__ int32_t keys() const { return end; }
-  __device__ __forceinline__ int32_t page(int32_t e) const { return span().page(e); }
-  __device__ __forceinline__ bool whole() const { return window_pieces(span().tiles, p.n_split) == 1; }
+  __device__ __forceinline__ int32_t page(int32_t e) const { return span.page(e); }
+  __device__ __forceinline__ bool whole() const {
+    int32_t e = end;
+    asm volatile("" : "+r"(e));
+    return window_pieces(window_span(e, p.window, p.sinks).tiles, p.n_split) == 1;
+  }
   __device__ __forceinline__ int64_t split_row() const {  // q * n_split + split: the item itself
     return static_cast<int64_t>(item) - p.num_parts;
   }

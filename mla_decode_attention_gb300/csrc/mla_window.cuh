@@ -48,10 +48,11 @@ struct WindowSpan {
   MLA_HD bool sees(int32_t t) const { return t < end && (t < first || t >= lo); }
   // bit i: key x + i is seen
   MLA_HD uint32_t mask32(int32_t x) const { return low_bits(end - x) & (low_bits(first - x) | ~low_bits(lo - x)); }
-  // every key of tile t is seen
-  MLA_HD bool full_tile(int32_t t) const {
-    const int32_t x0 = kWindowPage * page(2 * t), x1 = kWindowPage * page(2 * t + 1);
-    return (mask32(x0) & mask32(x0 + 32) & mask32(x1) & mask32(x1 + 32)) == ~0u;
+  // Whether tile t may hold a key that is not seen: the tiles with the last of
+  // the first tokens, with the window's first key and with the last key.
+  MLA_HD bool edge(int32_t t) const {
+    return t == tiles - 1 || (lo > 0 && t == (lo / kWindowPage - skip) / 2) ||
+           (first > 0 && t == (first - 1) / kWindowPage / 2);
   }
   MLA_HD static uint32_t low_bits(int32_t n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
 };
