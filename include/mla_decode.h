@@ -459,9 +459,9 @@ int mla_query_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_st
 
 /*
  * Size in bytes of mla_window_decode's workspace for these arguments: 0, or
- * batch * s_q * pieces rows of fp32 partial outputs and LSEs when the call cuts
- * every token's keys into several pieces (few tokens, long windows).  One
- * workspace serves one call at a time.
+ * fp32 partial outputs and LSEs of two blocks of query rows per part when the
+ * call cuts tokens' keys into several pieces to spread them over the parts.  It
+ * does not grow with batch or s_q.  One workspace serves one call at a time.
  */
 int mla_window_workspace_size(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts,
                               size_t* bytes);
@@ -489,8 +489,8 @@ int mla_window_workspace_size(int batch, int s_q, int h_q, int window, int sinks
  *  attn_sink    optional [h_q] fp32, as for mla_sparse_decode.
  *  num_sm_parts from mla_num_sm_parts (any value >= 1 gives the same result up
  *               to rounding).
- *  workspace    mla_window_workspace_size() bytes, 16-byte aligned; NULL when
- *               that is 0.
+ *  workspace    workspace_bytes bytes, at least mla_window_workspace_size(),
+ *               16-byte aligned; NULL when that is 0.
  *  A token that sees no key (padding slots among them) gets out = 0,
  *  lse = -inf.
  */
@@ -498,8 +498,8 @@ int mla_window_decode(const void* q, const void* kv_cache, int kv_format, int64_
                       const int32_t* block_table, int64_t block_table_stride, int64_t max_pages,
                       const int32_t* cache_seqlens, const int32_t* new_lens, int batch, int s_q,
                       int h_q, int window, int sinks, float softmax_scale, const float* attn_sink,
-                      int num_sm_parts, void* workspace, void* out, float* lse, uint32_t* err,
-                      cudaStream_t stream);
+                      int num_sm_parts, void* workspace, size_t workspace_bytes, void* out,
+                      float* lse, uint32_t* err, cudaStream_t stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -8,7 +8,6 @@ first call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -68,7 +67,7 @@ _SIGS = {
                                  _vp, _i64, _i64, _vp, _vp]),
     "mla_window_workspace_size": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "mla_window_decode": (_i, [_vp, _vp, _i, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp,
-                               _i, _vp, _vp, _vp, _vp, _vp]),
+                               _i, _vp, _sz, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -336,53 +335,77 @@ def mla_combine(metadata: torch.Tensor, batch: int, s_q: int, h_q: int, num_sm_p
 
 
 # ---------------------------------------------------------------- a step's tokens
+#
+# These calls run in a few microseconds on the GPU, so what is done here before
+# the launch counts: plain comparisons, no tensor or stream objects.
 
-def _call_on(name, device, stream, *tensors):
-    """Checks that every given tensor is on ``device``; returns (function, raw
-    stream, context): the call is made with that device current, on its
-    current stream unless one is given."""
-    if device.type != "cuda":
-        raise ValueError(f"{name}: tensors must be on a CUDA device")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: tensors are on {t.device} and {device}")
+def _launch(name: str, device: int, args: tuple) -> None:
+    """Calls the library with ``device`` current."""
+    fn = getattr(_lib or lib(), name)
+    if device == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != 0:
+        raise MlaError(name, status)
+
+
+def _step_stream(stream, device: int) -> int:
+    """Raw handle of ``stream``, or of the device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    here = device.index == torch.cuda.current_device()
-    return getattr(_lib or lib(), name), raw, (contextlib.nullcontext() if here else torch.cuda.device(device))
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _vector(t, dtype, n, name):
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
+def _vector(t: torch.Tensor, dtype, n: int, name: str, device: int) -> int:
+    """Data pointer of a contiguous tensor of n values."""
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on device {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _block_table(block_table, batch):
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch \
-            or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
-        raise ValueError("block_table must be an int32 tensor [batch, max_pages] with unit column stride")
-    return block_table.stride(0), block_table.shape[1]
+def _step_device(t: torch.Tensor) -> int:
+    device = t.get_device()
+    if device < 0 or not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    return device
 
 
-def _cache(kv_cache, kv_format):
-    if kv_format not in _FORMATS:
+def _step_table(block_table: torch.Tensor, batch: int, device: int):
+    """(pointer, entries from row to row, entries of a row)"""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.get_device() != device:
+        raise ValueError(f"block_table must be an int32 tensor [batch, max_pages] on device {device}")
+    rows, width = block_table.shape
+    row, col = block_table.stride()
+    if rows != batch or (col != 1 and width > 1):
+        raise ValueError(f"block_table must have {batch} rows and unit column stride")
+    return block_table.data_ptr(), row, width
+
+
+def _step_cache(kv_cache: torch.Tensor, kv_format: int, device: int) -> int:
+    """Columns of a query and of a new row for this cache."""
+    form = _FORMATS.get(kv_format)
+    if form is None:
         raise ValueError(f"unknown kv_format {kv_format}")
-    d_qk, token_bytes = _FORMATS[kv_format]
-    want = torch.bfloat16 if kv_format == MLA_KV_BF16 else torch.uint8
-    if kv_cache.dtype != want or kv_cache.dim() != 3 or kv_cache.shape[1:] != (64, token_bytes or 576) \
-            or not kv_cache.is_contiguous():
-        raise ValueError(f"kv_format {kv_format} needs a contiguous {want} kv_cache [pages, 64, {token_bytes or 576}]")
-    return d_qk
+    width = form[1] or 576
+    if kv_cache.dtype != (torch.bfloat16 if kv_format == MLA_KV_BF16 else torch.uint8) or kv_cache.dim() != 3 \
+            or kv_cache.shape[1] != 64 or kv_cache.shape[2] != width or not kv_cache.is_contiguous() \
+            or kv_cache.get_device() != device:
+        raise ValueError(f"kv_format {kv_format} needs a contiguous kv_cache [pages, 64, {width}] of "
+                         f"{'bfloat16' if kv_format == MLA_KV_BF16 else 'uint8'} on device {device}")
+    return form[0]
 
 
-def _rope(rope_table):
+def _step_rope(rope_table: Optional[torch.Tensor], device: int):
+    """(pointer, rows)"""
     if rope_table is None:
-        return 0
+        return None, 0
     if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or rope_table.shape[1] != 64 \
-            or not rope_table.is_contiguous():
-        raise ValueError("rope_table must be a contiguous float32 tensor [positions, 64]")
-    return rope_table.shape[0]
+            or not rope_table.is_contiguous() or rope_table.get_device() != device:
+        raise ValueError(f"rope_table must be a contiguous float32 tensor [positions, 64] on device {device}")
+    return rope_table.data_ptr(), rope_table.shape[0]
 
 
 def mla_append_kv(kv_new: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, block_table: torch.Tensor,
@@ -396,30 +419,40 @@ def mla_append_kv(kv_new: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, 
     (rope_table [positions, 64] float32: 32 cosines, 32 sines).  cache_seqlens
     [b] int32 counts the new tokens; new_lens [b] int32 says how many of the
     s_new slots hold one (all of them when None)."""
-    dev = kv_cache.device
-    fn, raw, on = _call_on("mla_append_kv", dev, stream, kv_new, block_table, cache_seqlens, rope_table, norm_weight,
-                           new_lens, err)
-    d = _cache(kv_cache, kv_format)
-    if kv_new.dtype != torch.bfloat16 or kv_new.dim() != 3 or kv_new.shape[2] != d or kv_new.stride(2) != 1:
-        raise ValueError(f"kv_new must be a bfloat16 tensor [batch, s_new, {d}] with unit column stride")
+    dev = _step_device(kv_cache)
+    d = _step_cache(kv_cache, kv_format, dev)
+    if kv_new.dtype != torch.bfloat16 or kv_new.dim() != 3 or kv_new.shape[2] != d or kv_new.stride(2) != 1 \
+            or kv_new.get_device() != dev:
+        raise ValueError(f"kv_new must be a bfloat16 tensor [batch, s_new, {d}] with unit column stride on device {dev}")
     b, s, _ = kv_new.shape
-    token = kv_new.stride(1) if s > 1 else kv_new.stride(0) if b > 1 else max(d, kv_new.stride(1) & ~7)
-    if b > 1 and s > 1 and kv_new.stride(0) != s * token:
+    request, token, _ = kv_new.stride()
+    if s == 1:
+        token = request if b > 1 else d
+    elif b > 1 and request != s * token:
         raise ValueError("kv_new's token slots must be evenly spaced over the batch")
-    _vector(cache_seqlens, torch.int32, b, "cache_seqlens")
-    if new_lens is not None:
-        _vector(new_lens, torch.int32, b, "new_lens")
-    if norm_weight is not None:
-        _vector(norm_weight, torch.float32, 512, "norm_weight")
-    if err is not None:
-        _vector(err, torch.int32, 1, "err")
-    bt = _block_table(block_table, b)
-    rows = _rope(rope_table)
-    with on:
-        _check("mla_append_kv", fn(
-            kv_new.data_ptr(), token, cache_seqlens.data_ptr(), _ptr(new_lens), b, s, _ptr(rope_table), rows,
-            rope_style, _ptr(norm_weight), norm_eps, kv_cache.data_ptr(), kv_format, kv_cache.shape[0],
-            block_table.data_ptr(), *bt, _ptr(err), raw))
+    table, table_rows = _step_rope(rope_table, dev)
+    _launch("mla_append_kv", dev, (
+        kv_new.data_ptr(), token, _vector(cache_seqlens, torch.int32, b, "cache_seqlens", dev),
+        None if new_lens is None else _vector(new_lens, torch.int32, b, "new_lens", dev), b, s, table, table_rows,
+        rope_style, None if norm_weight is None else _vector(norm_weight, torch.float32, 512, "norm_weight", dev),
+        norm_eps, kv_cache.data_ptr(), kv_format, kv_cache.shape[0], *_step_table(block_table, b, dev),
+        None if err is None else _vector(err, torch.int32, 1, "err", dev), _step_stream(stream, dev)))
+
+
+def _head_strides(t: torch.Tensor, name: str):
+    """Strides of a [b, s, h, d] tensor: from token slot to token slot over the
+    whole batch, and from head to head."""
+    if t.dtype != torch.bfloat16 or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a bfloat16 tensor with unit column stride")
+    b, s, h, d = t.shape
+    request, token, head, _ = t.stride()
+    if h == 1:
+        head = d
+    if s == 1:
+        token = request if b > 1 else h * head
+    elif b > 1 and request != s * token:
+        raise ValueError(f"{name}'s token slots must be evenly spaced over the batch")
+    return token, head
 
 
 def mla_query_norm_rope(q: torch.Tensor, out: torch.Tensor, cache_seqlens: torch.Tensor,
@@ -432,35 +465,19 @@ def mla_query_norm_rope(q: torch.Tensor, out: torch.Tensor, cache_seqlens: torch
     tensor of the same shape that does not overlap it).  Rows of padding slots
     stay as they were in out.  cache_seqlens, new_lens, rope_table: as for
     mla_append_kv."""
-    dev = q.device
-    fn, raw, on = _call_on("mla_query_norm_rope", dev, stream, out, cache_seqlens, rope_table, norm_weight, new_lens,
-                           err)
-    if q.dim() != 4 or q.shape != out.shape:
-        raise ValueError("q and out must be [batch, s_q, h_q, d]")
+    dev = _step_device(q)
+    if q.dim() != 4 or q.shape != out.shape or out.get_device() != dev:
+        raise ValueError(f"q and out must be [batch, s_q, h_q, d] on device {dev}")
     b, s, h, d = q.shape
-    strides = []
-    for t, name in ((q, "q"), (out, "out")):
-        if t.dtype != torch.bfloat16 or t.stride(3) != 1:
-            raise ValueError(f"{name} must be a bfloat16 tensor with unit column stride")
-        sb, ss, sh, _ = t.stride()
-        head = sh if h > 1 else d
-        token = ss if s > 1 else sb if b > 1 else h * head
-        if b > 1 and s > 1 and sb != s * token:
-            raise ValueError(f"{name}'s token slots must be evenly spaced over the batch")
-        strides += [token, head]
-    _vector(cache_seqlens, torch.int32, b, "cache_seqlens")
-    if new_lens is not None:
-        _vector(new_lens, torch.int32, b, "new_lens")
-    if norm_weight is not None:
-        _vector(norm_weight, torch.float32, d, "norm_weight")
-    if err is not None:
-        _vector(err, torch.int32, 1, "err")
-    rows = _rope(rope_table)
-    with on:
-        _check("mla_query_norm_rope", fn(
-            q.data_ptr(), strides[0], strides[1], cache_seqlens.data_ptr(), _ptr(new_lens), b, s, h, d,
-            _ptr(rope_table), rows, rope_style, _ptr(norm_weight), norm_eps, out.data_ptr(), strides[2], strides[3],
-            _ptr(err), raw))
+    q_token, q_head = _head_strides(q, "q")
+    out_token, out_head = (q_token, q_head) if out is q else _head_strides(out, "out")
+    table, table_rows = _step_rope(rope_table, dev)
+    _launch("mla_query_norm_rope", dev, (
+        q.data_ptr(), q_token, q_head, _vector(cache_seqlens, torch.int32, b, "cache_seqlens", dev),
+        None if new_lens is None else _vector(new_lens, torch.int32, b, "new_lens", dev), b, s, h, d, table, table_rows,
+        rope_style, None if norm_weight is None else _vector(norm_weight, torch.float32, d, "norm_weight", dev),
+        norm_eps, out.data_ptr(), out_token, out_head, None if err is None else _vector(err, torch.int32, 1, "err", dev),
+        _step_stream(stream, dev)))
 
 
 def mla_window_workspace_size(batch: int, s_q: int, h_q: int, window: int, sinks: int, num_sm_parts: int) -> int:
@@ -482,35 +499,25 @@ def mla_window_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, b
     attn_sink: optional [h] float32.  cache_seqlens, new_lens: as for
     mla_append_kv.  workspace: mla_window_workspace_size() bytes (None when
     that is 0), float32."""
-    dev = q.device
-    fn, raw, on = _call_on("mla_window_decode", dev, stream, kv_cache, block_table, cache_seqlens, workspace, out, lse,
-                           err, attn_sink, new_lens)
-    d = _cache(kv_cache, kv_format)
+    dev = _step_device(q)
+    d = _step_cache(kv_cache, kv_format, dev)
     if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[3] != d or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous bfloat16 tensor [batch, s_q, h_q, {d}]")
     b, s, h, _ = q.shape
-    if out.dtype != torch.bfloat16 or out.shape != (b, s, h, 512) or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bfloat16 tensor [batch, s_q, h_q, 512]")
-    _vector(lse, torch.float32, b * h * s, "lse")
-    _vector(cache_seqlens, torch.int32, b, "cache_seqlens")
-    if new_lens is not None:
-        _vector(new_lens, torch.int32, b, "new_lens")
-    if attn_sink is not None:
-        _vector(attn_sink, torch.float32, h, "attn_sink")
-    if err is not None:
-        _vector(err, torch.int32, 1, "err")
-    need = _sz()
-    _check("mla_window_workspace_size",
-           _lib.mla_window_workspace_size(b, s, h, window, sinks, num_sm_parts, ctypes.byref(need)))
-    if need.value and (workspace is None or workspace.numel() * workspace.element_size() < need.value
-                       or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor of at least {need.value} bytes")
-    bt = _block_table(block_table, b)
-    with on:
-        _check("mla_window_decode", fn(
-            q.data_ptr(), kv_cache.data_ptr(), kv_format, kv_cache.shape[0], block_table.data_ptr(), *bt,
-            cache_seqlens.data_ptr(), _ptr(new_lens), b, s, h, window, sinks, softmax_scale, _ptr(attn_sink),
-            num_sm_parts, _ptr(workspace) if need.value else None, out.data_ptr(), lse.data_ptr(), _ptr(err), raw))
+    if workspace is None:
+        ws, ws_bytes = None, 0
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
+    _launch("mla_window_decode", dev, (
+        q.data_ptr(), kv_cache.data_ptr(), kv_format, kv_cache.shape[0], *_step_table(block_table, b, dev),
+        _vector(cache_seqlens, torch.int32, b, "cache_seqlens", dev),
+        None if new_lens is None else _vector(new_lens, torch.int32, b, "new_lens", dev), b, s, h, window, sinks,
+        softmax_scale, None if attn_sink is None else _vector(attn_sink, torch.float32, h, "attn_sink", dev),
+        num_sm_parts, ws, ws_bytes, _vector(out, torch.bfloat16, b * s * h * 512, "out", dev),
+        _vector(lse, torch.float32, b * h * s, "lse", dev), None if err is None else _vector(err, torch.int32, 1, "err", dev),
+        _step_stream(stream, dev)))
 
 
 def mla_check_wait_timeout(err: torch.Tensor, stream=None) -> None:

@@ -8,7 +8,6 @@
 #include "mla_internal.h"
 #include "mla_ptx.cuh"
 #include "mla_schedule.cuh"
-#include "mla_window.cuh"
 
 namespace mla {
 
@@ -19,11 +18,33 @@ constexpr int kCombineThreads = 32 * kCombineWarps;
 
 // Lane l of a warp owns output columns [16 l, 16 l + 16): each split row is read
 // as 2 KB contiguous per warp, and the bf16 row is written as 1 KB contiguous.
+// At most 80 registers per thread (three CTAs, 24 warps per SM): no spills.
 // attn_sink (optional, [h]): the merged row is scaled by e^lse / (e^lse + e^sink).
-__device__ __forceinline__ void merge_row(int q, int head, int lane, int64_t off, int n_splits, int h, int s_q,
-                                          const float* __restrict__ ws_o, const float* __restrict__ ws_lse,
-                                          const float* __restrict__ attn_sink, __nv_bfloat16* __restrict__ out,
-                                          float* __restrict__ lse) {
+__global__ void __launch_bounds__(kCombineThreads, 3) combine_kernel(
+    const int32_t* __restrict__ meta, int batch, int h, int s_q, int num_parts, const float* __restrict__ ws_o,
+    const float* __restrict__ ws_lse, const int32_t* __restrict__ ws_ctrl, const float* __restrict__ attn_sink,
+    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  const int q = blockIdx.x;
+  const int head = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  pdl_wait_primary();
+  // The split kernel recorded in the workspace which schedule it walked (-1
+  // when it rejected the metadata) and whether that schedule left anything to
+  // merge or fill; with nothing to do, no other word is read.
+  const int32_t walked = ws_ctrl[0];
+  if ((walked != 0 && walked != 1) || ws_ctrl[1] == 0) return;
+  // Metadata for another shape: the split kernel computed nothing (and set
+  // MLA_DEVERR_METADATA); write nothing either.  The topk and causal words
+  // do not change the layout, so any matching batch / s_q / parts passes.
+  if (meta[kHMagic] != kMetaMagic || meta[kHVersion] != kMetaVersion || meta[kHNSeq] != batch * s_q ||
+      meta[kHParts] != num_parts || meta[kHSq] != s_q || meta[kHBatch] != batch)
+    return;
+  const bool use_b = walked == 1 && schedule_b(meta)[kHMagic] == kMetaMagic;
+  const int32_t* sched = use_b ? schedule_b(meta) : meta;
+  const int32_t* s = meta_seq(sched, num_parts, q);
+  const int n_splits = s[kSNSplits];
+  const int off = s[kSSplitOff];
+  if (head >= h || n_splits == 1) return;  // single split: written by the split kernel
   const int b = q / s_q, j = q % s_q;
   __nv_bfloat16* orow = out + (static_cast<int64_t>(q) * h + head) * kDv + 16 * lane;
   float* lse_out = lse + (static_cast<int64_t>(b) * h + head) * s_q + j;
@@ -33,7 +54,7 @@ __device__ __forceinline__ void merge_row(int q, int head, int lane, int64_t off
     if (lane == 0) *lse_out = -INFINITY;
     return;
   }
-  const float4* src = reinterpret_cast<const float4*>(ws_o + (off * h + head) * kDv) + 4 * lane;
+  const float4* src = reinterpret_cast<const float4*>(ws_o + (static_cast<int64_t>(off) * h + head) * kDv) + 4 * lane;
   const int64_t split_stride = static_cast<int64_t>(h) * kDv / 4;  // in float4
   // split 0's row is requested before the weights are known; split i + 1's
   // while split i is accumulated
@@ -41,7 +62,7 @@ __device__ __forceinline__ void merge_row(int q, int head, int lane, int64_t off
 #pragma unroll
   for (int c = 0; c < 4; ++c) cur[c] = src[c];
   // merged lse = ref + ln sum_i exp(lse_i - ref), ref = max_i lse_i
-  const float* lrow = ws_lse + off * h + head;
+  const float* lrow = ws_lse + static_cast<int64_t>(off) * h + head;
   float mx = -INFINITY;
   for (int i = lane; i < n_splits; i += 32) mx = fmaxf(mx, lrow[static_cast<int64_t>(i) * h]);
 #pragma unroll
@@ -86,51 +107,6 @@ __device__ __forceinline__ void merge_row(int q, int head, int lane, int64_t off
   if (lane == 0) *lse_out = total_lse;
 }
 
-// At most 80 registers per thread (three CTAs, 24 warps per SM): no spills.
-__global__ void __launch_bounds__(kCombineThreads, 3) combine_kernel(
-    const int32_t* __restrict__ meta, int batch, int h, int s_q, int num_parts, const float* __restrict__ ws_o,
-    const float* __restrict__ ws_lse, const int32_t* __restrict__ ws_ctrl, const float* __restrict__ attn_sink,
-    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
-  const int q = blockIdx.x;
-  const int head = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  pdl_wait_primary();
-  // The split kernel recorded in the workspace which schedule it walked (-1
-  // when it rejected the metadata) and whether that schedule left anything to
-  // merge or fill; with nothing to do, no other word is read.
-  const int32_t walked = ws_ctrl[0];
-  if ((walked != 0 && walked != 1) || ws_ctrl[1] == 0) return;
-  // Metadata for another shape: the split kernel computed nothing (and set
-  // MLA_DEVERR_METADATA); write nothing either.  The topk and causal words
-  // do not change the layout, so any matching batch / s_q / parts passes.
-  if (meta[kHMagic] != kMetaMagic || meta[kHVersion] != kMetaVersion || meta[kHNSeq] != batch * s_q ||
-      meta[kHParts] != num_parts || meta[kHSq] != s_q || meta[kHBatch] != batch)
-    return;
-  const bool use_b = walked == 1 && schedule_b(meta)[kHMagic] == kMetaMagic;
-  const int32_t* sched = use_b ? schedule_b(meta) : meta;
-  const int32_t* s = meta_seq(sched, num_parts, q);
-  const int n_splits = s[kSNSplits];
-  const int off = s[kSSplitOff];
-  if (head >= h || n_splits == 1) return;  // single split: written by the split kernel
-  merge_row(q, head, lane, off, n_splits, h, s_q, ws_o, ws_lse, attn_sink, out, lse);
-}
-
-// Windowed attention: token q's pieces are rows q * n_split .. of the
-// workspace, as many as its position gives (mla_window.cuh).
-__global__ void __launch_bounds__(kCombineThreads, 3) window_combine_kernel(
-    const int32_t* __restrict__ seqlens, const int32_t* __restrict__ new_lens, int window, int sinks, int n_split,
-    int h, int s_q, const float* __restrict__ ws_o, const float* __restrict__ ws_lse,
-    const float* __restrict__ attn_sink, __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
-  const int q = blockIdx.x;
-  const int head = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  pdl_wait_primary();
-  const int tiles = window_span(window_end(seqlens, new_lens, s_q, q / s_q, q % s_q), window, sinks).tiles;
-  const int n_splits = window_pieces(tiles, n_split);
-  if (head >= h || n_splits <= 1) return;  // written by the split kernel
-  merge_row(q, head, lane, static_cast<int64_t>(q) * n_split, n_splits, h, s_q, ws_o, ws_lse, attn_sink, out, lse);
-}
-
 }  // namespace
 
 int launch_combine(const void* metadata, int batch, int s_q, int h_q, int num_sm_parts,
@@ -154,25 +130,6 @@ int launch_combine(const void* metadata, int batch, int s_q, int h_q, int num_sm
                                            batch, h_q, s_q, num_sm_parts, ws_o, ws_lse, ws_ctrl, attn_sink,
                                            static_cast<__nv_bfloat16*>(out), lse);
   return e == cudaSuccess ? MLA_OK : record_cuda_error("combine kernel launch", e);
-}
-
-int launch_window_combine(const int32_t* seqlens, const int32_t* new_lens, int batch, int s_q, int h_q, int window,
-                          int sinks, int n_split, const void* workspace, const float* attn_sink, void* out, float* lse,
-                          cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(batch) * s_q * n_split * h_q;
-  const float* ws_o = static_cast<const float*>(workspace);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(batch * s_q, (h_q + kCombineWarps - 1) / kCombineWarps, 1);
-  cfg.blockDim = dim3(kCombineThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, window_combine_kernel, seqlens, new_lens, window, sinks, n_split, h_q,
-                                           s_q, ws_o, ws_o + rows * kDv, attn_sink, static_cast<__nv_bfloat16*>(out), lse);
-  return e == cudaSuccess ? MLA_OK : record_cuda_error("window combine kernel launch", e);
 }
 
 }  // namespace mla

@@ -59,7 +59,7 @@ extern "C" int mla_decode_splitkv(const void* q, const void* kv_cache, int kv_fo
   prm.rows = rows;
   prm.scale_log2 = softmax_scale * 1.4426950408889634f;
   CacheMaps maps;
-  rc = make_cache_maps(&maps, prm, kv_cache, kv_format);
+  rc = make_cache_maps(&maps, prm, kv_cache, kv_format, h_q == pair::kRows);
   if (rc != MLA_OK) return rc;
   if (kv_format == MLA_KV_FP8_528)
     return launch_split<KvMode::kPagedFp8V41>(maps.q, maps.kv, prm, stream, &maps.codes, &maps.scales);

@@ -38,11 +38,6 @@ int launch_combine(const void* metadata, int batch, int s_q, int h_q, int num_sm
                    const void* workspace, const float* attn_sink, void* out, float* lse,
                    cudaStream_t stream, bool pdl);
 
-// The same for a windowed call cut into n_split pieces a token.
-int launch_window_combine(const int32_t* seqlens, const int32_t* new_lens, int batch, int s_q, int h_q, int window,
-                          int sinks, int n_split, const void* workspace, const float* attn_sink, void* out, float* lse,
-                          cudaStream_t stream);
-
 // Workspace partition: partial O [rows, h, 512] fp32, partial LSE [rows, h]
 // fp32, then kWorkspaceCtrlBytes of control words.  Control word 0 holds the
 // schedule the last split kernel on this workspace walked (0 = A, 1 = B, -1 =

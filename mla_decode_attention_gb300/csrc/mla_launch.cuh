@@ -154,7 +154,7 @@ template <bool kSparse, bool kWindow = false>
 int launch_pair(const CUtensorMap& tm_kv, const CUtensorMap& tm_qa, const CUtensorMap& tm_qb,
                 const SplitParams& prm, cudaStream_t stream) {
   CUtensorMap tm_ql, tm_qr;
-  const uint64_t q_rows = static_cast<uint64_t>(prm.batch) * prm.s_q * pair::kRows;
+  const uint64_t q_rows = static_cast<uint64_t>(prm.batch) * prm.s_q * prm.h;
   if (!make_q_latent_map(&tm_ql, prm.q, q_rows) || !make_rows_map(&tm_qr, prm.q, q_rows, kDqk * 2, pair::kRows))
     return record_error("cuTensorMapEncodeTiled failed for the query rows", MLA_ERR_CUDA);
   static int state = 0;  // 0 unset, 1 ok, -1 failed (per instantiation)
@@ -191,11 +191,12 @@ int launch_pair(const CUtensorMap& tm_kv, const CUtensorMap& tm_qa, const CUtens
 }
 
 // The tensor maps of a paged call (the cache at `kv_cache`, the query rows and
-// sizes of `prm`); the ones that its format and head count do not use are not set.
+// sizes of `prm`), the page groups of the two-SM kernel when `quads`; the ones
+// that the format does not use are not set.
 struct CacheMaps {
   CUtensorMap q, kv, codes, scales, quad4, quad3;
 };
-int make_cache_maps(CacheMaps* m, const SplitParams& prm, const void* kv_cache, int kv_format) {
+int make_cache_maps(CacheMaps* m, const SplitParams& prm, const void* kv_cache, int kv_format, bool quads) {
   const uint64_t tokens = static_cast<uint64_t>(prm.num_pages) * kPage;
   if (!make_rows_map(&m->q, prm.q, static_cast<uint64_t>(prm.batch) * prm.s_q * prm.h, prm.d_qk * 2, prm.rows, prm.d_qk))
     return record_error("cuTensorMapEncodeTiled failed for q", MLA_ERR_CUDA);
@@ -223,7 +224,7 @@ int make_cache_maps(CacheMaps* m, const SplitParams& prm, const void* kv_cache, 
   } else {
     if (!make_rows_map(&m->kv, kv_cache, tokens, kDqk * 2, kPage))
       return record_error("cuTensorMapEncodeTiled failed for kv_cache", MLA_ERR_CUDA);
-    if (prm.h == pair::kRows && (!make_quad_map(&m->quad4, kv_cache, static_cast<uint64_t>(prm.num_pages), 4) ||
+    if (quads && (!make_quad_map(&m->quad4, kv_cache, static_cast<uint64_t>(prm.num_pages), 4) ||
                                  !make_quad_map(&m->quad3, kv_cache, static_cast<uint64_t>(prm.num_pages), 3)))
       return record_error("cuTensorMapEncodeTiled failed for the kv_cache page groups", MLA_ERR_CUDA);
   }

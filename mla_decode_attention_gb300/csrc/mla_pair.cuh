@@ -234,8 +234,18 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
   // whole-sequence schedule is walked) start towards L2 before the wait: a
   // prefetch only warms L2, so rows a preceding kernel is still writing are
   // read for real after the wait all the same.
-  if (rank == 0 && threadIdx.x == 32 * 2 && part < p.batch * p.s_q * (kWindow ? p.n_split : 1))
-    prefetch_l2(p.q + static_cast<int64_t>(kWindow ? part / p.n_split : part) * kRows * kDqk, kRows * kDqk * 2);
+  if constexpr (kWindow) {
+    if (rank == 0 && threadIdx.x == 32 * 2) {
+      const WindowPlan& w = p.plan;
+      const int item = part % w.lanes + w.lanes * static_cast<int>(window_first_item(w, part / w.lanes));
+      const int j0 = item % w.chunks * w.group;
+      if (item < w.items)
+        prefetch_l2(p.q + (static_cast<int64_t>(item / w.chunks) * p.s_q + j0) * p.h * kDqk,
+                    min(w.group, p.s_q - j0) * p.h * kDqk * 2);
+    }
+  } else if (rank == 0 && threadIdx.x == 32 * 2 && part < p.batch * p.s_q) {
+    prefetch_l2(p.q + static_cast<int64_t>(part) * kRows * kDqk, kRows * kDqk * 2);
+  }
   pdl_wait_primary();
   pdl_launch_dependents();  // the combine may launch now; it waits for this grid to finish
   // Schedule B (whole sequences) is walked when it is at most kSplitPenalty
@@ -287,8 +297,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           for (int i = 0; i < 4; ++i) {
             const uint32_t bar = smem_u32(&bars->q_box[i]);
             mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 0 ? kChunk : 0));
-            if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * kRows, bar, pol);
-            tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * kRows, 2 * i, bar, pol);
+            if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * p.h, bar, pol);
+            tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * p.h, 2 * i, bar, pol);
           }
           q_issued = true;
         };
@@ -388,8 +398,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             for (int i = 0; i < 4 && ok; ++i) {
               const uint32_t bar = smem_u32(&bars->q_tma);
               mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 0 ? kChunk : 0));
-              if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, q * kRows, bar, qpol);
-              tma_load_3d(base + kStage, &tm_ql, 0, q * kRows, 2 * i, bar, qpol);
+              if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, q * p.h, bar, qpol);
+              tma_load_3d(base + kStage, &tm_ql, 0, q * p.h, 2 * i, bar, qpol);
               q_pending = true;
               ok = mbar_wait(bar, qtma_n & 1, abort_flag, p.err);
               if (!ok) break;
@@ -499,9 +509,15 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         if (r == 0) {
           Pieces<kWindow> npc = pc;
           if (npc.next())
-            prefetch_l2(p.q + static_cast<int64_t>(npc.q) * kRows * kDqk, kRows * kDqk * 2);
+            prefetch_l2(p.q + static_cast<int64_t>(npc.q) * p.h * kDqk, npc.rows() * kDqk * 2);
         }
         float m_use = 0.f, lsum = 0.f, bsum = 0.f;
+        [[maybe_unused]] int32_t end = 0;     // windowed: of row r's token, 0 for padding
+        [[maybe_unused]] bool blind = false;  // windowed: row r has seen no key yet
+        if constexpr (kWindow) {
+          end = pc.end_of_row(r);
+          blind = end > 0;
+        }
         for (int t = t0; t < t1; ++t, ++tc) {
           const uint32_t sb = tc & 1;
           const uint32_t t_s = tmem + lane_off + kSCol + 128 * sb;
@@ -526,13 +542,12 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           if constexpr (kWindow) {
             // Scores of keys not seen become -inf in TMEM before the passes read
             // them: only the tiles at the runs' ends have any.
-            const WindowSpan& span = pc.span;
-            if (ok && span.edge(t)) {
+            if (ok && pc.span.edge(t)) {
               tc_fence_after();
 #pragma unroll 1
               for (int i = 0; i < 4; ++i) {
-                const uint32_t m = span.mask32(kPage * span.page(2 * t + (i >> 1)) + 32 * (i & 1));
-                if (m == ~0u) continue;
+                const uint32_t m = window_mask32(end, p.window, p.sinks, pc.key_at(t, 32 * i));
+                if (!__any_sync(0xffffffffu, m != ~0u)) continue;
                 float v[32];
                 tmem_ld32(t_s + 32 * i, v);
                 tmem_wait_ld();
@@ -573,10 +588,15 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             return u * sc;
           };
           float alpha = 1.f;
-          if (ok && t == t0) {
+          if (ok && (kWindow ? t == t0 || __any_sync(0xffffffffu, blind) : t == t0)) {
             tc_fence_after();
             const float u = row_max();
-            m_use = u == -INFINITY ? 0.f : u;
+            if constexpr (kWindow) {
+              if (t == t0 || blind) m_use = u == -INFINITY ? 0.f : u;
+              blind = blind && u == -INFINITY;
+            } else {
+              m_use = u == -INFINITY ? 0.f : u;
+            }
           }
           // p = 2^(s * scale - m) -> bf16 P row r in the staging buffer (two
           // 64-token chunks, 128-byte swizzle), and the two sums
@@ -629,9 +649,9 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
                              pk[4 * uu + 2], pk[4 * uu + 3]);
             }
             bool move = false;
-            if (__any_sync(0xffffffffu, t != t0 && !(ls + ls2 <= kMoveSum))) {
+            if (__any_sync(0xffffffffu, t != t0 && !(ls + ls2 <= kMoveSum) && (!kWindow || end > 0))) {
               const float u = row_max();
-              if (u > m_use + kRescaleLog2) {  // move the reference; the warp redoes the pass
+              if (u > m_use + kRescaleLog2 && (!kWindow || end > 0)) {  // move the reference; the warp redoes the pass
                 const float a_new = fast_exp2(m_use - u);
                 alpha *= a_new;
                 m_use = u;
@@ -651,11 +671,12 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           st_shared_f32(stage + kSideAlpha + 4 * r, alpha);
           if (t == t1 - 1) {
             float inv_l = bsum > 0.f ? 1.f / bsum : 0.f;
+            if (kWindow && end == 0) inv_l = 0.f;
             // attention sink: applied with 1/l to a final row, by the combine to a split row
             if ((kSparse || kWindow) && p.attn_sink && pc.whole()) {
               const float lse_t = (lsum > 0.f && bsum > 0.f) ? (m_use + __log2f(lsum)) * 0.69314718055994531f
                                                              : -INFINITY;
-              inv_l *= attn_sink_factor(lse_t, p.attn_sink[r]);
+              if (!kWindow || end > 0) inv_l *= attn_sink_factor(lse_t, p.attn_sink[kWindow ? r % p.h : r]);
             }
             st_shared_f32(stage + kSideInvL + 4 * r, inv_l);
           }
@@ -678,12 +699,17 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           }
         }
         // LSE of row r for this piece
-        const float lse_v = (lsum > 0.f && bsum > 0.f) ? (m_use + __log2f(lsum)) * 0.69314718055994531f
-                                                       : -INFINITY;
+        const float lse_v = (lsum > 0.f && bsum > 0.f && (!kWindow || end > 0))
+                                ? (m_use + __log2f(lsum)) * 0.69314718055994531f : -INFINITY;
         if (ok) {
           if (pc.whole()) {
-            const int b = q / p.s_q, j = q % p.s_q;
-            p.lse[(static_cast<int64_t>(b) * kRows + r) * p.s_q + j] = lse_v;
+            if constexpr (kWindow) {
+              if (r < pc.rows())
+                p.lse[(static_cast<int64_t>(pc.b()) * p.h + r % p.h) * p.s_q + pc.j0() + r / p.h] = lse_v;
+            } else {
+              const int b = q / p.s_q, j = q % p.s_q;
+              p.lse[(static_cast<int64_t>(b) * kRows + r) * p.s_q + j] = lse_v;
+            }
           } else {
             p.ws_lse[pc.split_row() * kRows + r] = lse_v;
           }
@@ -899,7 +925,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               if (ok && tc > 0) ok = mbar_wait(smem_u32(&bars->pv_done[(tc - 1) & 1]), ((tc - 1) >> 1) & 1, abort_flag, p.err);
               for (int hf = 0; hf < 2; ++hf)
                 if (ok) ok = mbar_wait(smem_u32(&bars->vfull[hf]), tc & 1, abort_flag, p.err);
-              if (ok && !pc.sees(t, r)) {
+              if (ok && !pc.any_sees(pc.key_at(t, r))) {
                 const uint32_t row = base + (r >> 6) * kHalfPage + ((r & 63) >> 3) * 4096 + (r & 7) * 128;
 #pragma unroll 1
                 for (int u = 0; u < 64; ++u)
@@ -966,8 +992,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           // goes through a swizzled 4 KB staging area so that every global
           // store instruction writes four whole 128-byte row segments.
           const bool final_out = pc.whole();
-          const int64_t row0 = (final_out ? static_cast<int64_t>(q) : pc.split_row()) *
-                                   kRows + 32 * (warp - 4);
+          const int64_t row0 = (kWindow && final_out ? static_cast<int64_t>(q) * p.h
+                                                     : (final_out ? static_cast<int64_t>(q) : pc.split_row()) * kRows) +
+                               32 * (warp - 4);
+          // windowed: the item's query rows among this warp's
+          [[maybe_unused]] const int n_rows = kWindow ? pc.rows() - 32 * (warp - 4) : 32;
           const uint32_t stg = base + kEpi + (warp - 4) * 4096;
           const int rr0 = lane >> 3, uu = lane & 7;
           if (final_out) {
@@ -994,7 +1023,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               for (int j = 0; j < 8; ++j) {
                 const int rr = 4 * j + rr0;
                 const uint4 x = ld_shared_v4(stg + rr * 128 + ((uu ^ (rr & 7)) << 4));
-                *reinterpret_cast<uint4*>(p.out + (row0 + rr) * kDv + 64 * blk + 8 * uu) = x;
+                if (!kWindow || rr < n_rows)
+                  *reinterpret_cast<uint4*>(p.out + (row0 + rr) * kDv + 64 * blk + 8 * uu) = x;
               }
               __syncwarp();
             }
@@ -1032,10 +1062,10 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       if constexpr (kWindow) {  // tokens that see no key: out = 0, lse = -inf
         Pieces<true> e(p, nullptr, part);
         while (pc.passed_empty && e.template next<true>()) {
-          const int b = e.q / p.s_q, j = e.q % p.s_q;
-          uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(e.q) * kRows * kDv);
-          for (int i = r; i < kRows * kDv / 8; i += kRowThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-          p.lse[(static_cast<int64_t>(b) * kRows + r) * p.s_q + j] = -INFINITY;
+          uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(e.q) * p.h * kDv);
+          for (int i = r; i < e.rows() * kDv / 8; i += kRowThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < e.rows())
+            p.lse[(static_cast<int64_t>(e.b()) * p.h + r % p.h) * p.s_q + e.j0() + r / p.h] = -INFINITY;
         }
       }
     } else if (warp == 3 && !kSparse) {

@@ -140,7 +140,7 @@ struct SplitParams {
   // windowed attention (no metadata): see mla_window.cuh
   const int32_t* new_lens; // optional [batch]
   int window, sinks;
-  int n_split;             // pieces that each query token's tiles are cut into
+  WindowPlan plan;
 };
 
 // The pieces that part `part` walks: next() moves to a piece (tiles [t0, t1) of
@@ -162,61 +162,78 @@ struct Pieces {
   __device__ __forceinline__ int32_t page(int32_t e) const { return e; }
   __device__ __forceinline__ bool whole() const { return rec()[kSNSplits] == 1; }
   __device__ __forceinline__ int64_t split_row() const { return static_cast<int64_t>(rec()[kSSplitOff] + split); }
+  __device__ __forceinline__ int rows() const { return p.h; }              // query rows of q
+  __device__ __forceinline__ int rows_from(int) const { return p.rows; }  // and of a CTA's block
 };
 
-// By the token's position and window.
+// By the tokens' positions and the window (mla_window.cuh): q is the first query
+// token of the item (a token of all requests' slots in turn).
 template <>
 struct Pieces<true> {
   const SplitParams& p;
-  int item, q, t0, t1;
-  int32_t end;
+  int part, m;                // the next item's number on the part's cost line
+  int q, t0, t1;
+  int32_t row;                // block of the split workspace, -1 for an item that is not cut
+  WindowEnds ends;
   WindowSpan span;
-  bool passed_empty = false;  // a token that sees no key was passed over
-  __device__ __forceinline__ Pieces(const SplitParams& prm, const int32_t*, int part) : p(prm), item(part) {}
-  // Moves to the next piece; with kEmpty to the next token that sees no key
+  bool passed_empty = false;  // an item that sees no key, and is this part's to write, was passed over
+  __device__ __forceinline__ Pieces(const SplitParams& prm, const int32_t*, int part_) : p(prm), part(part_) {
+    m = static_cast<int>(window_first_item(p.plan, part / p.plan.lanes));
+  }
+  // Moves to the next piece; with kEmpty to the next item that sees no key
   // instead (these have no piece).
   template <bool kEmpty = false>
   __device__ __forceinline__ bool next() {
-    const int items = p.batch * p.s_q * p.n_split;
-    while (item < items) {
-      q = item / p.n_split;
-      const int split = item - q * p.n_split;
-      item += p.num_parts;
-      const int b = q / p.s_q;
-      end = window_end(p.cache_seqlens, p.new_lens, p.s_q, b, q - b * p.s_q);
-      span = window_span(end, p.window, p.sinks);
-      const int tiles = span.tiles;
-      if (kEmpty) {
-        if (tiles == 0 && split == 0) return true;
-        continue;
+    const WindowPlan& w = p.plan;
+    const int lane = part % w.lanes, pl = part / w.lanes;
+    for (;;) {
+      const int item = lane + w.lanes * m;
+      if (item >= w.items || m * static_cast<int64_t>(w.tiles + w.fixed) >= (pl + 1) * w.per) return false;
+      const int b = item / w.chunks, j0 = (item - b * w.chunks) * w.group;
+      ends = window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group);
+      span = window_span(ends, p.window, p.sinks);
+      const WindowPiece piece = window_piece(w, m, pl, span.tiles);
+      row = piece.cut ? window_row(w, m, pl, lane) : -1;
+      ++m;
+      q = b * p.s_q + j0;
+      if (span.tiles == 0 && piece.owner) {
+        if (kEmpty) return true;
+        passed_empty = true;
       }
-      passed_empty |= tiles == 0;
-      const int pieces = window_pieces(tiles, p.n_split);
-      if (split >= pieces) continue;
-      window_piece(tiles, pieces, split, &t0, &t1);
-      return true;
+      t0 = piece.t0; t1 = piece.t1;
+      if (!kEmpty && t0 < t1) return true;
     }
-    return false;
   }
-  // Whether the token sees key i of tile t.  `span` is computed again from the
-  // position: the softmax threads of the one-SM kernel have no registers to
-  // hold it through a tile (they spilled).
-  __device__ __forceinline__ bool sees(int t, int i) const {
-    int32_t e = end;
-    asm volatile("" : "+r"(e));  // not to be computed ahead of its use
-    const WindowSpan w = window_span(e, p.window, p.sinks);
-    return w.sees(kPage * w.page(2 * t + (i >> 6)) + (i & 63));
+  // The end of the token of query row r of the item (0: padding, or a row past
+  // the item's tokens), and whether a token with this end sees key i of tile t.
+  // `span` is computed again: the softmax threads of the one-SM kernel have no
+  // registers to hold it through a tile (they spilled).
+  __device__ __forceinline__ int32_t end_of_row(int r) const {
+    const int j = r / p.h;
+    return r < rows() ? window_end(p.cache_seqlens, p.new_lens, p.s_q, b(), j0() + j) : 0;
   }
-  __device__ __forceinline__ int32_t keys() const { return end; }
+  __device__ __forceinline__ int32_t position(int t, int i) const {
+    WindowEnds e = ends;
+    asm volatile("" : "+r"(e.least), "+r"(e.most));  // not to be computed ahead of its use
+    return kPage * window_span(e, p.window, p.sinks).page(2 * t + (i >> 6)) + (i & 63);
+  }
+  // The same from `span`: position of key i of tile t.
+  __device__ __forceinline__ int32_t key_at(int t, int i) const { return kPage * span.page(2 * t + (i >> 6)) + (i & 63); }
+  // Whether any of the item's tokens sees the key at position x.
+  __device__ __forceinline__ bool any_sees(int32_t x) const {
+    return x < ends.most && (x < p.sinks || x >= window_lo(ends.least, p.window));
+  }
+  // query rows of the item that belong to token slots of its request
+  __device__ __forceinline__ int rows() const {
+    return min(p.plan.group, p.s_q - j0()) * p.h;
+  }
+  __device__ __forceinline__ int b() const { return q / p.s_q; }   // request
+  __device__ __forceinline__ int j0() const { return q % p.s_q; }  // and slot of the item's first token
+  __device__ __forceinline__ int rows_from(int row) const { return min(rows() - row, p.rows); }
+  __device__ __forceinline__ int32_t keys() const { return ends.most; }
   __device__ __forceinline__ int32_t page(int32_t e) const { return span.page(e); }
-  __device__ __forceinline__ bool whole() const {
-    int32_t e = end;
-    asm volatile("" : "+r"(e));
-    return window_pieces(window_span(e, p.window, p.sinks).tiles, p.n_split) == 1;
-  }
-  __device__ __forceinline__ int64_t split_row() const {  // q * n_split + split: the item itself
-    return static_cast<int64_t>(item) - p.num_parts;
-  }
+  __device__ __forceinline__ bool whole() const { return row < 0; }
+  __device__ __forceinline__ int64_t split_row() const { return row; }
 };
 
 struct SmemSmall {
@@ -696,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Pieces<kWindow> npc = pc;
           if (npc.next())
             prefetch_l2(p.q + (static_cast<int64_t>(npc.q) * p.h + hb * kRowsPerCta) * p.d_qk,
-                        p.rows * p.d_qk * 2);
+                        npc.rows_from(hb * kRowsPerCta) * p.d_qk * 2);
         }
         const int32_t keys = pc.keys();
         const int32_t* bt_row = bt_row_of(p, q);
@@ -839,15 +856,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t keys = pc.keys();
       const int32_t* idx_row = (kMode == KvMode::kSparseBf16)
                                    ? p.indices + static_cast<int64_t>(q) * p.topk : nullptr;
+      [[maybe_unused]] int32_t end = 0;  // windowed: of the token of this warpgroup's rows (h is a multiple of 16)
+      if constexpr (kWindow) end = pc.end_of_row(hb * kRowsPerCta + R * g);
       float m_true = NEG_INF;  // running max of row R*g + (lane & 15) (-inf: no key yet)
       float m_use = 0.f;       // reference the probabilities are taken against
       float m_low = NEG_INF;   // smallest m_true over the warpgroup's rows
       float lsum = 0.f;        // sum p of row R*g + (lane & 15) over this warp's tokens
       float bsum = 0.f;        // sum bf16(p) of the same row
       for (int t = t0; t < t1; ++t) {
-        // windowed: whether the token sees the key of this thread's row
-        [[maybe_unused]] bool seen = true;
-        if constexpr (kWindow) seen = pc.sees(t, r);
+        // windowed: whether this warpgroup's token, or any of the item's, sees
+        // the key of this thread's row
+        [[maybe_unused]] bool seen = true, seen_any = true;
+        if constexpr (kWindow) {
+          const int32_t x = pc.position(t, r);
+          seen = window_sees(end, p.window, p.sinks, x);
+          seen_any = pc.any_sees(x);
+        }
         if constexpr (is_fp8(kMode)) {
           // ---- FP8: convert this tile's owned latent chunks in place.  Thread
           // = (token dq_r, 16-code unit dq_u); reads of the staging finish at
@@ -855,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // is decided at a barrier, so all 16 warps leave together.
           const int own0 = share ? hb : 0, own_step = share ? 2 : 1;
           [[maybe_unused]] bool seen_dq = true;  // windowed: the same for the key that it converts
-          if constexpr (kWindow) seen_dq = pc.sees(t, dq_r);
+          if constexpr (kWindow) seen_dq = pc.any_sees(pc.position(t, dq_r));
 #pragma unroll 1
           for (int c = own0; c < kChunks - 1; c += own_step) {
             if (lane == 0 && ok) ok = mbar_wait(smem_u32(&sm->raw_full[c]), tile_ctr & 1, abort_flag, p.err);
@@ -922,7 +946,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  fmaxf(sm->red_max[g][2][row], sm->red_max[g][3][row]));
           const float m_new = fmaxf(m_true, mt);
           const float m_use_new = (m_new == NEG_INF) ? 0.f : m_new;
-          const float alpha = (t == t0) ? 1.f : fast_exp2(m_use - m_use_new);
+          // (windowed: also for a row that has seen no key yet)
+          const float alpha = (t == t0 || (kWindow && m_true == NEG_INF)) ? 1.f : fast_exp2(m_use - m_use_new);
           m_true = m_new;
           m_use = m_use_new;
           m_low = warp_min_f32(m_true);
@@ -979,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kWindow && !is_fp8(kMode)) {
           // the rows of keys not seen become zeros before P.V reads them (Q.K^T
           // has): their weight 0 times what is there could be NaN
-          if (!seen) {
+          if (!seen_any) {
             const uint32_t row = kv_base + 2 * g * kChunkBytes + r * 128;
 #pragma unroll 1
             for (uint32_t u = lane; u < lane + 8u; ++u) {
@@ -1018,16 +1043,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       float inv_l = has ? 1.f / bsum : 0.f;
       const float lse_v = has ? (m_use + __log2f(lsum)) * 0.69314718055994531f : NEG_INF;
       // attention sink: applied here to a final row, by the combine to a split row
-      if (p.attn_sink && final_out && hb * kRowsPerCta + R * g + row < p.h)
-        inv_l *= attn_sink_factor(lse_v, p.attn_sink[hb * kRowsPerCta + R * g + row]);
+      const int row0 = hb * kRowsPerCta + R * g;        // first query row of this warpgroup
+      const int head0 = kWindow ? row0 % p.h : row0;    // and its head
+      const int n_rows = kWindow ? pc.rows() : p.h;
+      if (p.attn_sink && final_out && row0 + row < n_rows)
+        inv_l *= attn_sink_factor(lse_v, p.attn_sink[head0 + row]);
       if (lane < R) bc_a[lane] = inv_l;
       __syncwarp();
       const volatile float* il = bc_a;  // 1 / sum of row i, read per store (broadcast)
-      const int row0 = hb * kRowsPerCta + R * g;  // first head of this warpgroup
-      const int64_t split_row = pc.split_row();
-      const int b = q / p.s_q, j = q % p.s_q;
+      const int64_t ws_row0 = pc.split_row() * (kWindow ? p.n_hblk * kRowsPerCta : p.h) + row0;
+      const int b = q / p.s_q, j = q % p.s_q + (kWindow ? row0 / p.h : 0);
       // h is a multiple of 16, so a warpgroup's 16 rows are all heads or all padding
-      if (row0 < p.h) {
+      if (row0 < n_rows) {
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
           float o[R];  // O^T rows d of block m, columns = this warpgroup's 16 query rows
@@ -1044,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[i * kDv] = __float2bfloat16_rn(f != 0.f ? o[i] * f : 0.f);
             }
           } else {
-            float* dst = p.ws_o + (split_row * p.h + row0) * kDv + d;
+            float* dst = p.ws_o + ws_row0 * kDv + d;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
               const float f = il[i];
@@ -1053,22 +1080,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (wq == 0 && lane < R && row0 + lane < p.h) {
+      if (wq == 0 && lane < R && row0 + lane < n_rows) {
         if (final_out)
-          p.lse[(static_cast<int64_t>(b) * p.h + row0 + lane) * p.s_q + j] = lse_v;
+          p.lse[(static_cast<int64_t>(b) * p.h + head0 + lane) * p.s_q + j] = lse_v;
         else
-          p.ws_lse[split_row * p.h + row0 + lane] = lse_v;
+          p.ws_lse[ws_row0 + lane] = lse_v;
       }
       ++item_ctr;
     }
     if constexpr (kWindow) {  // tokens that see no key: out = 0, lse = -inf
       Pieces<true> e(p, nullptr, part);
       while (pc.passed_empty && e.template next<true>()) {
-        const int b = e.q / p.s_q, j = e.q % p.s_q, row0 = hb * kRowsPerCta;
+        const int row0 = hb * kRowsPerCta, n_rows = min(e.rows() - row0, kRowsPerCta);
         uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(e.q) * p.h + row0) * kDv);
-        for (int i = threadIdx.x; i < p.rows * kDv / 8; i += 128 * kSoftmaxGroups) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (static_cast<int>(threadIdx.x) < p.rows)
-          p.lse[(static_cast<int64_t>(b) * p.h + row0 + threadIdx.x) * p.s_q + j] = NEG_INF;
+        for (int i = threadIdx.x; i < n_rows * kDv / 8; i += 128 * kSoftmaxGroups) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        const int r = row0 + threadIdx.x;
+        if (static_cast<int>(threadIdx.x) < n_rows)
+          p.lse[(static_cast<int64_t>(e.b()) * p.h + r % p.h) * p.s_q + e.j0() + r / p.h] = NEG_INF;
       }
     }
   }

@@ -1,5 +1,5 @@
 // Host entry points of the windowed decode (mla_window.cuh): argument checks,
-// the number of pieces a token's tiles are cut into, launches.
+// how the work is laid out and cut, launches; and the merge of cut items.
 #include "mla_decode.h"
 #include "mla_internal.h"
 #include "mla_launch.cuh"
@@ -9,30 +9,122 @@ namespace mla {
 
 namespace {
 
-// Pieces per token.  Every token has at most `tiles` tiles; a piece costs its
-// tiles plus kFixedCost (query load, epilogue), and cutting costs the fp32
-// partial rows and the combine besides, about kSplitCost tiles.  With few
-// tokens the parts would otherwise idle.
-constexpr int kSplitCost = 2;
-int window_splits(int64_t n_seq, int tiles, int parts) {
-  int best = 1;
-  int64_t best_cost = 0;
-  for (int n = 1; n <= tiles && n <= 2 * parts; ++n) {
-    const int64_t rounds = (n_seq * n + parts - 1) / parts;
-    const int64_t cost = rounds * ((tiles + n - 1) / n + kFixedCost) + (n > 1 ? kSplitCost : 0);
-    if (n == 1 || cost < best_cost) {
-      best = n;
-      best_cost = cost;
-    }
-    if (n_seq * n >= 2 * static_cast<int64_t>(parts)) break;  // every part has work: more pieces only cost
+// Merge of the items that were cut.  A cut item belongs to the part with its
+// first tile, which ends inside it, so a part has at most one: block (part,
+// row) merges one query row of it,
+//   lse = ln sum_i e^lse_i,   out = sum_i e^(lse_i - lse) o_i,
+// over the item's pieces (those that hold no tile were not written and are left
+// out).  Thread t owns columns 4t .. 4t + 3; the pieces' rows are requested
+// four at a time, the first four before the weights are known, since with few
+// tokens an item has dozens of pieces and the reads' latency is all there is.
+constexpr int kMergeThreads = kDv / 4;
+constexpr int kMergeAhead = 4;
+
+__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const __grid_constant__ SplitParams p, int block_rows) {
+  __shared__ float s_w[kMergeThreads];
+  __shared__ int32_t s_row[kMergeThreads];
+  const WindowPlan& w = p.plan;
+  const int part = blockIdx.x, r = blockIdx.y, lane = part % w.lanes, pl = part / w.lanes;
+  const int64_t m = floordiv((pl + 1) * w.per - 1, w.tiles + w.fixed);
+  const int64_t item = lane + w.lanes * m;
+  if (item >= w.items || window_first_part(w, m) != pl) return;
+  const int pieces = static_cast<int>(window_last_part(w, m) - pl) + 1;
+  const int b = static_cast<int>(item) / w.chunks, j0 = (static_cast<int>(item) - b * w.chunks) * w.group;
+  const int j = j0 + r / p.h, head = r % p.h;
+  if (pieces == 1 || r >= w.group * p.h || j >= p.s_q) return;
+  const int tiles = window_span(window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group), p.window, p.sinks).tiles;
+  pdl_wait_primary();
+  if (tiles == 0) return;  // the walking part wrote its rows
+  // row of piece i (at most one block's threads' worth of pieces a round)
+  auto row_of = [&](int i) {
+    const WindowPiece piece = window_piece(w, m, pl + i, tiles);
+    return piece.t0 < piece.t1 ? window_row(w, m, pl + i, lane) * block_rows + r : -1;
+  };
+  // the maximum over all pieces
+  float mx = -INFINITY;
+  for (int i = threadIdx.x; i < pieces; i += kMergeThreads) {
+    const int32_t row = row_of(i);
+    if (row >= 0) mx = fmaxf(mx, p.ws_lse[row]);
   }
-  return best;
+  mx = warp_max_f32(mx);
+  if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(s_w[0], s_w[1]), fmaxf(s_w[2], s_w[3]));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int i0 = 0; i0 < pieces; i0 += kMergeThreads) {
+    const int n = min(pieces - i0, kMergeThreads);
+    if (static_cast<int>(threadIdx.x) < n) {
+      const int32_t row = row_of(i0 + threadIdx.x);
+      s_row[threadIdx.x] = row;
+      s_w[threadIdx.x] = row >= 0 ? __expf(p.ws_lse[row] - ref) : 0.f;
+    }
+    __syncthreads();
+    for (int i = 0; i < n; i += kMergeAhead) {
+      float4 v[kMergeAhead];
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k) {
+        const int32_t row = i + k < n ? s_row[i + k] : -1;
+        v[k] = row >= 0 ? reinterpret_cast<const float4*>(p.ws_o + static_cast<int64_t>(row) * kDv)[threadIdx.x]
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k) {
+        const float e = i + k < n ? s_w[i + k] : 0.f;
+        sum += e;
+        acc.x += e * v[k].x; acc.y += e * v[k].y; acc.z += e * v[k].z; acc.w += e * v[k].w;
+      }
+    }
+    __syncthreads();
+  }
+  const float lse = sum > 0.f ? ref + __logf(sum) : -INFINITY;
+  float inv = sum > 0.f ? 1.f / sum : 0.f;
+  if (p.attn_sink) inv *= attn_sink_factor(lse, p.attn_sink[head]);
+  const int64_t tok = static_cast<int64_t>(b) * p.s_q + j;
+  reinterpret_cast<uint2*>(p.out + (tok * p.h + head) * kDv)[threadIdx.x] =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (threadIdx.x == 0) p.lse[(static_cast<int64_t>(b) * p.h + head) * p.s_q + j] = lse;
 }
 
 int check_window(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts) {
   if (batch <= 0 || s_q <= 0 || static_cast<int64_t>(batch) * s_q > (1 << 24)) return MLA_ERR_SHAPE;
-  if (!heads_supported(h_q) || window <= 0 || sinks < 0 || num_sm_parts <= 0) return MLA_ERR_SHAPE;
+  if (!heads_supported(h_q) || window <= 0 || sinks < 0 || num_sm_parts <= 0 || num_sm_parts > (1 << 20))
+    return MLA_ERR_SHAPE;
   return MLA_OK;
+}
+
+// Which kernel a call runs on, and its plan.  The two-SM kernel takes 128 query
+// rows and the bf16 cache; the one-SM kernel 64 rows (two CTAs for 128 heads)
+// and every cache.  Fewer heads than rows: tokens of a request fill the block.
+// A bf16 call goes to the two-SM kernel when a block of it gets more rows than
+// a block of the other would hold.
+struct WindowCall {
+  bool pair;
+  int block_rows;  // query rows of a block = rows of a workspace block
+  WindowPlan plan;
+};
+// fixed cost of an item and cost of a cut, in tiles
+constexpr int kPairFixed = 5, kPairCut = 8, kOneFixed = 2, kOneCut = 4;
+
+WindowCall window_call(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts, bool bf16, bool ragged) {
+  WindowCall c;
+  const int sms = num_sm_parts * head_blocks(h_q);  // SMs that the parts stand for
+  const int most = pair::kRows / h_q;
+  const int fill = (s_q < most ? s_q : most) * h_q;
+  c.pair = bf16 && fill > kRowsPerCta;
+  c.block_rows = c.pair || h_q > kRowsPerCta ? pair::kRows : kRowsPerCta;
+  const int tokens = c.block_rows / h_q;
+  const int parts = c.pair ? (sms > 1 ? sms / 2 : 1) : num_sm_parts;
+  c.plan = window_plan(batch, s_q, s_q < tokens ? s_q : tokens, window, sinks, parts, ragged,
+                       c.pair ? kPairFixed : kOneFixed, c.pair ? kPairCut : kOneCut);
+  return c;
+}
+
+// Two blocks of partial rows per part, as many rows whichever kernel runs.
+size_t window_bytes(const WindowCall& c) {
+  return c.plan.whole ? 0 : static_cast<size_t>(2) * c.plan.parts * c.block_rows * (kDv + 1) * sizeof(float);
 }
 
 }  // namespace
@@ -46,9 +138,13 @@ extern "C" int mla_window_workspace_size(int batch, int s_q, int h_q, int window
   if (!bytes) return MLA_ERR_NULL;
   const int rc = check_window(batch, s_q, h_q, window, sinks, num_sm_parts);
   if (rc != MLA_OK) return rc;
-  const int64_t n_seq = static_cast<int64_t>(batch) * s_q;
-  const int n_split = window_splits(n_seq, window_max_tiles(window, sinks), num_sm_parts);
-  *bytes = n_split == 1 ? 0 : static_cast<size_t>(n_seq) * n_split * h_q * (kDv + 1) * sizeof(float);
+  // the call may be with either kind of cache, with or without new_lens
+  size_t most = 0;
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    const size_t n = window_bytes(window_call(batch, s_q, h_q, window, sinks, num_sm_parts, bf16 != 0, false));
+    most = n > most ? n : most;
+  }
+  *bytes = most;
   return MLA_OK;
 }
 
@@ -56,7 +152,8 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
                                  const int32_t* block_table, int64_t block_table_stride, int64_t max_pages,
                                  const int32_t* cache_seqlens, const int32_t* new_lens, int batch, int s_q, int h_q,
                                  int window, int sinks, float softmax_scale, const float* attn_sink, int num_sm_parts,
-                                 void* workspace, void* out, float* lse, uint32_t* err, cudaStream_t stream) {
+                                 void* workspace, size_t workspace_bytes, void* out, float* lse, uint32_t* err,
+                                 cudaStream_t stream) {
   int rc = check_window(batch, s_q, h_q, window, sinks, num_sm_parts);
   if (rc != MLA_OK) return rc;
   if (!q || !kv_cache || !block_table || !cache_seqlens || !out || !lse) return MLA_ERR_NULL;
@@ -68,9 +165,11 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
   if (!(softmax_scale > 0.f) || !(softmax_scale < 1e30f)) return MLA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(workspace) || !aligned16(out)) return MLA_ERR_ALIGN;
 
-  const int n_seq = batch * s_q;
-  const int n_split = window_splits(n_seq, window_max_tiles(window, sinks), num_sm_parts);
-  if (n_split > 1 && !workspace) return MLA_ERR_NULL;
+  const WindowCall call = window_call(batch, s_q, h_q, window, sinks, num_sm_parts, kv_format == MLA_KV_BF16,
+                                      new_lens != nullptr);
+  const size_t need = window_bytes(call);
+  if (need > 0 && !workspace) return MLA_ERR_NULL;
+  if (need > workspace_bytes) return record_error("mla_window_decode: the workspace is too small", MLA_ERR_SHAPE);
   SplitParams prm = {};
   prm.block_table = block_table;
   prm.bt_stride = block_table_stride;
@@ -80,37 +179,48 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
   prm.new_lens = new_lens;
   prm.window = window;
   prm.sinks = sinks;
-  prm.n_split = n_split;
+  prm.plan = call.plan;
   prm.batch = batch;
   prm.attn_sink = attn_sink;
   prm.kv_rows = static_cast<const __nv_bfloat16*>(kv_cache);
   prm.kv_fp8 = static_cast<const uint8_t*>(kv_cache);
   prm.q = static_cast<const __nv_bfloat16*>(q);
   prm.ws_o = static_cast<float*>(workspace);
-  prm.ws_lse = prm.ws_o + static_cast<int64_t>(n_seq) * n_split * h_q * kDv;
+  if (need > 0) prm.ws_lse = prm.ws_o + static_cast<int64_t>(2) * call.plan.parts * call.block_rows * kDv;
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
   prm.err = err;
   prm.h = h_q;
   prm.d_qk = kv_format == MLA_KV_FP8_528 ? kV41HeadDim : kDqk;
   prm.s_q = s_q;
-  prm.num_parts = num_sm_parts;
+  // parts past the last line's have nothing to walk
+  prm.num_parts = call.plan.whole ? call.plan.lanes : call.plan.parts;
   prm.n_hblk = head_blocks(h_q);
-  prm.rows = h_q < kRowsPerCta ? h_q : kRowsPerCta;
+  prm.rows = h_q > kRowsPerCta ? kRowsPerCta : (call.pair ? kRowsPerCta : call.plan.group * h_q);
   prm.scale_log2 = softmax_scale * 1.4426950408889634f;
 
   CacheMaps maps;
-  rc = make_cache_maps(&maps, prm, kv_cache, kv_format);
+  rc = make_cache_maps(&maps, prm, kv_cache, kv_format, call.pair);
   if (rc != MLA_OK) return rc;
   if (kv_format == MLA_KV_FP8_528)
     rc = launch_split<KvMode::kPagedFp8V41, true>(maps.q, maps.kv, prm, stream, &maps.codes, &maps.scales);
   else if (kv_format == MLA_KV_FP8_656)
     rc = launch_split<KvMode::kPagedFp8, true>(maps.q, maps.kv, prm, stream, &maps.codes, &maps.scales);
-  else if (h_q == pair::kRows)
+  else if (call.pair)
     rc = launch_pair<false, true>(maps.kv, maps.quad4, maps.quad3, prm, stream);
   else
     rc = launch_split<KvMode::kPagedBf16, true>(maps.q, maps.kv, prm, stream);
-  if (rc != MLA_OK || n_split == 1) return rc;
-  return launch_window_combine(cache_seqlens, new_lens, batch, s_q, h_q, window, sinks, n_split, workspace, attn_sink,
-                               out, lse, stream);
+  if (rc != MLA_OK || call.plan.whole) return rc;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(call.plan.parts, call.plan.group * h_q, 1);
+  cfg.blockDim = dim3(kMergeThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, window_merge_kernel, prm, call.block_rows);
+  return e == cudaSuccess ? MLA_OK : record_cuda_error("window merge kernel launch", e);
 }

@@ -1,20 +1,25 @@
-// Windowed attention: which keys a query token sees and how its work is cut.
+// Windowed attention: which keys query tokens see and how the work is cut.
 // Pure integer arithmetic, compiled for host and device.
 //
 // A token at position p of its request sees the keys t <= p with t > p - window
-// or t < sinks.  The pages that hold any of them are two runs, the first
-// tokens' and the window's (one run when they meet); written one after the
-// other they form the token's page list, and a 128-key tile is two consecutive
-// entries of that list.  So a tile always holds a visible key, pages between
-// the runs are never touched, and a few first tokens share their tile with the
-// window's first page.  Keys of a tile that the token does not see are masked
-// by position.
+// or t < sinks.  A kernel's block of query rows holds the heads of `group`
+// consecutive tokens of a request (an item): with few heads several tokens fill
+// a block, and they see nearly the same keys.  The pages that hold a key that
+// any of them sees are two runs, the first tokens' and the window's (one run
+// when they meet); written one after the other they form the item's page list,
+// and a 128-key tile is two consecutive entries of that list.  Pages between the
+// runs are never touched, and a few first tokens share their tile with the
+// window's first page.  Keys of a tile that a token does not see are masked by
+// position.
 //
-// No schedule is needed: a token has at most window / 128 + 2 tiles (and the
-// first tokens'), so every token's list is cut into the same number of pieces,
-// chosen on the host, and part i walks the pieces i, i + parts, ...
-// Neighbouring tokens of a request are walked at the same time and find each
-// other's keys in L2.
+// No schedule is built on the device: an item has at most `tiles` tiles, so the
+// cost line of all items is known without their lengths.  Each item takes
+// fixed + tiles cost units on it, a part walks the units [part * per, (part + 1)
+// * per), and an item with fewer tiles scales its range.  With per a multiple of
+// an item's cost nothing is cut; otherwise an item on a boundary is cut into
+// pieces that the combine merges.  The items are dealt to `lanes` cost lines in
+// turn, so that neighbouring items, which share keys, are walked at the same
+// time by different parts and find each other's keys in L2.
 #pragma once
 
 #include <cstdint>
@@ -37,53 +42,164 @@ MLA_HD int32_t window_end(const int32_t* seqlens, const int32_t* new_lens, int s
   return (j >= n || L <= 0 || end < 0) ? 0 : end;
 }
 
+// The ends of the tokens j0 .. j0 + group - 1 that are no padding: the least and
+// the largest (both 0 when there is none).
+struct WindowEnds {
+  int32_t least, most;
+};
+MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j0, int group) {
+  int32_t n = new_lens ? new_lens[b] : s;
+  n = n < 0 ? 0 : (n > s ? s : n);
+  int32_t L = seqlens[b];
+  L = L > kWindowMaxLen ? kWindowMaxLen : L;
+  const int32_t last = (j0 + group < n ? j0 + group : n) - 1;  // the last token that is not past the new ones
+  WindowEnds e;
+  e.most = L - n + last + 1;
+  e.least = L - n + j0 + 1 > 1 ? L - n + j0 + 1 : 1;
+  if (last < j0 || L <= 0 || e.most <= 0) e.least = e.most = 0;
+  return e;
+}
+
+MLA_HD int32_t window_lo(int32_t end, int32_t window) { return end > window ? end - window : 0; }
+MLA_HD uint32_t low_bits(int32_t n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+// Whether a token with this end sees key t; bit i of the mask: key x + i.
+MLA_HD bool window_sees(int32_t end, int32_t window, int32_t sinks, int32_t t) {
+  return t < end && (t < sinks || t >= window_lo(end, window));
+}
+MLA_HD uint32_t window_mask32(int32_t end, int32_t window, int32_t sinks, int32_t x) {
+  return low_bits(end - x) & (low_bits(sinks - x) | ~low_bits(window_lo(end, window) - x));
+}
+
+// The page list of an item.
 struct WindowSpan {
-  int32_t end, lo, first;  // key t is seen when t < end and (t < first or t >= lo)
-  int32_t head_pages;      // list entries of the first tokens' run
-  int32_t skip;            // pages between the two runs
+  int32_t head_pages;  // entries of the first tokens' run
+  int32_t skip;        // pages between the two runs
   int32_t tiles;
+  // tiles that may hold a key that one of the tokens does not see: the one with
+  // the last of the first tokens, those with the tokens' first window keys, and
+  // from the one with the first token's last key on
+  int32_t edge_head, edge_lo, edge_hi, edge_end;
 
   // logical page of entry e of the list
   MLA_HD int32_t page(int32_t e) const { return e < head_pages ? e : e + skip; }
-  MLA_HD bool sees(int32_t t) const { return t < end && (t < first || t >= lo); }
-  // bit i: key x + i is seen
-  MLA_HD uint32_t mask32(int32_t x) const { return low_bits(end - x) & (low_bits(first - x) | ~low_bits(lo - x)); }
-  // Whether tile t may hold a key that is not seen: the tiles with the last of
-  // the first tokens, with the window's first key and with the last key.
-  MLA_HD bool edge(int32_t t) const {
-    return t == tiles - 1 || (lo > 0 && t == (lo / kWindowPage - skip) / 2) ||
-           (first > 0 && t == (first - 1) / kWindowPage / 2);
-  }
-  MLA_HD static uint32_t low_bits(int32_t n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+  MLA_HD bool edge(int32_t t) const { return t == edge_head || (t >= edge_lo && t <= edge_hi) || t >= edge_end; }
 };
 
-MLA_HD WindowSpan window_span(int32_t end, int32_t window, int32_t sinks) {
+MLA_HD WindowSpan window_span(WindowEnds e, int32_t window, int32_t sinks) {
   WindowSpan w;
-  w.end = end;
-  w.lo = end > window ? end - window : 0;
-  w.first = sinks < w.lo ? sinks : 0;
-  if (sinks >= w.lo) w.lo = 0;  // the two runs of keys meet: everything is seen
-  w.head_pages = w.first > 0 ? (w.first - 1) / kWindowPage + 1 : 0;
-  const int32_t first_page = w.lo / kWindowPage;
+  const int32_t lo = window_lo(e.least, window), lo_most = window_lo(e.most, window);
+  const bool two = sinks > 0 && sinks < lo;  // the runs of keys do not meet
+  w.head_pages = two ? (sinks - 1) / kWindowPage + 1 : 0;
+  const int32_t first_page = (sinks > 0 && !two) ? 0 : lo / kWindowPage;
   w.skip = first_page > w.head_pages ? first_page - w.head_pages : 0;
-  const int32_t pages = end > 0 ? (end - 1) / kWindowPage + 1 - w.skip : 0;
+  const int32_t pages = e.most > 0 ? (e.most - 1) / kWindowPage + 1 - w.skip : 0;
   w.tiles = (pages + 1) / 2;
+  w.edge_head = sinks > 0 && sinks < lo_most ? (sinks - 1) / kWindowPage / 2 : -1;
+  w.edge_lo = lo_most > 0 ? (lo / kWindowPage - w.skip) / 2 : 0;
+  w.edge_hi = lo_most > 0 ? (lo_most / kWindowPage - w.skip) / 2 : -1;
+  const int32_t from = (e.least / kWindowPage - w.skip) / 2;
+  w.edge_end = from < w.tiles - 1 ? from : w.tiles - 1;
   return w;
 }
 
-// The most tiles that any token can have.
-MLA_HD int32_t window_max_tiles(int32_t window, int32_t sinks) {
-  const int64_t w = window < kWindowMaxLen ? window : kWindowMaxLen, k = sinks < kWindowMaxLen ? sinks : kWindowMaxLen;
+// The most tiles that an item of `group` tokens can have.
+MLA_HD int32_t window_max_tiles(int32_t window, int32_t sinks, int32_t group) {
+  const int64_t w = (window < kWindowMaxLen ? window : kWindowMaxLen) + static_cast<int64_t>(group) - 1;
+  const int64_t k = sinks < kWindowMaxLen ? sinks : kWindowMaxLen;
   const int64_t pages = (w + kWindowPage - 2) / kWindowPage + 1 + (k + kWindowPage - 1) / kWindowPage;
   return static_cast<int32_t>((pages + 1) / 2);
 }
 
-// Piece `split` of n_split of a token's tiles: [t0, t1); a token with fewer
-// tiles than n_split has one piece a tile.
-MLA_HD int32_t window_pieces(int32_t tiles, int32_t n_split) { return tiles < n_split ? tiles : n_split; }
-MLA_HD void window_piece(int32_t tiles, int32_t pieces, int32_t split, int* t0, int* t1) {
-  *t0 = static_cast<int>(static_cast<int64_t>(split) * tiles / pieces);
-  *t1 = static_cast<int>(static_cast<int64_t>(split + 1) * tiles / pieces);
+// How a call's items are laid on the cost lines and cut.
+struct WindowPlan {
+  int32_t group;   // tokens per item
+  int32_t chunks;  // items per request
+  int32_t items;
+  int32_t parts;
+  int32_t tiles;   // of an item on the cost line
+  int32_t fixed;   // cost of an item besides its tiles
+  int32_t lanes;   // cost lines: item i is number i / lanes of line i % lanes; part p is number p / lanes of line p % lanes
+  int64_t per;     // cost units per part
+  bool whole;      // per is a multiple of an item's cost: nothing is cut
+};
+
+// Piece of item number m of a line that the line's part number pl walks, out of
+// n_tiles tiles: [t0, t1), empty when t0 >= t1.
+struct WindowPiece {
+  int32_t t0, t1;
+  bool owner;  // the part with the item's first unit: it writes items without a key
+  bool cut;    // other parts walk tiles of the item too
+};
+MLA_HD int32_t window_scaled(int64_t unit, int32_t n_tiles, int32_t tiles) {
+  return tiles == n_tiles ? static_cast<int32_t>(unit) : static_cast<int32_t>(floordiv(unit * n_tiles, tiles));
+}
+MLA_HD WindowPiece window_piece(const WindowPlan& w, int64_t m, int64_t pl, int32_t n_tiles) {
+  const int64_t at = m * (w.tiles + w.fixed) + w.fixed;  // the unit of its first tile
+  const int64_t x0 = pl * w.per - at, x1 = x0 + w.per;
+  const int64_t b = x0 > 0 ? x0 : 0, e = x1 < w.tiles ? x1 : w.tiles;
+  WindowPiece p;
+  p.owner = x0 <= 0 && x1 > 0;
+  p.cut = b > 0 || e < w.tiles;
+  p.t0 = p.t1 = 0;
+  if (b < e) {
+    p.t0 = window_scaled(b, n_tiles, w.tiles);
+    p.t1 = window_scaled(e, n_tiles, w.tiles);
+  }
+  return p;
+}
+// First item number that part number pl walks, and the line's parts that walk
+// tiles of item number m.
+MLA_HD int64_t window_first_item(const WindowPlan& w, int64_t pl) { return floordiv(pl * w.per, w.tiles + w.fixed); }
+MLA_HD int64_t window_first_part(const WindowPlan& w, int64_t m) {
+  return floordiv(m * (w.tiles + w.fixed) + w.fixed, w.per);
+}
+MLA_HD int64_t window_last_part(const WindowPlan& w, int64_t m) {
+  return floordiv((m + 1) * (w.tiles + w.fixed) - 1, w.per);
+}
+// Workspace block of a cut item's piece: a part walks at most two such pieces,
+// of the item in whose units it begins and of another at its end.
+MLA_HD int32_t window_row(const WindowPlan& w, int64_t m, int64_t pl, int32_t lane) {
+  return static_cast<int32_t>(2 * (pl * w.lanes + lane) + (window_first_item(w, pl) == m ? 0 : 1));
+}
+
+// split_cost: what a cut costs besides the cost line, in tiles: the extra piece
+// of a part, the fp32 partial rows and the combine.
+inline WindowPlan window_plan(int batch, int s_q, int group, int window, int sinks, int parts, bool ragged, int fixed,
+                              int split_cost) {
+  WindowPlan w;
+  w.group = group;
+  w.chunks = (s_q + group - 1) / group;
+  w.items = batch * w.chunks;
+  w.parts = parts;
+  w.tiles = window_max_tiles(window, sinks, group);
+  w.fixed = fixed;
+  const int64_t cost = static_cast<int64_t>(w.tiles) + fixed;
+  // whole items, dealt round
+  const int lines = w.items < parts ? w.items : parts;
+  const int64_t whole = (w.items + lines - 1) / lines * cost;
+  w.lanes = lines;
+  w.per = whole;
+  w.whole = true;
+  // cut into equal parts; with new_lens many items may be padding, and only
+  // dealing whole items round spreads them evenly
+  if (ragged && w.items >= parts) return w;
+  int64_t best = 0;
+  int best_lanes = 1;
+  for (int lanes = 1; lanes <= 16 && lanes <= w.chunks && lanes <= parts; ++lanes) {
+    const int64_t line = (w.items + lanes - 1) / lanes * cost;
+    const int64_t n = parts / lanes;
+    const int64_t per = (line + n - 1) / n;
+    if (lanes == 1) best = per;
+    if (per * 20 <= best * 21) best_lanes = lanes;  // shared keys are worth 5 %
+  }
+  const int64_t n = parts / best_lanes;
+  const int64_t per = ((w.items + best_lanes - 1) / best_lanes * cost + n - 1) / n;
+  if (per + split_cost < whole) {
+    w.lanes = best_lanes;
+    w.per = per;
+    w.whole = false;
+  }
+  return w;
 }
 
 }  // namespace mla

@@ -120,10 +120,20 @@ def test_long_windows_one_after_the_other(fmt, h, parts):
     parity(fmt, [1100, 1900, 1333, 1500, 1920], 2, h, 1000, 70, seed=12, parts=parts)
 
 
-@pytest.mark.parametrize("fmt,h", [(BF16, 128), (BF16, 16), (FP8_656, 64), (FP8_528, 128)])
-def test_a_chunk_of_a_prompt(fmt, h):
-    """Many tokens a request: every part walks several pieces."""
-    parity(fmt, [170, 150], 150, h, 70, 5, new=[150, 131], seed=6, parts=20)
+@pytest.mark.parametrize("fmt,h", [(BF16, 128), (BF16, 16), (BF16, 48), (BF16, 32), (BF16, 64), (FP8_656, 64), (FP8_656, 16),
+                                   (FP8_528, 128), (FP8_528, 32)])
+@pytest.mark.parametrize("window,sinks", [(70, 5), (3, 0)])
+def test_a_chunk_of_a_prompt(fmt, h, window, sinks):
+    """Many tokens a request, several of them in a block of query rows with few
+    heads: every part walks several pieces, blocks begin and end with padding."""
+    parity(fmt, [170, 150, 131], 133, h, window, sinks, new=[133, 121, 9], seed=6, parts=20)
+
+
+@pytest.mark.parametrize("h", [16, 32, 48, 64])
+@pytest.mark.parametrize("fmt", [BF16, FP8_528])
+def test_long_windows_of_blocks_of_tokens(fmt, h):
+    """Blocks of several tokens that are cut into pieces and merged."""
+    parity(fmt, [1900, 700, 64, 12], 11, h, 1200, 3, new=None, seed=13, logits=True)
 
 
 @pytest.mark.parametrize("fmt,h", [(BF16, 128), (BF16, 32), (FP8_656, 128), (FP8_528, 64)])
@@ -192,13 +202,13 @@ def test_binding_refusals():
     def but(i, v):
         return ok[:i] + [v] + ok[i + 1:]
     for bad in (but(0, q.float()), but(0, q[0]), but(0, q[..., :512]), but(0, torch.cat([q, q], 3)[..., :576]), but(1, cache.float()),
-                but(2, 5), but(3, bt.long()), but(3, bt[:1]), but(4, sl.long()), but(9, None), but(9, buf.workspace[:-1]),
+                but(2, 5), but(3, bt.long()), but(3, bt[:1]), but(4, sl.long()), but(9, buf.workspace.cpu()),
                 but(10, buf.out.float()), but(10, buf.out[:, :, :32]), but(11, buf.lse[:1]), but(11, buf.lse.cpu())):
         with pytest.raises(ValueError):
             binding.mla_window_decode(*bad)
     for kw in (dict(attn_sink=torch.zeros(63, device=DEV)), dict(new_lens=sl.long()), dict(err=sl)):
         with pytest.raises(ValueError):
             binding.mla_window_decode(*ok, **kw)
-    for bad in (but(6, 0), but(7, -1), but(5, 0.0), but(8, 0)):
+    for bad in (but(6, 0), but(7, -1), but(5, 0.0), but(8, 0), but(9, None), but(9, buf.workspace[:-1])):
         with pytest.raises(binding.MlaError):
             binding.mla_window_decode(*bad)

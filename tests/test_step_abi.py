@@ -21,7 +21,7 @@ APPEND = dict(x=0x10000, stride=576, sl=0x20000, new=None, b=2, s=1, table=0x300
 QUERY = dict(q=0x10000, qt=1024, qh=512, sl=0x20000, new=None, b=2, s=1, h=2, d=512, table=0x30000, rows=100, style=0,
              w=0x40000, eps=1e-6, out=0x50000, ot=1024, oh=512, err=None, stream=None)
 WINDOW = dict(q=0x10000, cache=0x20000, fmt=0, pages=8, bt=0x30000, bts=4, width=4, sl=0x40000, new=None, b=2, s=1, h=16,
-              window=128, sinks=4, scale=0.07, sink=None, parts=152, ws=0x50000, out=0x60000, lse=0x70000, err=None,
+              window=128, sinks=4, scale=0.07, sink=None, parts=152, ws=0x50000, wsb=1 << 40, out=0x60000, lse=0x70000, err=None,
               stream=None)
 NAN = float("nan")
 
@@ -58,7 +58,7 @@ def test_query_refuses(over, code):
 
 @pytest.mark.parametrize("over,code", [
     (dict(q=None), -1), (dict(cache=None), -1), (dict(bt=None), -1), (dict(sl=None), -1), (dict(out=None), -1),
-    (dict(lse=None), -1), (dict(b=1, window=8192, ws=None), -1), (dict(b=0), -2), (dict(s=0), -2),
+    (dict(lse=None), -1), (dict(b=1, window=8192, ws=None), -1), (dict(b=1, window=8192, wsb=1000), -2), (dict(b=0), -2), (dict(s=0), -2),
     (dict(b=1 << 20, s=17), -2), (dict(h=100), -2), (dict(h=256), -2), (dict(window=0), -2), (dict(window=-5), -2),
     (dict(sinks=-1), -2), (dict(parts=0), -2), (dict(pages=0), -2), (dict(width=0), -2), (dict(bts=2), -2),
     (dict(scale=0.0), -2), (dict(scale=NAN), -2), (dict(q=0x10008), -3), (dict(cache=0x20001), -3), (dict(out=0x60002), -3),
@@ -70,12 +70,13 @@ def test_window_refuses(over, code):
 
 def test_window_workspace():
     size = binding.mla_window_workspace_size
-    assert size(64, 1, 128, 128, 4, 76) == 0            # as many tokens as parts: nothing is cut
-    one = size(1, 1, 64, 8192, 0, 152)
-    assert one > 0 and one % (64 * 513 * 4) == 0        # whole rows of partials
-    assert one // (64 * 513 * 4) <= 65                  # at most one piece a tile
-    assert size(1, 1, 64, 2**31 - 1, 2**31 - 1, 152) > 0
-    assert size(1 << 20, 16, 128, 2**31 - 1, 0, 76) == 0
+    assert size(64, 1, 128, 128, 4, 76) == 0            # nothing is cut
+    one = 2 * 152 * 64 * 513 * 4                        # two blocks of rows per part
+    assert size(1, 1, 64, 8192, 0, 152) == one
+    assert size(1, 1, 128, 8192, 0, 76) == one          # 76 parts of two SMs
+    assert size(1, 9, 16, 8192, 0, 152) == one          # several tokens a block, either kernel
+    assert size(1, 1, 64, 2**31 - 1, 2**31 - 1, 152) == one
+    assert size(1 << 20, 16, 128, 4096, 0, 76) == 0
     for bad in ((0, 1, 64, 1, 0, 1), (1, 1, 63, 1, 0, 1), (1, 1, 64, 0, 0, 1), (1, 1, 64, 1, -1, 1), (1, 1, 64, 1, 0, 0)):
         with pytest.raises(binding.MlaError):
             size(*bad)
