@@ -826,6 +826,9 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           }
         }
       }
+      if constexpr (kWindow) {
+        if (warp == 2) write_unseen(p, part, 0, kRows, lane, 32);
+      }
     } else if (warp == 1) {
       // ---------------------------------------------------- O += P . V
       if (lane == 0) {
@@ -1058,15 +1061,6 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));
         ++item;
-      }
-      if constexpr (kWindow) {  // tokens that see no key: out = 0, lse = -inf
-        Pieces<true> e(p, nullptr, part);
-        while (pc.passed_empty && e.template next<true>()) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(e.q) * p.h * kDv);
-          for (int i = r; i < e.rows() * kDv / 8; i += kRowThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < e.rows())
-            p.lse[(static_cast<int64_t>(e.b()) * p.h + r % p.h) * p.s_q + e.j0() + r / p.h] = -INFINITY;
-        }
       }
     } else if (warp == 3 && !kSparse) {
       // ---------------------------------------------------- P buffer hand-back

@@ -173,10 +173,8 @@ struct Pieces<true> {
   const SplitParams& p;
   int part, m;                // the next item's number on the part's cost line
   int q, t0, t1;
-  int32_t row;                // block of the split workspace, -1 for an item that is not cut
   WindowEnds ends;
   WindowSpan span;
-  bool passed_empty = false;  // an item that sees no key, and is this part's to write, was passed over
   __device__ __forceinline__ Pieces(const SplitParams& prm, const int32_t*, int part_) : p(prm), part(part_) {
     m = static_cast<int>(window_first_item(p.plan, part / p.plan.lanes));
   }
@@ -193,13 +191,9 @@ struct Pieces<true> {
       ends = window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group);
       span = window_span(ends, p.window, p.sinks);
       const WindowPiece piece = window_piece(w, m, pl, span.tiles);
-      row = piece.cut ? window_row(w, m, pl, lane) : -1;
       ++m;
       q = b * p.s_q + j0;
-      if (span.tiles == 0 && piece.owner) {
-        if (kEmpty) return true;
-        passed_empty = true;
-      }
+      if (kEmpty && span.tiles == 0 && piece.owner) return true;
       t0 = piece.t0; t1 = piece.t1;
       if (!kEmpty && t0 < t1) return true;
     }
@@ -232,9 +226,24 @@ struct Pieces<true> {
   __device__ __forceinline__ int rows_from(int row) const { return min(rows() - row, p.rows); }
   __device__ __forceinline__ int32_t keys() const { return ends.most; }
   __device__ __forceinline__ int32_t page(int32_t e) const { return span.page(e); }
-  __device__ __forceinline__ bool whole() const { return row < 0; }
-  __device__ __forceinline__ int64_t split_row() const { return row; }
+  __device__ __forceinline__ bool whole() const { return !window_piece(p.plan, m - 1, part / p.plan.lanes, 1).cut; }
+  __device__ __forceinline__ int64_t split_row() const {
+    return window_row(p.plan, m - 1, part / p.plan.lanes, part % p.plan.lanes);
+  }
 };
+
+// Windowed: rows row0 .. row0 + most - 1 of the items that see no key and are
+// this part's to write: out = 0, lse = -inf.  Called by threads i = 0 .. n - 1.
+__device__ __forceinline__ void write_unseen(const SplitParams& p, int part, int row0, int most, int i0, int n) {
+  Pieces<true> pc(p, nullptr, part);
+  while (pc.next<true>()) {
+    const int rows = min(pc.rows() - row0, most);
+    uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(pc.q) * p.h + row0) * kDv);
+    for (int i = i0; i < rows * kDv / 8; i += n) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int r = row0 + i0; r < row0 + rows; r += n)
+      p.lse[(static_cast<int64_t>(pc.b()) * p.h + r % p.h) * p.s_q + pc.j0() + r / p.h] = -INFINITY;
+  }
+}
 
 struct SmemSmall {
   // float arrays first: each row of 32 floats is read back as float4 vectors,
@@ -628,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++item_ctr;
       }
+    } else if constexpr (kWindow) {
+      write_unseen(p, part, hb * kRowsPerCta, kRowsPerCta, lane - 1, 31);
     }
   } else if (warp == kProducerWarp && kMode == KvMode::kSparseBf16) {
     // ===================================================== producer (gather)
@@ -754,6 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+    } else if constexpr (kWindow) {
+      write_unseen(p, part, hb * kRowsPerCta, kRowsPerCta, lane - 1, 31);
     }
   } else if (warp == kMmaWarp) {
     // ===================================================== MMA issuer
@@ -856,22 +869,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t keys = pc.keys();
       const int32_t* idx_row = (kMode == KvMode::kSparseBf16)
                                    ? p.indices + static_cast<int64_t>(q) * p.topk : nullptr;
-      [[maybe_unused]] int32_t end = 0;  // windowed: of the token of this warpgroup's rows (h is a multiple of 16)
-      if constexpr (kWindow) end = pc.end_of_row(hb * kRowsPerCta + R * g);
       float m_true = NEG_INF;  // running max of row R*g + (lane & 15) (-inf: no key yet)
       float m_use = 0.f;       // reference the probabilities are taken against
       float m_low = NEG_INF;   // smallest m_true over the warpgroup's rows
       float lsum = 0.f;        // sum p of row R*g + (lane & 15) over this warp's tokens
       float bsum = 0.f;        // sum bf16(p) of the same row
       for (int t = t0; t < t1; ++t) {
-        // windowed: whether this warpgroup's token, or any of the item's, sees
-        // the key of this thread's row
-        [[maybe_unused]] bool seen = true, seen_any = true;
-        if constexpr (kWindow) {
-          const int32_t x = pc.position(t, r);
-          seen = window_sees(end, p.window, p.sinks, x);
-          seen_any = pc.any_sees(x);
-        }
         if constexpr (is_fp8(kMode)) {
           // ---- FP8: convert this tile's owned latent chunks in place.  Thread
           // = (token dq_r, 16-code unit dq_u); reads of the staging finish at
@@ -905,6 +908,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&sm->full[c]));
           }
           if (!ok) break;
+        }
+        // windowed: whether this warpgroup's token, or any of the item's, sees
+        // the key of this thread's row
+        [[maybe_unused]] bool seen = true, seen_any = true;
+        if constexpr (kWindow) {
+          const int32_t x = pc.position(t, r);
+          // (h is a multiple of 16, so the warpgroup's rows are one token's)
+          seen = window_sees(pc.end_of_row(hb * kRowsPerCta + R * g), p.window, p.sinks, x);
+          seen_any = pc.any_sees(x);
         }
         ok = mbar_wait(smem_u32(&sm->s_full), tile_ctr & 1, abort_flag, p.err);
         if constexpr (is_fp8(kMode))  // leave together (the barrier above)
@@ -1087,17 +1099,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.ws_lse[ws_row0 + lane] = lse_v;
       }
       ++item_ctr;
-    }
-    if constexpr (kWindow) {  // tokens that see no key: out = 0, lse = -inf
-      Pieces<true> e(p, nullptr, part);
-      while (pc.passed_empty && e.template next<true>()) {
-        const int row0 = hb * kRowsPerCta, n_rows = min(e.rows() - row0, kRowsPerCta);
-        uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(e.q) * p.h + row0) * kDv);
-        for (int i = threadIdx.x; i < n_rows * kDv / 8; i += 128 * kSoftmaxGroups) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-        const int r = row0 + threadIdx.x;
-        if (static_cast<int>(threadIdx.x) < n_rows)
-          p.lse[(static_cast<int64_t>(e.b()) * p.h + r % p.h) * p.s_q + e.j0() + r / p.h] = NEG_INF;
-      }
     }
   }
 

@@ -9,83 +9,96 @@ namespace mla {
 
 namespace {
 
-// Merge of the items that were cut.  A cut item belongs to the part with its
-// first tile, which ends inside it, so a part has at most one: block (part,
-// row) merges one query row of it,
+// Merge of the items that were cut, one query row a block at a time,
 //   lse = ln sum_i e^lse_i,   out = sum_i e^(lse_i - lse) o_i,
 // over the item's pieces (those that hold no tile were not written and are left
-// out).  Thread t owns columns 4t .. 4t + 3; the pieces' rows are requested
-// four at a time, the first four before the weights are known, since with few
-// tokens an item has dozens of pieces and the reads' latency is all there is.
+// out).  A cut item belongs to the part with its first tile, which ends inside
+// it, so a part has at most one.  Thread t owns columns 4t .. 4t + 3; in every
+// warp lane i looks after piece i, so the warps need no barrier.  A row is a few
+// dependent reads and little else: the pieces' rows are requested four at a
+// time, the first four before the weights are known, and there are as many
+// blocks as fit the device at once, no more (a block for every row of every part
+// took 13 to 19 us a call, most of it blocks that found nothing to do).
 constexpr int kMergeThreads = kDv / 4;
 constexpr int kMergeAhead = 4;
 
-__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const __grid_constant__ SplitParams p, int block_rows) {
-  __shared__ float s_w[kMergeThreads];
-  __shared__ int32_t s_row[kMergeThreads];
+// Parts that may own a cut item: part k * step for k below the count.
+struct MergeOwners {
+  int count, step;
+};
+MergeOwners merge_owners(const WindowPlan& w) {
+  // every item cut into the same pieces, a part each: its first one
+  if (w.lanes == 1 && w.fixed == 0 && w.tiles % w.per == 0) return {w.items, static_cast<int>(w.tiles / w.per)};
+  return {w.parts, 1};
+}
+
+__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const __grid_constant__ SplitParams p,
+                                                                     int block_rows, int owner_step) {
   const WindowPlan& w = p.plan;
-  const int part = blockIdx.x, r = blockIdx.y, lane = part % w.lanes, pl = part / w.lanes;
+  const int part = blockIdx.x * owner_step, line = part % w.lanes, pl = part / w.lanes, lane = threadIdx.x & 31;
   const int64_t m = floordiv((pl + 1) * w.per - 1, w.tiles + w.fixed);
-  const int64_t item = lane + w.lanes * m;
+  const int64_t item = line + w.lanes * m;
   if (item >= w.items || window_first_part(w, m) != pl) return;
   const int pieces = static_cast<int>(window_last_part(w, m) - pl) + 1;
+  if (pieces == 1) return;
   const int b = static_cast<int>(item) / w.chunks, j0 = (static_cast<int>(item) - b * w.chunks) * w.group;
-  const int j = j0 + r / p.h, head = r % p.h;
-  if (pieces == 1 || r >= w.group * p.h || j >= p.s_q) return;
+  const int rows = min(w.group, p.s_q - j0) * p.h;
   const int tiles = window_span(window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group), p.window, p.sinks).tiles;
-  pdl_wait_primary();
-  if (tiles == 0) return;  // the walking part wrote its rows
-  // row of piece i (at most one block's threads' worth of pieces a round)
-  auto row_of = [&](int i) {
+  if (tiles == 0) return;  // the walking part writes its rows
+  // workspace block of piece i, -1 where it holds no tile
+  auto block_of = [&](int i) {
+    if (i >= pieces) return -1;
     const WindowPiece piece = window_piece(w, m, pl + i, tiles);
-    return piece.t0 < piece.t1 ? window_row(w, m, pl + i, lane) * block_rows + r : -1;
+    return piece.t0 < piece.t1 ? window_row(w, m, pl + i, line) : -1;
   };
-  // the maximum over all pieces
-  float mx = -INFINITY;
-  for (int i = threadIdx.x; i < pieces; i += kMergeThreads) {
-    const int32_t row = row_of(i);
-    if (row >= 0) mx = fmaxf(mx, p.ws_lse[row]);
-  }
-  mx = warp_max_f32(mx);
-  if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(s_w[0], s_w[1]), fmaxf(s_w[2], s_w[3]));
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  for (int i0 = 0; i0 < pieces; i0 += kMergeThreads) {
-    const int n = min(pieces - i0, kMergeThreads);
-    if (static_cast<int>(threadIdx.x) < n) {
-      const int32_t row = row_of(i0 + threadIdx.x);
-      s_row[threadIdx.x] = row;
-      s_w[threadIdx.x] = row >= 0 ? __expf(p.ws_lse[row] - ref) : 0.f;
-    }
-    __syncthreads();
-    for (int i = 0; i < n; i += kMergeAhead) {
+  int block = block_of(lane);
+  pdl_wait_primary();
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+      if (pieces > 32) block = block_of(i0 + lane);
+      const float l = block >= 0 ? p.ws_lse[static_cast<int64_t>(block) * block_rows + r] : -INFINITY;
+      const int n = min(pieces - i0, 32);
+      auto load = [&](int i, float4 (&v)[kMergeAhead]) {
+#pragma unroll
+        for (int k = 0; k < kMergeAhead; ++k) {
+          const int at = __shfl_sync(0xffffffffu, block, (i + k) & 31);
+          v[k] = i + k < n && at >= 0
+                     ? reinterpret_cast<const float4*>(p.ws_o + (static_cast<int64_t>(at) * block_rows + r) * kDv)[threadIdx.x]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      };
       float4 v[kMergeAhead];
+      load(0, v);
+      const float mx_new = fmaxf(mx, warp_max_f32(l));
+      const float ref = mx_new == -INFINITY ? 0.f : mx_new;
+      const float keep = i0 == 0 ? 0.f : __expf(mx - ref);  // what was summed before, at the new reference
+      mx = mx_new;
+      const float e = __expf(l - ref);
+      float part_sum = e;
 #pragma unroll
-      for (int k = 0; k < kMergeAhead; ++k) {
-        const int32_t row = i + k < n ? s_row[i + k] : -1;
-        v[k] = row >= 0 ? reinterpret_cast<const float4*>(p.ws_o + static_cast<int64_t>(row) * kDv)[threadIdx.x]
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      for (int sh = 16; sh > 0; sh >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, sh);
+      sum = sum * keep + part_sum;
+      acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+      for (int i = 0; i < n; i += kMergeAhead) {
+        if (i > 0) load(i, v);
 #pragma unroll
-      for (int k = 0; k < kMergeAhead; ++k) {
-        const float e = i + k < n ? s_w[i + k] : 0.f;
-        sum += e;
-        acc.x += e * v[k].x; acc.y += e * v[k].y; acc.z += e * v[k].z; acc.w += e * v[k].w;
+        for (int k = 0; k < kMergeAhead; ++k) {
+          const float f = __shfl_sync(0xffffffffu, e, (i + k) & 31);  // 0 past the last piece
+          acc.x += f * v[k].x; acc.y += f * v[k].y; acc.z += f * v[k].z; acc.w += f * v[k].w;
+        }
       }
     }
-    __syncthreads();
+    const float lse = sum > 0.f ? (mx + __logf(sum)) : -INFINITY;
+    float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int j = j0 + r / p.h, head = r % p.h;
+    if (p.attn_sink) inv *= attn_sink_factor(lse, p.attn_sink[head]);
+    const int64_t tok = static_cast<int64_t>(b) * p.s_q + j;
+    reinterpret_cast<uint2*>(p.out + (tok * p.h + head) * kDv)[threadIdx.x] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (threadIdx.x == 0) p.lse[(static_cast<int64_t>(b) * p.h + head) * p.s_q + j] = lse;
   }
-  const float lse = sum > 0.f ? ref + __logf(sum) : -INFINITY;
-  float inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (p.attn_sink) inv *= attn_sink_factor(lse, p.attn_sink[head]);
-  const int64_t tok = static_cast<int64_t>(b) * p.s_q + j;
-  reinterpret_cast<uint2*>(p.out + (tok * p.h + head) * kDv)[threadIdx.x] =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (threadIdx.x == 0) p.lse[(static_cast<int64_t>(b) * p.h + head) * p.s_q + j] = lse;
 }
 
 int check_window(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts) {
@@ -105,8 +118,8 @@ struct WindowCall {
   int block_rows;  // query rows of a block = rows of a workspace block
   WindowPlan plan;
 };
-// fixed cost of an item and cost of a cut, in tiles
-constexpr int kPairFixed = 5, kPairCut = 8, kOneFixed = 2, kOneCut = 4;
+// fixed cost of a piece and cost of a merge, in tiles
+constexpr int kPairFixed = 5, kPairMerge = 3, kOneFixed = 2, kOneMerge = 2;
 
 WindowCall window_call(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts, bool bf16, bool ragged) {
   WindowCall c;
@@ -118,7 +131,7 @@ WindowCall window_call(int batch, int s_q, int h_q, int window, int sinks, int n
   const int tokens = c.block_rows / h_q;
   const int parts = c.pair ? (sms > 1 ? sms / 2 : 1) : num_sm_parts;
   c.plan = window_plan(batch, s_q, s_q < tokens ? s_q : tokens, window, sinks, parts, ragged,
-                       c.pair ? kPairFixed : kOneFixed, c.pair ? kPairCut : kOneCut);
+                       c.pair ? kPairFixed : kOneFixed, c.pair ? kPairMerge : kOneMerge);
   return c;
 }
 
@@ -193,8 +206,7 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
   prm.h = h_q;
   prm.d_qk = kv_format == MLA_KV_FP8_528 ? kV41HeadDim : kDqk;
   prm.s_q = s_q;
-  // parts past the last line's have nothing to walk
-  prm.num_parts = call.plan.whole ? call.plan.lanes : call.plan.parts;
+  prm.num_parts = call.plan.parts;
   prm.n_hblk = head_blocks(h_q);
   prm.rows = h_q > kRowsPerCta ? kRowsPerCta : (call.pair ? kRowsPerCta : call.plan.group * h_q);
   prm.scale_log2 = softmax_scale * 1.4426950408889634f;
@@ -213,7 +225,9 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
   if (rc != MLA_OK || call.plan.whole) return rc;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(call.plan.parts, call.plan.group * h_q, 1);
+  const MergeOwners owners = merge_owners(call.plan);
+  const int rows = call.plan.group * h_q, fit = 8 * num_sm_parts * head_blocks(h_q) / owners.count;
+  cfg.gridDim = dim3(owners.count, fit < 1 ? 1 : (fit < rows ? fit : rows), 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -221,6 +235,7 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, window_merge_kernel, prm, call.block_rows);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, window_merge_kernel, prm, call.block_rows,
+                                           owners.step);
   return e == cudaSuccess ? MLA_OK : record_cuda_error("window merge kernel launch", e);
 }

@@ -134,6 +134,7 @@ MLA_HD int32_t window_scaled(int64_t unit, int32_t n_tiles, int32_t tiles) {
   return tiles == n_tiles ? static_cast<int32_t>(unit) : static_cast<int32_t>(floordiv(unit * n_tiles, tiles));
 }
 MLA_HD WindowPiece window_piece(const WindowPlan& w, int64_t m, int64_t pl, int32_t n_tiles) {
+  if (w.whole) return {0, n_tiles, true, false};
   const int64_t at = m * (w.tiles + w.fixed) + w.fixed;  // the unit of its first tile
   const int64_t x0 = pl * w.per - at, x1 = x0 + w.per;
   const int64_t b = x0 > 0 ? x0 : 0, e = x1 < w.tiles ? x1 : w.tiles;
@@ -147,9 +148,11 @@ MLA_HD WindowPiece window_piece(const WindowPlan& w, int64_t m, int64_t pl, int3
   }
   return p;
 }
-// First item number that part number pl walks, and the line's parts that walk
-// tiles of item number m.
-MLA_HD int64_t window_first_item(const WindowPlan& w, int64_t pl) { return floordiv(pl * w.per, w.tiles + w.fixed); }
+// First item number that part number pl walks (0 for whole items: every line has
+// one part), and the line's parts that walk tiles of item number m.
+MLA_HD int64_t window_first_item(const WindowPlan& w, int64_t pl) {
+  return w.whole ? 0 : floordiv(pl * w.per, w.tiles + w.fixed);
+}
 MLA_HD int64_t window_first_part(const WindowPlan& w, int64_t m) {
   return floordiv(m * (w.tiles + w.fixed) + w.fixed, w.per);
 }
@@ -162,22 +165,21 @@ MLA_HD int32_t window_row(const WindowPlan& w, int64_t m, int64_t pl, int32_t la
   return static_cast<int32_t>(2 * (pl * w.lanes + lane) + (window_first_item(w, pl) == m ? 0 : 1));
 }
 
-// split_cost: what a cut costs besides the cost line, in tiles: the extra piece
-// of a part, the fp32 partial rows and the combine.
+// fixed: what a piece costs besides its tiles (query load, epilogue), and
+// merge: what writing partial rows and merging them costs a call, in tiles.
 inline WindowPlan window_plan(int batch, int s_q, int group, int window, int sinks, int parts, bool ragged, int fixed,
-                              int split_cost) {
+                              int merge) {
   WindowPlan w;
   w.group = group;
   w.chunks = (s_q + group - 1) / group;
   w.items = batch * w.chunks;
-  w.parts = parts;
   w.tiles = window_max_tiles(window, sinks, group);
   w.fixed = fixed;
   const int64_t cost = static_cast<int64_t>(w.tiles) + fixed;
   // whole items, dealt round
   const int lines = w.items < parts ? w.items : parts;
   const int64_t whole = (w.items + lines - 1) / lines * cost;
-  w.lanes = lines;
+  w.parts = w.lanes = lines;
   w.per = whole;
   w.whole = true;
   // cut into equal parts; with new_lens many items may be padding, and only
@@ -194,7 +196,18 @@ inline WindowPlan window_plan(int batch, int s_q, int group, int window, int sin
   }
   const int64_t n = parts / best_lanes;
   const int64_t per = ((w.items + best_lanes - 1) / best_lanes * cost + n - 1) / n;
-  if (per + split_cost < whole) {
+  // few items: each into the same number of pieces, a part each
+  const int pieces = parts / w.items < w.tiles ? parts / w.items : w.tiles;
+  const int64_t each = pieces > 1 ? (static_cast<int64_t>(w.tiles) + pieces - 1) / pieces : 0;
+  if (each > 0 && each <= per && each + fixed + merge < whole) {
+    w.parts = parts;
+    w.lanes = 1;
+    w.per = each;
+    w.tiles = static_cast<int32_t>(each * pieces);
+    w.fixed = 0;
+    w.whole = false;
+  } else if (per + fixed + merge < whole) {
+    w.parts = parts;
     w.lanes = best_lanes;
     w.per = per;
     w.whole = false;

@@ -40,7 +40,7 @@ void ends_of(const int* lens, const int* fresh, int s, int b, int j0, int group,
 static WindowPlan plan;
 void make(int batch, int s, int group, int window, int sinks, int parts, int ragged, int fixed, int cut, long long* out) {
   plan = window_plan(batch, s, group, window, sinks, parts, ragged, fixed, cut);
-  out[0] = plan.items; out[1] = plan.tiles; out[2] = plan.lanes; out[3] = plan.per; out[4] = plan.whole; out[5] = plan.chunks;
+  out[0] = plan.items; out[1] = plan.tiles; out[2] = plan.lanes; out[3] = plan.per; out[4] = plan.whole; out[5] = plan.parts;
 }
 // the walk of a part as the kernels do it: (item, t0, t1, cut, workspace block, owner) each
 int walk(int part, const int* item_tiles, int* out) {
@@ -148,8 +148,9 @@ def test_parts_cover_every_tile_once(spans, shape, parts):
     for ragged in (0, 1):
         info = (ctypes.c_longlong * 6)()
         spans.make(batch, s, group, window, sinks, parts, ragged, 5, 8, info)
-        items, tiles, lanes, per, whole, chunks = list(info)
-        assert items == batch * -(-s // group) and tiles == spans.max_tiles(window, sinks, group)
+        items, tiles, lanes, per, whole, used = list(info)
+        assert 1 <= used <= parts and lanes <= used
+        assert items == batch * -(-s // group) and tiles >= spans.max_tiles(window, sinks, group)
         for kind in range(3):
             most = min(tiles, 300)
             n_tiles = np.full(items, tiles if tiles < 300 else 7) if kind == 0 else rng.integers(0, most + 1, items)
@@ -158,7 +159,7 @@ def test_parts_cover_every_tile_once(spans, shape, parts):
             arr = (ctypes.c_int * items)(*n_tiles.tolist())
             covered = {i: [] for i in range(items)}
             blocks, owners = {}, {}
-            for part in range(parts):
+            for part in range(used):
                 out = (ctypes.c_int * (6 * (2 * items + 8)))()
                 for k in range(spans.walk(part, arr, out)):
                     item, t0, t1, cut, block, owner = out[6 * k:6 * k + 6]
@@ -174,7 +175,7 @@ def test_parts_cover_every_tile_once(spans, shape, parts):
             assert all(sorted(covered[i]) == list(range(n_tiles[i])) for i in range(items))
             assert owners == {i: 1 for i in range(items)}
             merged = {}
-            for part in range(parts):
+            for part in range(used):
                 out = (ctypes.c_int * (parts + 2))()
                 item = spans.merge(part, arr, out)
                 if item >= 0:
