@@ -100,7 +100,8 @@ int configure_kernel() {
   std::lock_guard<std::mutex> lock(mu);
   if (state == 0) {
     const cudaError_t e = cudaFuncSetAttribute(
-        mla_splitkv_kernel<kMode, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        mla_splitkv_kernel<kMode, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kWindow ? kSmemBytesWindow : kSmemBytes);
     state = e == cudaSuccess ? 1 : -1;
     if (e != cudaSuccess) return record_cuda_error("cudaFuncSetAttribute(split kernel)", e);
   }
@@ -116,15 +117,18 @@ int launch_split(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const SplitP
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(prm.num_parts * prm.n_hblk, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = kWindow ? kSmemBytesWindow : kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = prm.n_hblk;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  // windowed: the prologue overlaps the previous kernel, whose results it waits for
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = kWindow ? 2 : 1;
   // the FP8 code and scale maps are read only by the FP8 instantiation
   const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_splitkv_kernel<kMode, kWindow>, tm_q, tm_kv,
                                            tm_codes ? *tm_codes : tm_kv,
@@ -163,7 +167,8 @@ int launch_pair(const CUtensorMap& tm_kv, const CUtensorMap& tm_qa, const CUtens
     std::lock_guard<std::mutex> lock(mu);
     if (state == 0) {
       const cudaError_t e = cudaFuncSetAttribute(
-          pair::mla_pair_kernel<kSparse, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize, pair::kSmemBytes);
+          pair::mla_pair_kernel<kSparse, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          kWindow ? pair::kSmemBytesWindow : pair::kSmemBytes);
       state = e == cudaSuccess ? 1 : -1;
       if (e != cudaSuccess) return record_cuda_error("cudaFuncSetAttribute(pair kernel)", e);
     }
@@ -172,7 +177,7 @@ int launch_pair(const CUtensorMap& tm_kv, const CUtensorMap& tm_qa, const CUtens
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(prm.num_parts * 2, 1, 1);
   cfg.blockDim = dim3(kSparse ? pair::kThreadsSparse : pair::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = pair::kSmemBytes;
+  cfg.dynamicSmemBytes = kWindow ? pair::kSmemBytesWindow : pair::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

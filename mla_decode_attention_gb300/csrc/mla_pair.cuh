@@ -134,7 +134,9 @@ static_assert(kBarOffset % 16 == 0, "barrier block alignment");
 static_assert(sizeof(Bars) <= 1024, "barrier block size");
 static_assert(kStage + kXferBytes <= kBarOffset, "score CTA layout");
 static_assert(kXferBytes <= kPBufStride && kXferBytes % 16 == 0, "P transfer size");
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr int kWork = kEpi + 4 * 4096;              // windowed: the list of pieces
+constexpr int kSmemBytesWindow = kSmemBytes + kWorkBytes;
+static_assert(kSmemBytesWindow <= 232448 && kWork % 16 == 0, "shared memory per CTA");
 
 // Sparse: the index list entries of key slots 128 t + 4 lane .. + 3 of
 // sequence q (-1 past its n_slots = topk or topk_length); validated by the caller.
@@ -213,6 +215,11 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
     mbar_init(smem_u32(&bars->o_drained), 1);
     mbar_init(smem_u32(&bars->o_rescaled), 4);
     mbar_init(smem_u32(&bars->v_clean), 4);
+    if constexpr (kWindow) {
+      WorkList* list = reinterpret_cast<WorkList*>(smem + kWork);
+      mbar_init(smem_u32(&list->full), 1);
+      mbar_init(smem_u32(&list->free), 6);  // all roles but the planning row warp
+    }
     bars->abort = 0;
     fence_mbarrier_init();
     if (rank == 1) {  // both P buffers start empty and armed for their first copy
@@ -234,19 +241,14 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
   // whole-sequence schedule is walked) start towards L2 before the wait: a
   // prefetch only warms L2, so rows a preceding kernel is still writing are
   // read for real after the wait all the same.
-  if constexpr (kWindow) {
-    if (rank == 0 && threadIdx.x == 32 * 2) {
-      const WindowPlan& w = p.plan;
-      const int item = part % w.lanes + w.lanes * static_cast<int>(window_first_item(w, part / w.lanes));
-      const int j0 = item % w.chunks * w.group;
-      if (item < w.items)
-        prefetch_l2(p.q + (static_cast<int64_t>(item / w.chunks) * p.s_q + j0) * p.h * kDqk,
-                    min(w.group, p.s_q - j0) * p.h * kDqk * 2);
-    }
-  } else if (rank == 0 && threadIdx.x == 32 * 2 && part < p.batch * p.s_q) {
+  if (!kWindow && rank == 0 && threadIdx.x == 32 * 2 && part < p.batch * p.s_q)
     prefetch_l2(p.q + static_cast<int64_t>(part) * kRows * kDqk, kRows * kDqk * 2);
-  }
-  pdl_wait_primary();
+  // Windowed: the first row warp works out what the part walks (plan_first).
+  constexpr int kPlanWarp = 4;
+  [[maybe_unused]] WorkList* work = reinterpret_cast<WorkList*>(smem + kWork);
+  const int unseen_rows = rank == 1 ? kRows : 0;  // the output CTA writes the rows that see no key
+  if (kWindow && warp == kPlanWarp) plan_first(p, work, part, 0, unseen_rows);
+  else pdl_wait_primary();
   pdl_launch_dependents();  // the combine may launch now; it waits for this grid to finish
   // Schedule B (whole sequences) is walked when it is at most kSplitPenalty
   // tiles longer than A: on b=64, t=4096 (~2.3 us per dense tile) splitting
@@ -282,7 +284,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         constexpr int kIssuers = kSparse ? kKIssuersSparse : 2;
         const int pw = issuer_index(warp);
         const uint64_t pol = l2_policy_evict_first();
-        Pieces<kWindow> pc(p, meta, part);
+        auto pc = role_pieces<kWindow>(p, meta, part, work, false);
         uint32_t tc = 0;
         int32_t issued[kKGroups];  // ring round of this issuer's last load per group slot
         for (int i = 0; i < kKGroups; ++i) issued[i] = -1;
@@ -381,7 +383,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
     } else if (warp == 1) {
       // ---------------------------------------------------- S = Q . K^T
       if (lane == 0) {
-        Pieces<kWindow> pc(p, meta, part);
+        auto pc = role_pieces<kWindow>(p, meta, part, work, false);
         uint32_t tc = 0, item = 0, qtma_n = 0, qcp_n = 0;  // completed phases of q_tma, q_cp
         bool ok = true, q_pending = false;  // q_pending: a query box is in flight
         const uint64_t qpol = l2_policy_evict_first();
@@ -498,7 +500,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       const uint32_t stage = base + kStage;
       const uint32_t prow = stage + (r >> 3) * 1024 + (r & 7) * 128;
       const float sc = p.scale_log2;
-      Pieces<kWindow> pc(p, meta, part);
+      auto pc = role_pieces<kWindow>(p, meta, part, work, true);
+      if constexpr (kWindow) pc.plan_by(warp == kPlanWarp, 0, unseen_rows);
       uint32_t tc = 0, item = 0;
       bool ok = true;
       while (pc.next()) {
@@ -507,9 +510,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         // the piece's query rows come by TMA and tcgen05.cp (QK issuer); the
         // next piece's rows (147 KB, contiguous) start towards L2
         if (r == 0) {
-          Pieces<kWindow> npc = pc;
-          if (npc.next())
-            prefetch_l2(p.q + static_cast<int64_t>(npc.q) * p.h * kDqk, npc.rows() * kDqk * 2);
+          const int nq = pc.peek_q();
+          if (nq >= 0) prefetch_l2(p.q + static_cast<int64_t>(nq) * p.h * kDqk, pc.peek_rows(0, kRows) * kDqk * 2);
         }
         float m_use = 0.f, lsum = 0.f, bsum = 0.f;
         [[maybe_unused]] int32_t end = 0;     // windowed: of row r's token, 0 for padding
@@ -539,21 +541,25 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             for (int k = 0; k < 4; ++k)
               vm[k] = __ballot_sync(0xffffffffu, sid[k] >= 0 && static_cast<int64_t>(sid[k]) < p.s_kv);
           }
+          // Windowed: scores of keys not seen become -inf in TMEM before the
+          // passes read them, and the row max is taken on the way; only the
+          // tiles at the runs' ends have any.
+          [[maybe_unused]] float u_edge = -INFINITY;
+          const bool edge = kWindow && pc.edge(t);
           if constexpr (kWindow) {
-            // Scores of keys not seen become -inf in TMEM before the passes read
-            // them: only the tiles at the runs' ends have any.
-            if (ok && pc.span.edge(t)) {
+            if (ok && edge) {
               tc_fence_after();
 #pragma unroll 1
               for (int i = 0; i < 4; ++i) {
                 const uint32_t m = window_mask32(end, p.window, p.sinks, pc.key_at(t, 32 * i));
-                if (!__any_sync(0xffffffffu, m != ~0u)) continue;
                 float v[32];
                 tmem_ld32(t_s + 32 * i, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = (m >> j) & 1u ? v[j] : -INFINITY;
                 tmem_st32(t_s + 32 * i, v);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) u_edge = fmax3(u_edge, v[j], v[j + 1]);
               }
               tmem_wait_st();
             }
@@ -590,7 +596,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           float alpha = 1.f;
           if (ok && (kWindow ? t == t0 || __any_sync(0xffffffffu, blind) : t == t0)) {
             tc_fence_after();
-            const float u = row_max();
+            const float u = edge ? u_edge * sc : row_max();
             if constexpr (kWindow) {
               if (t == t0 || blind) m_use = u == -INFINITY ? 0.f : u;
               blind = blind && u == -INFINITY;
@@ -719,7 +725,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       if (kSparse && r == 0) bulk_wait_all();  // the last copy has landed in the peer
     } else if (warp == 3 && !kSparse) {
       // ---------------------------------------------------- P transfers (dense)
-      Pieces<kWindow> pc(p, meta, part);
+      auto pc = role_pieces<kWindow>(p, meta, part, work, true);
       uint32_t tc = 0;
       bool ok = true;
       while (pc.next()) {
@@ -759,7 +765,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         constexpr int kIssuers = kSparse ? kVIssuersSparse : 2;
         const int pw = issuer_index(warp);
         const uint64_t pol = l2_policy_evict_first();
-        Pieces<kWindow> pc(p, meta, part);
+        auto pc = role_pieces<kWindow>(p, meta, part, work, false);
         uint32_t tc = 0;
         int32_t issued[kVGroups];
         for (int i = 0; i < kVGroups; ++i) issued[i] = -1;
@@ -826,13 +832,10 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           }
         }
       }
-      if constexpr (kWindow) {
-        if (warp == 2) write_unseen(p, part, 0, kRows, lane, 32);
-      }
     } else if (warp == 1) {
       // ---------------------------------------------------- O += P . V
       if (lane == 0) {
-        Pieces<kWindow> pc(p, meta, part);
+        auto pc = role_pieces<kWindow>(p, meta, part, work, false);
         uint32_t tc = 0, item = 0, rc = 0;
         [[maybe_unused]] uint32_t vc = 0;  // windowed: tiles with keys not seen
         bool ok = true;
@@ -857,7 +860,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             if (!ok) continue;
             tc_fence_after();
             if constexpr (kWindow) {
-              if (pc.span.edge(t)) {  // the row warps have zeroed the rows of keys not seen
+              if (pc.edge(t)) {  // the row warps have zeroed the rows of keys not seen
                 ok = mbar_wait(smem_u32(&bars->v_clean), vc & 1, abort_flag, p.err);
                 ++vc;
                 if (!ok) continue;
@@ -907,7 +910,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       // ---------------------------------------------------- rescale, epilogue
       const int r = threadIdx.x - 128;
       const uint32_t t_o = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16);
-      Pieces<kWindow> pc(p, meta, part);
+      auto pc = role_pieces<kWindow>(p, meta, part, work, true);
+      if constexpr (kWindow) pc.plan_by(warp == kPlanWarp, 0, unseen_rows);
       uint32_t tc = 0, item = 0, rc = 0;
       bool ok = true;
       while (pc.next()) {
@@ -917,7 +921,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           const uint32_t b = tc & 1;
           const uint32_t side = base + kPBuf0 + b * kPBufStride;
           if constexpr (kWindow) {
-            if (pc.span.edge(t)) {
+            if (pc.edge(t)) {
               // The rows of keys not seen become zeros before P.V reads them:
               // their weight 0 times what is there could be NaN.  Thread r =
               // key r of the tile.  The previous tile's P.V is waited for first:
@@ -1064,7 +1068,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
       }
     } else if (warp == 3 && !kSparse) {
       // ---------------------------------------------------- P buffer hand-back
-      Pieces<kWindow> pc(p, meta, part);
+      auto pc = role_pieces<kWindow>(p, meta, part, work, true);
       uint32_t tc = 0;
       bool ok = true;
       while (pc.next()) {

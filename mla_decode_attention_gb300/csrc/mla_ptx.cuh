@@ -93,6 +93,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same without heed of the abort flag, for phases that every role completes
+// whatever became of its other waits.
+__device__ __forceinline__ bool mbar_wait_all_roles(uint32_t bar, uint32_t parity, uint32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > 2 * kWaitTimeoutNs) {
+      if (err) atomicOr(err, MLA_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- fences
 
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -347,6 +361,11 @@ __device__ __forceinline__ void prefetch_l2(const void* gptr, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gptr), "r"(bytes) : "memory");
 }
 
+// Prefetch the cache line of a global address into L2.
+__device__ __forceinline__ void prefetch_line_l2(const void* gptr) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(gptr));
+}
+
 // ------------------------------------------------------------------ misc
 
 // Two float8 e4m3 values (low byte first) -> two exact fp16 values.
@@ -546,6 +565,11 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t code) {
   return __uint_as_float(code << 23);
 }
 
+__device__ __forceinline__ int32_t ld_shared_i32(uint32_t addr) {
+  int32_t v;
+  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");

@@ -60,7 +60,9 @@ constexpr int kSmemSmall = kSmemQ + kChunks * kQChunkBytes;   // 221184
 constexpr int kNumBarriers = 3 * kChunks + 4;
 constexpr int kSmallBytes = 8 * kNumBarriers + 16 + 5 * 4 * 4 * 4 * 16;
 constexpr int kSmemBytes = kSmallBytes + kSmemSmall + 1024;   // + alignment slack
-static_assert(kSmemBytes <= 232448, "dynamic shared memory per CTA");
+constexpr int kSmemWork = (kSmemSmall + kSmallBytes + 15) / 16 * 16;  // windowed: the list of pieces
+constexpr int kSmemBytesWindow = kSmemWork + 2688 + 1024;
+static_assert(kSmemBytesWindow <= 232448, "dynamic shared memory per CTA");
 constexpr int kSoftmaxGroups = 4;                  // warpgroups on the softmax
 constexpr int kRowsPerGroup = kRowsPerCta / kSoftmaxGroups;  // 16 query rows each
 constexpr int kSoftmaxWarp0 = 0;
@@ -160,89 +162,202 @@ struct Pieces {
   __device__ __forceinline__ const int32_t* rec() const { return meta_seq(meta, p.num_parts, q); }
   __device__ __forceinline__ int32_t keys() const { return rec()[kSKeys]; }
   __device__ __forceinline__ int32_t page(int32_t e) const { return e; }
+  __device__ __forceinline__ bool edge(int) const { return false; }
   __device__ __forceinline__ bool whole() const { return rec()[kSNSplits] == 1; }
   __device__ __forceinline__ int64_t split_row() const { return static_cast<int64_t>(rec()[kSSplitOff] + split); }
   __device__ __forceinline__ int rows() const { return p.h; }              // query rows of q
-  __device__ __forceinline__ int rows_from(int) const { return p.rows; }  // and of a CTA's block
+  __device__ __forceinline__ int peek_rows(int, int block) const { return block; }
+  __device__ __forceinline__ int peek_q() const {                         // the next piece's sequence, -1: none
+    PartCursor nc = cur;
+    int nq, nt0, nt1, ns;
+    return next_piece(meta, p.num_parts, &nc, &nq, &nt0, &nt1, &ns) ? nq : -1;
+  }
 };
 
-// By the tokens' positions and the window (mla_window.cuh): q is the first query
-// token of the item (a token of all requests' slots in turn).
+// Windowed: what a part walks, worked out 32 items at a time (lane i of one warp,
+// item i) into shared memory, from which every role reads it.  With the
+// arithmetic in every role the cold start of a short call was bound by fetching
+// seven copies of it.
+struct WorkItem {
+  int32_t q, rows;                                // first query token (of all requests' slots in turn), query rows
+  int32_t t0, t1;                                 // tiles of the piece
+  int32_t row;                                    // block of the split workspace, -1 for an item that is not cut
+  int32_t b, j0;                                  // request, slot of the first token
+  int32_t least, most, first, count;              // WindowEnds
+  int32_t head_pages, skip;                       // page list
+  int32_t edge_head, edge_lo, edge_hi, edge_end;  // tiles with keys not seen
+  int32_t pad[3];
+};
+constexpr int kWorkItems = 32;
+struct WorkList {
+  WorkItem item[kWorkItems];
+  uint64_t full, free;  // a batch is written (one arrival) / every role but the planner's is done with it
+  int64_t m;            // the next batch's first item number on the part's cost line
+  int32_t line, pl;     // the line, and the part's number on it
+  int32_t n, more;      // pieces of the batch; whether another may follow
+};
+constexpr int kWorkBytes = 2688;
+static_assert(sizeof(WorkItem) == 80 && sizeof(WorkList) <= kWorkBytes && kWorkBytes % 128 == 0, "work list");
+
+// Called by a whole warp: the part's next batch of items.  Pieces go into the
+// list; tokens that see no key have none: their rows (row0 .. row0 + most - 1 of
+// the item's) are zeroed here by the part that owns the item.
+__device__ __noinline__ static void plan_batch(const SplitParams& p, WorkList* list, bool commit, int row0, int most) {
+  const WindowPlan& w = p.plan;
+  const int lane = threadIdx.x & 31, line = list->line, pl = list->pl;
+  const int64_t mine = list->m + lane, item = line + w.lanes * mine;
+  const bool in = item < w.items && (w.whole || mine * (w.tiles + w.fixed) < (pl + 1) * w.per);
+  WorkItem x = {};
+  WindowPiece piece = {};
+  if (in) {
+    x.b = static_cast<int32_t>(item) / w.chunks;
+    x.j0 = (static_cast<int32_t>(item) - x.b * w.chunks) * w.group;
+    x.q = x.b * p.s_q + x.j0;
+    x.rows = min(w.group, p.s_q - x.j0) * p.h;
+    const WindowEnds e = window_ends(p.cache_seqlens, p.new_lens, p.s_q, x.b, x.j0, w.group);
+    const WindowSpan span = window_span(e, p.window, p.sinks);
+    piece = window_piece(w, mine, pl, span.tiles);
+    x.row = piece.cut ? window_row(w, mine, pl, line) : -1;
+    x.t0 = piece.t0; x.t1 = piece.t1;
+    x.least = e.least; x.most = e.most; x.first = e.first; x.count = e.count;
+    x.head_pages = span.head_pages; x.skip = span.skip;
+    x.edge_head = span.edge_head; x.edge_lo = span.edge_lo; x.edge_hi = span.edge_hi; x.edge_end = span.edge_end;
+  }
+  const uint32_t has = __ballot_sync(0xffffffffu, x.t0 < x.t1);
+  if (x.t0 < x.t1) list->item[__popc(has & ((1u << lane) - 1u))] = x;
+  const bool more = __all_sync(0xffffffffu, in);
+  __syncwarp();
+  if (lane == 0) {
+    list->n = __popc(has);
+    list->more = more ? 1 : 0;
+    if (commit) {
+      list->m = mine + kWorkItems;
+      mbar_arrive(smem_u32(&list->full));
+    }
+  }
+  __syncwarp();
+  uint32_t none = commit && most > 0 ? __ballot_sync(0xffffffffu, in && x.most == 0 && piece.owner) : 0u;
+  for (; none; none &= none - 1) {
+    const int from = __ffs(none) - 1;
+    const int q = __shfl_sync(0xffffffffu, x.q, from), rows = min(__shfl_sync(0xffffffffu, x.rows, from) - row0, most);
+    const int b = q / p.s_q, j0 = q - b * p.s_q;
+    uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(q) * p.h + row0) * kDv);
+    for (int i = lane; i < rows * kDv / 8; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int r = row0 + lane; r < row0 + rows; r += 32)
+      p.lse[(static_cast<int64_t>(b) * p.h + r % p.h) * p.s_q + j0 + r / p.h] = -INFINITY;
+  }
+}
+
+// Called by the planning warp in place of pdl_wait_primary(): the first batch.
+// What it reads is only final once the preceding kernel is done, but the way
+// there is gone twice, once before the wait: that fetches the code, and starts
+// the first item's query rows, length and page slots towards L2.
+__device__ __forceinline__ void plan_first(const SplitParams& p, WorkList* list, int part, int row0, int most) {
+  const int lane = threadIdx.x & 31;
+  const WindowPlan& w = p.plan;
+  const int line = part % w.lanes, pl = part / w.lanes;
+  const int64_t m = window_first_item(w, pl);
+  if (lane == 0) {
+    list->line = line; list->pl = pl; list->m = m;
+  }
+  __syncwarp();
+  plan_batch(p, list, false, row0, most);
+  const int64_t item = line + w.lanes * m;
+  if (item < w.items) {
+    const int64_t b = item / w.chunks, j0 = (item - b * w.chunks) * w.group;
+    const int rows = min(w.group, p.s_q - static_cast<int>(j0)) * p.h;
+    if (lane == 0) prefetch_l2(p.q + (b * p.s_q + j0) * p.h * p.d_qk, rows * p.d_qk * 2);
+    if (lane == 1) prefetch_line_l2(p.cache_seqlens + b);
+    if (lane == 2 && p.new_lens) prefetch_line_l2(p.new_lens + b);
+    for (int64_t i = 32 * lane; i < p.bt_width && i < 4096; i += 1024) prefetch_line_l2(p.block_table + b * p.bt_stride + i);
+  }
+  __syncwarp();
+  pdl_wait_primary();
+  plan_batch(p, list, true, row0, most);
+}
+
+// The roles' side.
 template <>
 struct Pieces<true> {
   const SplitParams& p;
-  int part, m;                // the next item's number on the part's cost line
+  uint32_t list;   // shared memory address of the WorkList
+  bool warps;      // a role of whole warps (one arrival each), not of one thread
+  bool plans;      // the planning warp's role, and the query rows that it writes for items without a key:
+  int row0, most;
+  int i = 0, n = 0;
+  uint32_t batch = 0;
   int q, t0, t1;
-  WindowEnds ends;
-  WindowSpan span;
-  __device__ __forceinline__ Pieces(const SplitParams& prm, const int32_t*, int part_) : p(prm), part(part_) {
-    m = static_cast<int>(window_first_item(p.plan, part / p.plan.lanes));
+  __device__ __forceinline__ Pieces(const SplitParams& prm, WorkList* l, bool whole_warps)
+      : p(prm), list(smem_u32(l)), warps(whole_warps), plans(false), row0(0), most(0) {}
+  __device__ __forceinline__ void plan_by(bool planner, int first_row, int rows) {
+    plans = planner; row0 = first_row; most = rows;
   }
-  // Moves to the next piece; with kEmpty to the next item that sees no key
-  // instead (these have no piece).
-  template <bool kEmpty = false>
   __device__ __forceinline__ bool next() {
-    const WindowPlan& w = p.plan;
-    const int lane = part % w.lanes, pl = part / w.lanes;
-    for (;;) {
-      const int item = lane + w.lanes * m;
-      if (item >= w.items || m * static_cast<int64_t>(w.tiles + w.fixed) >= (pl + 1) * w.per) return false;
-      const int b = item / w.chunks, j0 = (item - b * w.chunks) * w.group;
-      ends = window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group);
-      span = window_span(ends, p.window, p.sinks);
-      const WindowPiece piece = window_piece(w, m, pl, span.tiles);
-      ++m;
-      q = b * p.s_q + j0;
-      if (kEmpty && span.tiles == 0 && piece.owner) return true;
-      t0 = piece.t0; t1 = piece.t1;
-      if (!kEmpty && t0 < t1) return true;
+    const uint32_t full = list + offsetof(WorkList, full), free = list + offsetof(WorkList, free);
+    while (i == n) {
+      // (Every role comes here whatever became of its waits, so these end.)
+      if (batch > 0) {
+        if (ld_shared_i32(list + offsetof(WorkList, more)) == 0) return false;
+        if (warps) __syncwarp();
+        if (plans) {
+          (void)mbar_wait_all_roles(free, (batch - 1) & 1, p.err);
+          plan_batch(p, reinterpret_cast<WorkList*>(__cvta_shared_to_generic(list)), true, row0, most);
+        } else if (!warps || (threadIdx.x & 31) == 0) {
+          mbar_arrive(free);
+        }
+      }
+      if (!mbar_wait_all_roles(full, batch & 1, p.err)) return false;
+      ++batch;
+      i = 0;
+      n = ld_shared_i32(list + offsetof(WorkList, n));
     }
+    ++i;
+    q = at(offsetof(WorkItem, q)); t0 = at(offsetof(WorkItem, t0)); t1 = at(offsetof(WorkItem, t1));
+    return true;
+  }
+  __device__ __forceinline__ int32_t at(int field) const {  // of the present item
+    return ld_shared_i32(list + (i - 1) * static_cast<int>(sizeof(WorkItem)) + field);
+  }
+  // Query token of the piece after this one, -1 when it is not known.
+  __device__ __forceinline__ int peek_q() const { return i < n ? at(sizeof(WorkItem) + offsetof(WorkItem, q)) : -1; }
+  __device__ __forceinline__ int peek_rows(int row, int block) const {
+    return min(at(sizeof(WorkItem) + offsetof(WorkItem, rows)) - row, block);
   }
   // The end of the token of query row r of the item (0: padding, or a row past
-  // the item's tokens), and whether a token with this end sees key i of tile t.
-  // `span` is computed again: the softmax threads of the one-SM kernel have no
-  // registers to hold it through a tile (they spilled).
+  // the item's tokens).
   __device__ __forceinline__ int32_t end_of_row(int r) const {
-    const int j = r / p.h;
-    return r < rows() ? window_end(p.cache_seqlens, p.new_lens, p.s_q, b(), j0() + j) : 0;
+    if (r >= rows()) return 0;
+    const int j = p.plan.group == 1 ? 0 : r / p.h;
+    const int32_t e = at(offsetof(WorkItem, first)) + j;
+    return j < at(offsetof(WorkItem, count)) && e > 0 ? e : 0;
   }
-  __device__ __forceinline__ int32_t position(int t, int i) const {
-    WindowEnds e = ends;
-    asm volatile("" : "+r"(e.least), "+r"(e.most));  // not to be computed ahead of its use
-    return kPage * window_span(e, p.window, p.sinks).page(2 * t + (i >> 6)) + (i & 63);
+  __device__ __forceinline__ int32_t page(int32_t e) const {
+    return e < at(offsetof(WorkItem, head_pages)) ? e : e + at(offsetof(WorkItem, skip));
   }
-  // The same from `span`: position of key i of tile t.
-  __device__ __forceinline__ int32_t key_at(int t, int i) const { return kPage * span.page(2 * t + (i >> 6)) + (i & 63); }
+  // position of key k of tile t
+  __device__ __forceinline__ int32_t key_at(int t, int k) const { return kPage * page(2 * t + (k >> 6)) + (k & 63); }
+  // Whether tile t may hold a key that one of the item's tokens does not see.
+  __device__ __forceinline__ bool edge(int t) const {
+    return t == at(offsetof(WorkItem, edge_head)) || t >= at(offsetof(WorkItem, edge_end)) ||
+           (t >= at(offsetof(WorkItem, edge_lo)) && t <= at(offsetof(WorkItem, edge_hi)));
+  }
   // Whether any of the item's tokens sees the key at position x.
   __device__ __forceinline__ bool any_sees(int32_t x) const {
-    return x < ends.most && (x < p.sinks || x >= window_lo(ends.least, p.window));
+    return x < keys() && (x < p.sinks || x >= window_lo(at(offsetof(WorkItem, least)), p.window));
   }
-  // query rows of the item that belong to token slots of its request
-  __device__ __forceinline__ int rows() const {
-    return min(p.plan.group, p.s_q - j0()) * p.h;
-  }
-  __device__ __forceinline__ int b() const { return q / p.s_q; }   // request
-  __device__ __forceinline__ int j0() const { return q % p.s_q; }  // and slot of the item's first token
-  __device__ __forceinline__ int rows_from(int row) const { return min(rows() - row, p.rows); }
-  __device__ __forceinline__ int32_t keys() const { return ends.most; }
-  __device__ __forceinline__ int32_t page(int32_t e) const { return span.page(e); }
-  __device__ __forceinline__ bool whole() const { return !window_piece(p.plan, m - 1, part / p.plan.lanes, 1).cut; }
-  __device__ __forceinline__ int64_t split_row() const {
-    return window_row(p.plan, m - 1, part / p.plan.lanes, part % p.plan.lanes);
-  }
+  __device__ __forceinline__ int rows() const { return at(offsetof(WorkItem, rows)); }  // of its request's token slots
+  __device__ __forceinline__ int b() const { return at(offsetof(WorkItem, b)); }
+  __device__ __forceinline__ int j0() const { return at(offsetof(WorkItem, j0)); }
+  __device__ __forceinline__ int32_t keys() const { return at(offsetof(WorkItem, most)); }
+  __device__ __forceinline__ bool whole() const { return at(offsetof(WorkItem, row)) < 0; }
+  __device__ __forceinline__ int64_t split_row() const { return at(offsetof(WorkItem, row)); }
 };
 
-// Windowed: rows row0 .. row0 + most - 1 of the items that see no key and are
-// this part's to write: out = 0, lse = -inf.  Called by threads i = 0 .. n - 1.
-__device__ __forceinline__ void write_unseen(const SplitParams& p, int part, int row0, int most, int i0, int n) {
-  Pieces<true> pc(p, nullptr, part);
-  while (pc.next<true>()) {
-    const int rows = min(pc.rows() - row0, most);
-    uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(pc.q) * p.h + row0) * kDv);
-    for (int i = i0; i < rows * kDv / 8; i += n) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int r = row0 + i0; r < row0 + rows; r += n)
-      p.lse[(static_cast<int64_t>(pc.b()) * p.h + r % p.h) * p.s_q + pc.j0() + r / p.h] = -INFINITY;
-  }
+template <bool kWindow>
+__device__ __forceinline__ Pieces<kWindow> role_pieces(const SplitParams& p, const int32_t* meta, int part,
+                                                       WorkList* work, bool whole_warps) {
+  if constexpr (kWindow) return Pieces<true>(p, work, whole_warps);
+  else return Pieces<false>(p, meta, part);
 }
 
 struct SmemSmall {
@@ -462,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x / p.n_hblk;
   const int hb = blockIdx.x % p.n_hblk;
+  [[maybe_unused]] WorkList* work = reinterpret_cast<WorkList*>(smem + kSmemWork);  // windowed
   // The metadata must describe this call; otherwise nothing is read or written.
   // (A windowed call has no metadata.)
   const bool meta_ok = kWindow || meta_header_matches(p.meta, p.batch, p.s_q, p.num_parts, p.topk, p.causal);
@@ -500,6 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sm->s_full), 1);
     mbar_init(smem_u32(&sm->p_full), 4 * kSoftmaxGroups);  // one arrive per softmax warp
     mbar_init(smem_u32(&sm->o_done), 1);
+    if constexpr (kWindow) {
+      mbar_init(smem_u32(&work->full), 1);
+      mbar_init(smem_u32(&work->free), 4 * kSoftmaxGroups + 1);  // all roles but the planning softmax warp
+    }
     sm->abort = 0;
     fence_mbarrier_init();
     // the first tile's arm of every chunk the peer converts (the MMA thread
@@ -536,6 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm->tmem_base;
   volatile uint32_t* abort_flag = &sm->abort;
 
+  if constexpr (kWindow) {
+    // everything above overlaps the previous kernel of the stream
+    if (warp == kSoftmaxWarp0) plan_first(p, work, part, hb * kRowsPerCta, kRowsPerCta);
+    else pdl_wait_primary();
+    pdl_launch_dependents();  // the merge may launch now; it waits for this grid to finish
+  }
+
   if (!meta_ok) {
     // nothing to do: every role is skipped, the teardown below still runs
   } else if (is_fp8(kMode) && warp == kProducerWarp) {
@@ -550,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int own0 = share ? hb : 0, own_step = share ? 2 : 1;
       const int n_own = (kChunks - 1) / own_step;
       const int n_req = kMode == KvMode::kPagedFp8V41 ? n_own : n_own + 1;  // + the RoPE chunk
-      Pieces<kWindow> pc(p, meta, part);
+      auto pc = role_pieces<kWindow>(p, meta, part, work, false);
       uint32_t tile_ctr = 0, item_ctr = 0;
       bool ok = true;
       const uint64_t pol = l2_policy_evict_first();
@@ -637,15 +764,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++item_ctr;
       }
-    } else if constexpr (kWindow) {
-      write_unseen(p, part, hb * kRowsPerCta, kRowsPerCta, lane - 1, 31);
     }
   } else if (warp == kProducerWarp && kMode == KvMode::kSparseBf16) {
     // ===================================================== producer (gather)
     // Lane L gathers rows 4L..4L+3 of each 128-row tile with one tile::gather4
     // per column chunk; lane 0 owns the barriers.  Invalid slots (-1, out of
     // range, past topk) fetch pool row 0 and are masked by the softmax.
-    Pieces<kWindow> pc(p, meta, part);
+    auto pc = role_pieces<kWindow>(p, meta, part, work, false);
     uint32_t tile_ctr = 0, item_ctr = 0;
     int32_t issued[kChunks];  // tile counter of each slot's latest gather, -1 = none
     for (int c = 0; c < kChunks; ++c) issued[c] = -1;
@@ -706,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint64_t pol_kv = l2_policy_evict_first();
       const uint64_t pol_q = l2_policy_evict_last();
-      Pieces<kWindow> pc(p, meta, part);
+      auto pc = role_pieces<kWindow>(p, meta, part, work, false);
       uint32_t tile_ctr = 0, item_ctr = 0;
       int32_t issued[kChunks];  // tile counter of each slot's latest load, -1 = none
       for (int c = 0; c < kChunks; ++c) issued[c] = -1;
@@ -721,10 +846,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kChunks; ++c)
           tma_load_2d(q_base + c * kQChunkBytes, &tm_q, c * 64, q_row, smem_u32(&sm->q_full), pol_q);
         {  // the next piece's query rows into L2
-          Pieces<kWindow> npc = pc;
-          if (npc.next())
-            prefetch_l2(p.q + (static_cast<int64_t>(npc.q) * p.h + hb * kRowsPerCta) * p.d_qk,
-                        npc.rows_from(hb * kRowsPerCta) * p.d_qk * 2);
+          const int nq = pc.peek_q();
+          if (nq >= 0)
+            prefetch_l2(p.q + (static_cast<int64_t>(nq) * p.h + hb * kRowsPerCta) * p.d_qk,
+                        pc.peek_rows(hb * kRowsPerCta, p.rows) * p.d_qk * 2);
         }
         const int32_t keys = pc.keys();
         const int32_t* bt_row = bt_row_of(p, q);
@@ -765,13 +890,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-    } else if constexpr (kWindow) {
-      write_unseen(p, part, hb * kRowsPerCta, kRowsPerCta, lane - 1, 31);
     }
   } else if (warp == kMmaWarp) {
     // ===================================================== MMA issuer
     if (lane == 0) {
-      Pieces<kWindow> pc(p, meta, part);
+      auto pc = role_pieces<kWindow>(p, meta, part, work, false);
       uint32_t tile_ctr = 0, item_ctr = 0;
       bool ok = true;
       const uint32_t p_base = kv_base + 8 * kChunkBytes;
@@ -861,7 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* red_w = &sm->red_max[g][wq][0];
     float* bc_m = &sm->bcast[g][wq][0];
     float* bc_a = &sm->bcast2[g][wq][0];
-    Pieces<kWindow> pc(p, meta, part);
+    auto pc = role_pieces<kWindow>(p, meta, part, work, true);
+    if constexpr (kWindow) pc.plan_by(warp == kSoftmaxWarp0, hb * kRowsPerCta, kRowsPerCta);
     uint32_t tile_ctr = 0, item_ctr = 0;
     bool ok = true;
     while (ok && pc.next()) {
@@ -882,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // is decided at a barrier, so all 16 warps leave together.
           const int own0 = share ? hb : 0, own_step = share ? 2 : 1;
           [[maybe_unused]] bool seen_dq = true;  // windowed: the same for the key that it converts
-          if constexpr (kWindow) seen_dq = pc.any_sees(pc.position(t, dq_r));
+          if constexpr (kWindow) seen_dq = pc.any_sees(pc.key_at(t, dq_r));
 #pragma unroll 1
           for (int c = own0; c < kChunks - 1; c += own_step) {
             if (lane == 0 && ok) ok = mbar_wait(smem_u32(&sm->raw_full[c]), tile_ctr & 1, abort_flag, p.err);
@@ -913,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the key of this thread's row
         [[maybe_unused]] bool seen = true, seen_any = true;
         if constexpr (kWindow) {
-          const int32_t x = pc.position(t, r);
+          const int32_t x = pc.key_at(t, r);
           // (h is a multiple of 16, so the warpgroup's rows are one token's)
           seen = window_sees(pc.end_of_row(hb * kRowsPerCta + R * g), p.window, p.sinks, x);
           seen_any = pc.any_sees(x);
@@ -1106,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (share) cluster_sync();  // no peer still writes into this CTA's smem
-  pdl_launch_dependents();
+  if (!kWindow) pdl_launch_dependents();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

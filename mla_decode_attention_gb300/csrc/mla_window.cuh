@@ -42,10 +42,11 @@ MLA_HD int32_t window_end(const int32_t* seqlens, const int32_t* new_lens, int s
   return (j >= n || L <= 0 || end < 0) ? 0 : end;
 }
 
-// The ends of the tokens j0 .. j0 + group - 1 that are no padding: the least and
-// the largest (both 0 when there is none).
+// Of the tokens j0 .. j0 + group - 1: the least and the largest end among those
+// that are no padding (both 0 when there is none); token j0 + j has end first + j
+// when j < count and that is positive, else it is padding.
 struct WindowEnds {
-  int32_t least, most;
+  int32_t least, most, first, count;
 };
 MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j0, int group) {
   int32_t n = new_lens ? new_lens[b] : s;
@@ -54,9 +55,11 @@ MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, i
   L = L > kWindowMaxLen ? kWindowMaxLen : L;
   const int32_t last = (j0 + group < n ? j0 + group : n) - 1;  // the last token that is not past the new ones
   WindowEnds e;
+  e.first = L - n + j0 + 1;
+  e.count = last - j0 + 1;
   e.most = L - n + last + 1;
-  e.least = L - n + j0 + 1 > 1 ? L - n + j0 + 1 : 1;
-  if (last < j0 || L <= 0 || e.most <= 0) e.least = e.most = 0;
+  e.least = e.first > 1 ? e.first : 1;
+  if (e.count <= 0 || L <= 0 || e.most <= 0) e.least = e.most = e.count = 0;
   return e;
 }
 

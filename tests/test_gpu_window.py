@@ -129,6 +129,16 @@ def test_a_chunk_of_a_prompt(fmt, h, window, sinks):
     parity(fmt, [170, 150, 131], 133, h, window, sinks, new=[133, 121, 9], seed=6, parts=20)
 
 
+@pytest.mark.parametrize("fmt,h", [(BF16, 128), (BF16, 64), (FP8_656, 64)])
+def test_parts_that_begin_with_padding(fmt, h):
+    """The first item of a part, or of every part, has no token; some parts have
+    nothing to do at all."""
+    parity(fmt, [100, 90, 0, 0, 0, 300], 6, h, 50, 2, new=[0, 6, 6, 6, 0, 1], seed=14, parts=4)
+    parity(fmt, [0, 0, 70], 2, h, 50, 0, new=[0, 1, 2], seed=15)
+    parity(fmt, [0], 1, h, 50, 0, seed=16)
+    parity(fmt, [0, 2000], 1, h, 1500, 1, seed=17)
+
+
 @pytest.mark.parametrize("h", [16, 32, 48, 64])
 @pytest.mark.parametrize("fmt", [BF16, FP8_528])
 def test_long_windows_of_blocks_of_tokens(fmt, h):
