@@ -336,76 +336,23 @@ def mla_combine(metadata: torch.Tensor, batch: int, s_q: int, h_q: int, num_sm_p
 
 # ---------------------------------------------------------------- a step's tokens
 #
-# These calls run in a few microseconds on the GPU, so what is done here before
-# the launch counts: plain comparisons, no tensor or stream objects.
+# These calls run for a few microseconds on the GPU, so their arguments are
+# checked and marshalled by a native module (csrc/step_binding.cpp): same checks,
+# same errors, without the time that they take in Python.
 
-def _launch(name: str, device: int, args: tuple) -> None:
-    """Calls the library with ``device`` current."""
-    fn = getattr(_lib or lib(), name)
-    if device == torch.cuda.current_device():
-        status = fn(*args)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args)
-    if status != 0:
-        raise MlaError(name, status)
+_step = None
 
 
-def _step_stream(stream, device: int) -> int:
-    """Raw handle of ``stream``, or of the device's current stream."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _vector(t: torch.Tensor, dtype, n: int, name: str, device: int) -> int:
-    """Data pointer of a contiguous tensor of n values."""
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on device {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _step_device(t: torch.Tensor) -> int:
-    device = t.get_device()
-    if device < 0 or not t.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    return device
-
-
-def _step_table(block_table: torch.Tensor, batch: int, device: int):
-    """(pointer, entries from row to row, entries of a row)"""
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.get_device() != device:
-        raise ValueError(f"block_table must be an int32 tensor [batch, max_pages] on device {device}")
-    rows, width = block_table.shape
-    row, col = block_table.stride()
-    if rows != batch or (col != 1 and width > 1):
-        raise ValueError(f"block_table must have {batch} rows and unit column stride")
-    return block_table.data_ptr(), row, width
-
-
-def _step_cache(kv_cache: torch.Tensor, kv_format: int, device: int) -> int:
-    """Columns of a query and of a new row for this cache."""
-    form = _FORMATS.get(kv_format)
-    if form is None:
-        raise ValueError(f"unknown kv_format {kv_format}")
-    width = form[1] or 576
-    if kv_cache.dtype != (torch.bfloat16 if kv_format == MLA_KV_BF16 else torch.uint8) or kv_cache.dim() != 3 \
-            or kv_cache.shape[1] != 64 or kv_cache.shape[2] != width or not kv_cache.is_contiguous() \
-            or kv_cache.get_device() != device:
-        raise ValueError(f"kv_format {kv_format} needs a contiguous kv_cache [pages, 64, {width}] of "
-                         f"{'bfloat16' if kv_format == MLA_KV_BF16 else 'uint8'} on device {device}")
-    return form[0]
-
-
-def _step_rope(rope_table: Optional[torch.Tensor], device: int):
-    """(pointer, rows)"""
-    if rope_table is None:
-        return None, 0
-    if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or rope_table.shape[1] != 64 \
-            or not rope_table.is_contiguous() or rope_table.get_device() != device:
-        raise ValueError(f"rope_table must be a contiguous float32 tensor [positions, 64] on device {device}")
-    return rope_table.data_ptr(), rope_table.shape[0]
+def _load_step():
+    """Loads the native module (once).  Raises if it has not been built."""
+    global _step
+    lib()
+    try:
+        from . import _step as module
+    except ImportError as e:
+        raise RuntimeError(f"the step module is missing ({e}): build it with __graft_entry__.build()") from e
+    _step = module
+    return module
 
 
 def mla_append_kv(kv_new: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, block_table: torch.Tensor,
@@ -419,40 +366,10 @@ def mla_append_kv(kv_new: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, 
     (rope_table [positions, 64] float32: 32 cosines, 32 sines).  cache_seqlens
     [b] int32 counts the new tokens; new_lens [b] int32 says how many of the
     s_new slots hold one (all of them when None)."""
-    dev = _step_device(kv_cache)
-    d = _step_cache(kv_cache, kv_format, dev)
-    if kv_new.dtype != torch.bfloat16 or kv_new.dim() != 3 or kv_new.shape[2] != d or kv_new.stride(2) != 1 \
-            or kv_new.get_device() != dev:
-        raise ValueError(f"kv_new must be a bfloat16 tensor [batch, s_new, {d}] with unit column stride on device {dev}")
-    b, s, _ = kv_new.shape
-    request, token, _ = kv_new.stride()
-    if s == 1:
-        token = request if b > 1 else d
-    elif b > 1 and request != s * token:
-        raise ValueError("kv_new's token slots must be evenly spaced over the batch")
-    table, table_rows = _step_rope(rope_table, dev)
-    _launch("mla_append_kv", dev, (
-        kv_new.data_ptr(), token, _vector(cache_seqlens, torch.int32, b, "cache_seqlens", dev),
-        None if new_lens is None else _vector(new_lens, torch.int32, b, "new_lens", dev), b, s, table, table_rows,
-        rope_style, None if norm_weight is None else _vector(norm_weight, torch.float32, 512, "norm_weight", dev),
-        norm_eps, kv_cache.data_ptr(), kv_format, kv_cache.shape[0], *_step_table(block_table, b, dev),
-        None if err is None else _vector(err, torch.int32, 1, "err", dev), _step_stream(stream, dev)))
-
-
-def _head_strides(t: torch.Tensor, name: str):
-    """Strides of a [b, s, h, d] tensor: from token slot to token slot over the
-    whole batch, and from head to head."""
-    if t.dtype != torch.bfloat16 or t.stride(3) != 1:
-        raise ValueError(f"{name} must be a bfloat16 tensor with unit column stride")
-    b, s, h, d = t.shape
-    request, token, head, _ = t.stride()
-    if h == 1:
-        head = d
-    if s == 1:
-        token = request if b > 1 else h * head
-    elif b > 1 and request != s * token:
-        raise ValueError(f"{name}'s token slots must be evenly spaced over the batch")
-    return token, head
+    status = (_step or _load_step()).append_kv(kv_new, kv_cache, kv_format, block_table, cache_seqlens, rope_table,
+                                               rope_style, norm_weight, norm_eps, new_lens, err, stream)
+    if status != 0:
+        raise MlaError("mla_append_kv", status)
 
 
 def mla_query_norm_rope(q: torch.Tensor, out: torch.Tensor, cache_seqlens: torch.Tensor,
@@ -465,19 +382,10 @@ def mla_query_norm_rope(q: torch.Tensor, out: torch.Tensor, cache_seqlens: torch
     tensor of the same shape that does not overlap it).  Rows of padding slots
     stay as they were in out.  cache_seqlens, new_lens, rope_table: as for
     mla_append_kv."""
-    dev = _step_device(q)
-    if q.dim() != 4 or q.shape != out.shape or out.get_device() != dev:
-        raise ValueError(f"q and out must be [batch, s_q, h_q, d] on device {dev}")
-    b, s, h, d = q.shape
-    q_token, q_head = _head_strides(q, "q")
-    out_token, out_head = (q_token, q_head) if out is q else _head_strides(out, "out")
-    table, table_rows = _step_rope(rope_table, dev)
-    _launch("mla_query_norm_rope", dev, (
-        q.data_ptr(), q_token, q_head, _vector(cache_seqlens, torch.int32, b, "cache_seqlens", dev),
-        None if new_lens is None else _vector(new_lens, torch.int32, b, "new_lens", dev), b, s, h, d, table, table_rows,
-        rope_style, None if norm_weight is None else _vector(norm_weight, torch.float32, d, "norm_weight", dev),
-        norm_eps, out.data_ptr(), out_token, out_head, None if err is None else _vector(err, torch.int32, 1, "err", dev),
-        _step_stream(stream, dev)))
+    status = (_step or _load_step()).query_norm_rope(q, out, cache_seqlens, rope_table, rope_style, norm_weight,
+                                                     norm_eps, new_lens, err, stream)
+    if status != 0:
+        raise MlaError("mla_query_norm_rope", status)
 
 
 def mla_window_workspace_size(batch: int, s_q: int, h_q: int, window: int, sinks: int, num_sm_parts: int) -> int:
@@ -499,25 +407,11 @@ def mla_window_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, b
     attn_sink: optional [h] float32.  cache_seqlens, new_lens: as for
     mla_append_kv.  workspace: mla_window_workspace_size() bytes (None when
     that is 0), float32."""
-    dev = _step_device(q)
-    d = _step_cache(kv_cache, kv_format, dev)
-    if q.dtype != torch.bfloat16 or q.dim() != 4 or q.shape[3] != d or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous bfloat16 tensor [batch, s_q, h_q, {d}]")
-    b, s, h, _ = q.shape
-    if workspace is None:
-        ws, ws_bytes = None, 0
-    else:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        if not workspace.is_contiguous() or workspace.get_device() != dev:
-            raise ValueError(f"workspace must be a contiguous tensor on device {dev}")
-    _launch("mla_window_decode", dev, (
-        q.data_ptr(), kv_cache.data_ptr(), kv_format, kv_cache.shape[0], *_step_table(block_table, b, dev),
-        _vector(cache_seqlens, torch.int32, b, "cache_seqlens", dev),
-        None if new_lens is None else _vector(new_lens, torch.int32, b, "new_lens", dev), b, s, h, window, sinks,
-        softmax_scale, None if attn_sink is None else _vector(attn_sink, torch.float32, h, "attn_sink", dev),
-        num_sm_parts, ws, ws_bytes, _vector(out, torch.bfloat16, b * s * h * 512, "out", dev),
-        _vector(lse, torch.float32, b * h * s, "lse", dev), None if err is None else _vector(err, torch.int32, 1, "err", dev),
-        _step_stream(stream, dev)))
+    status = (_step or _load_step()).window_decode(q, kv_cache, kv_format, block_table, cache_seqlens, softmax_scale,
+                                                   window, sinks, num_sm_parts, workspace, out, lse, err, stream,
+                                                   attn_sink, new_lens)
+    if status != 0:
+        raise MlaError("mla_window_decode", status)
 
 
 def mla_check_wait_timeout(err: torch.Tensor, stream=None) -> None:

@@ -1,4 +1,5 @@
-"""Builds the in-tree C-ABI library ``libmla_decode.so`` for sm_103a.
+"""Builds the in-tree C-ABI library ``libmla_decode.so`` for sm_103a, and the
+Python module ``_step`` that marshals the per-step calls.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc, then
 linked into one shared library next to this file.  The build fails when any
@@ -15,6 +16,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -48,6 +50,39 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _step_module() -> str:
+    """File name of the Python module for the step calls."""
+    return "_step" + sysconfig.get_config_var("EXT_SUFFIX")
+
+
+def _compile_step() -> str:
+    """Compiles csrc/step_binding.cpp (host C++ against torch's headers)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    obj = os.path.join(BUILD_DIR, "step_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-c", os.path.join(CSRC, "step_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on step_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_step(obj: str) -> None:
+    """Links it against the library beside it and the installed torch."""
+    import torch
+    out = os.path.join(HERE, _step_module())
+    cmd = ["g++", "-shared", "-o", out + ".tmp", obj, "-L", HERE, "-l:" + LIB_NAME, "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the step module failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+
+
 _ENTRY = re.compile(r"Compiling entry function '([^']+)'")
 _SPILL = re.compile(r"(\d+) bytes spill stores, (\d+) bytes spill loads")
 
@@ -74,7 +109,9 @@ def spill_report(ptxas_log: str) -> list[str]:
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        step = ex.submit(_compile_step)
         results = list(ex.map(_compile, _sources()))
+        step_obj = step.result()
     objs = [o for o, _ in results]
     log = "\n".join(l for _, l in results)
     with open(os.path.join(BUILD_DIR, "ptxas.log"), "w") as f:
@@ -92,6 +129,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    _link_step(step_obj)
     return lib
 
 

@@ -62,9 +62,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   const bool in = tok < p.rope.batch * p.rope.s;
   const int b = in ? tok / p.rope.s : 0, j = in ? tok - b * p.rope.s : 0;
   const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(tok) * p.x_token) + l;
-  uint4 raw[kUnits];  // requested before the position is known
+  uint4 raw[kUnits];
+  auto load = [&](bool real) {
 #pragma unroll
-  for (int k = 0; k < kUnits; ++k) raw[k] = in ? src[kRowLanes * k] : make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < kUnits; ++k) raw[k] = real ? src[kRowLanes * k] : make_uint4(0u, 0u, 0u, 0u);
+  };
+  // requested before the position is known, unless many tokens may be padding
+  if (!p.rope.new_lens) load(in);
   int32_t pos = in ? token_position(p.rope.seqlens, p.rope.new_lens, p.rope.s, b, j) : -1;
   const bool turn = p.rope.table != nullptr;
   int64_t slot = 0;
@@ -80,6 +84,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       pos = -1;
     }
   }
+  if (p.rope.new_lens) load(pos >= 0);
   Turn t = {};
   if (turn && pos >= 0) load_turn(t, p.rope.table, pos, l, p.rope.style);
   float inv = 1.f;
