@@ -67,9 +67,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) raw[k] = real ? src[kRowLanes * k] : make_uint4(0u, 0u, 0u, 0u);
   };
+  pdl_wait_primary();
   // requested before the position is known, unless many tokens may be padding
   if (!p.rope.new_lens) load(in);
-  int32_t pos = in ? token_position(p.rope.seqlens, p.rope.new_lens, p.rope.s, b, j) : -1;
+  int32_t pos = in ? token_position(p.rope.seqlens[b], p.rope.new_lens ? p.rope.new_lens[b] : p.rope.s, p.rope.s, j) : -1;
   const bool turn = p.rope.table != nullptr;
   int64_t slot = 0;
   if (pos >= 0) {
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
     if (pos >= 0 && l == 0) *reinterpret_cast<uint4*>(dst + kV41HeadDim) = make_uint4(codes8[0], codes8[1], codes8[2], codes8[3]);
   }
+  pdl_launch_dependents();
 }
 
 }  // namespace
@@ -210,12 +212,8 @@ extern "C" int mla_append_kv(const void* kv_new, int64_t token_stride, const int
   p.bt_width = max_pages;
   const int per_block = kAppendThreads / kRowLanes;
   const int blocks = (batch * s_new + per_block - 1) / per_block;
-  if (kv_format == MLA_KV_BF16)
-    append_kernel<MLA_KV_BF16><<<blocks, kAppendThreads, 0, stream>>>(p);
-  else if (kv_format == MLA_KV_FP8_656)
-    append_kernel<MLA_KV_FP8_656><<<blocks, kAppendThreads, 0, stream>>>(p);
-  else
-    append_kernel<MLA_KV_FP8_528><<<blocks, kAppendThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? MLA_OK : record_cuda_error("append kernel launch", e);
+  const char* what = "append kernel launch";
+  if (kv_format == MLA_KV_BF16) return launch_step(append_kernel<MLA_KV_BF16>, p, blocks, 1, kAppendThreads, stream, what);
+  if (kv_format == MLA_KV_FP8_656) return launch_step(append_kernel<MLA_KV_FP8_656>, p, blocks, 1, kAppendThreads, stream, what);
+  return launch_step(append_kernel<MLA_KV_FP8_528>, p, blocks, 1, kAppendThreads, stream, what);
 }

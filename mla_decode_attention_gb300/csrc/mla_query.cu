@@ -21,21 +21,23 @@ struct QueryParams {
   const float* weight;
   float eps;
   float inv_d;
-  uint32_t h, tokens;
+  uint32_t h;
   uint32_t groups;          // of heads in a token
 };
 
 // kRows heads per eight lanes, one after the other in a token's heads: short
 // heads alone would leave too few bytes in flight (d = 192, b = 128, two tokens
-// of 128 heads: 6.6 us with one, 5.2 with two).
+// of 128 heads: 6.6 us with one, 5.1 with two).
 template <int kUnits, int kRows>
 __global__ void __launch_bounds__(kQueryThreads) query_kernel(const __grid_constant__ QueryParams p) {
-  const uint32_t group = (blockIdx.x * kQueryThreads + threadIdx.x) / kRowLanes;
-  const int l = threadIdx.x % kRowLanes;
-  const uint32_t tok = group / p.groups, head0 = (group - tok * p.groups) * kRows;
-  const bool in = tok < p.tokens;
-  const int b = in ? static_cast<int>(tok / static_cast<uint32_t>(p.rope.s)) : 0;
-  const int j = in ? static_cast<int>(tok - static_cast<uint32_t>(b) * p.rope.s) : 0;
+  const int b = blockIdx.y, l = threadIdx.x % kRowLanes;
+  pdl_wait_primary();
+  const int32_t L = p.rope.seqlens[b], fresh = p.rope.new_lens ? p.rope.new_lens[b] : p.rope.s;
+  const uint32_t group = (blockIdx.x * kQueryThreads + threadIdx.x) / kRowLanes;  // of the request
+  const int j = static_cast<int>(group / p.groups);
+  const uint32_t head0 = (group - j * p.groups) * kRows;
+  const bool in = j < p.rope.s;
+  const int64_t tok = static_cast<int64_t>(b) * p.rope.s + j;
   const __nv_bfloat16* src = p.q + tok * p.q_token + head0 * p.q_head + 8 * l;
   uint4 raw[kRows][kUnits];
   auto load = [&](bool real) {
@@ -48,7 +50,7 @@ __global__ void __launch_bounds__(kQueryThreads) query_kernel(const __grid_const
   };
   // requested before the position is known, unless many tokens may be padding
   if (!p.rope.new_lens) load(in);
-  int32_t pos = in ? token_position(p.rope.seqlens, p.rope.new_lens, p.rope.s, b, j) : -1;
+  int32_t pos = in ? token_position(L, fresh, p.rope.s, j) : -1;
   const bool turn = p.rope.table != nullptr;
   if (turn && pos >= p.rope.rows) {  // no angles for this position: the rows stay as they were
     if (p.rope.err && l == 0) atomicOr(p.rope.err, MLA_DEVERR_BAD_INDEX);
@@ -103,15 +105,26 @@ __global__ void __launch_bounds__(kQueryThreads) query_kernel(const __grid_const
     for (int r = 0; r < kRows; ++r)
       if (pos >= 0 && head0 + r < p.h) reinterpret_cast<uint4*>(dst + r * p.out_head)[kRowLanes * k] = raw[r][k];
   }
+  pdl_launch_dependents();
 }
 
 template <int kUnits, int kRows>
 int launch_query(QueryParams p, cudaStream_t stream) {
   p.groups = (p.h + kRows - 1) / kRows;
-  const int64_t threads = static_cast<int64_t>(p.tokens) * p.groups * kRowLanes;
-  query_kernel<kUnits, kRows><<<static_cast<uint32_t>((threads + kQueryThreads - 1) / kQueryThreads), kQueryThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? MLA_OK : record_cuda_error("query kernel launch", e);
+  constexpr int64_t per_block = kQueryThreads / kRowLanes;
+  const int64_t blocks = (static_cast<int64_t>(p.rope.s) * p.groups + per_block - 1) / per_block;
+  // a request's tokens along x, requests along y (at most 65535 a launch)
+  for (int b = 0; b < p.rope.batch; b += 65535) {
+    QueryParams part = p;
+    part.rope.seqlens += b;
+    if (part.rope.new_lens) part.rope.new_lens += b;
+    part.q += static_cast<int64_t>(b) * p.rope.s * p.q_token;
+    part.out += static_cast<int64_t>(b) * p.rope.s * p.out_token;
+    const int n = p.rope.batch - b < 65535 ? p.rope.batch - b : 65535;
+    const int rc = launch_step(query_kernel<kUnits, kRows>, part, blocks, n, kQueryThreads, stream, "query kernel launch");
+    if (rc != MLA_OK) return rc;
+  }
+  return MLA_OK;
 }
 
 }  // namespace
@@ -148,7 +161,6 @@ extern "C" int mla_query_norm_rope(const void* q, int64_t q_token_stride, int64_
   p.eps = norm_eps;
   p.inv_d = 1.f / static_cast<float>(d);
   p.h = static_cast<uint32_t>(h_q);
-  p.tokens = static_cast<uint32_t>(batch) * static_cast<uint32_t>(s_q);
   // rotation alone, in place: only the last 64 columns change
   if (norm_eps == 0.f && q == out && q_token_stride == out_token_stride && q_head_stride == out_head_stride) {
     p.q += d - 64;

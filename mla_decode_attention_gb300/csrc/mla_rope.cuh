@@ -30,12 +30,10 @@ struct RopeParams {
   uint32_t* err;
 };
 
-// Position of token slot j of request b, or -1 for padding (slots past
-// new_lens[b], positions before the first).
-__device__ __forceinline__ int32_t token_position(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j) {
-  int32_t n = new_lens ? new_lens[b] : s;
+// Position of token slot j of a request of length L, n of whose s slots hold new
+// tokens, or -1 for padding (slots past those, positions before the first).
+__device__ __forceinline__ int32_t token_position(int32_t L, int32_t n, int s, int j) {
   n = n < 0 ? 0 : (n > s ? s : n);
-  const int32_t L = seqlens[b];
   if (j >= n || L <= 0) return -1;
   const int32_t pos = L - n + j;
   return pos < 0 ? -1 : pos;
@@ -98,6 +96,25 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const Turn& t, int l, int
       x[i] = x[i] * t.c[i] + sign * (other * t.s[i]);
     }
   }
+}
+
+// Launch of a kernel whose blocks may start while the preceding kernel of the
+// stream ends; it waits for that kernel (pdl_wait_primary) before it reads or
+// writes anything.
+template <class Kernel, class Params>
+int launch_step(Kernel kernel, const Params& p, int64_t blocks, int blocks_y, int threads, cudaStream_t stream,
+                const char* what) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(blocks_y), 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e == cudaSuccess ? MLA_OK : record_cuda_error(what, e);
 }
 
 // Host-side checks of the arguments that the two entry points share.
