@@ -915,12 +915,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // toward the next one, before the peer can start its copy
             if (from_peer) mbar_arrive_expect_tx(smem_u32(&sm->full[c]), kChunkBytes);
             tc_fence_after();
+            const uint64_t a = sw128_desc(kv_base + c * kChunkBytes, 16, 1024);
+            const uint64_t bq = sw128_desc(q_base + c * kQChunkBytes, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint64_t a = sw128_desc(kv_base + c * kChunkBytes + 32 * k, 16, 1024);
-              const uint64_t bq = sw128_desc(q_base + c * kQChunkBytes + 32 * k, 16, 1024);
-              mma_bf16_ss(tmem + kTmemS, a, bq, kIdescQK, (c | k) != 0);
-            }
+            for (int k = 0; k < 4; ++k)
+              mma_bf16_ss(tmem + kTmemS, a + static_cast<uint64_t>((32 * k) >> 4), bq + static_cast<uint64_t>((32 * k) >> 4),
+                          kIdescQK, (c | k) != 0);
           }
           if (!ok) break;
           if (t == t1 - 1) mma_commit(smem_u32(&sm->q_empty));
@@ -931,13 +931,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(smem_u32(&sm->p_full), par, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t vd = sw128_desc(kv_base, kChunkBytes, 1024), pd = sw128_desc(p_base, kChunkBytes, 1024);
+#pragma unroll
           for (int m = 0; m < 4; ++m) {
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-              const uint64_t a = sw128_desc(kv_base + 2 * m * kChunkBytes + 2048 * s, kChunkBytes, 1024);
-              const uint64_t bp = sw128_desc(p_base + 2048 * s, kChunkBytes, 1024);
-              mma_bf16_ss(tmem + kTmemO + 64 * m, a, bp, kIdescPV, (t != t0 || s != 0) ? 1u : 0u);
-            }
+            for (int s = 0; s < 8; ++s)
+              mma_bf16_ss(tmem + kTmemO + 64 * m, vd + static_cast<uint64_t>((2 * m * kChunkBytes + 2048 * s) >> 4),
+                          pd + static_cast<uint64_t>((2048 * s) >> 4), kIdescPV, (t != t0 || s != 0) ? 1u : 0u);
             if (share) {  // the slot is written by both CTAs' converters
               mma_commit_multicast(smem_u32(&sm->empty[2 * m]), 0x3);
               mma_commit_multicast(smem_u32(&sm->empty[2 * m + 1]), 0x3);

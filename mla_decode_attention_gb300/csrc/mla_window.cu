@@ -9,18 +9,20 @@ namespace mla {
 
 namespace {
 
-// Merge of the items that were cut, one query row a block at a time,
+// Merge of the items that were cut, per query row
 //   lse = ln sum_i e^lse_i,   out = sum_i e^(lse_i - lse) o_i,
 // over the item's pieces (those that hold no tile were not written and are left
 // out).  A cut item belongs to the part with its first tile, which ends inside
-// it, so a part has at most one.  Thread t owns columns 4t .. 4t + 3; in every
-// warp lane i looks after piece i, so the warps need no barrier.  A row is a few
-// dependent reads and little else: the pieces' rows are requested four at a
-// time, the first four before the weights are known, and there are as many
-// blocks as fit the device at once, no more (a block for every row of every part
-// took 13 to 19 us a call, most of it blocks that found nothing to do).
-constexpr int kMergeThreads = kDv / 4;
-constexpr int kMergeAhead = 4;
+// it, so a part has at most one.  Reads and their latency are all there is, so
+// as many rows as possible are merged at once, a warp each, and a row with many
+// pieces is shared by the eight warps of a block (128 rows of 76 items in two
+// pieces: 18 us with a block per row, 8 rows after one another; 64 rows of 3
+// items in 50 pieces: 19 us with one chain of reads a row).
+constexpr int kMergeWarps = 8;
+constexpr int kMergeThreads = 32 * kMergeWarps;
+// A block shares a row that has more pieces than this, when there are at most
+// this many rows (two blocks an SM; more rows fill the device by themselves).
+constexpr int kMergePieces = 6, kMergeRows = 304;
 
 // Parts that may own a cut item: part k * step for k below the count.
 struct MergeOwners {
@@ -32,10 +34,15 @@ MergeOwners merge_owners(const WindowPlan& w) {
   return {w.parts, 1};
 }
 
-__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const __grid_constant__ SplitParams p,
+// kShare: warps per row, 1 or kMergeWarps.
+template <int kShare>
+__global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __grid_constant__ SplitParams p,
                                                                      int block_rows, int owner_step) {
+  __shared__ float4 s_acc[kShare > 1 ? kMergeWarps : 1][kDv / 4];
+  __shared__ float s_mx[kMergeWarps], s_sum[kMergeWarps];
   const WindowPlan& w = p.plan;
-  const int part = blockIdx.x * owner_step, line = part % w.lanes, pl = part / w.lanes, lane = threadIdx.x & 31;
+  const int part = blockIdx.x * owner_step, line = part % w.lanes, pl = part / w.lanes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = kShare > 1 ? warp : 0;
   const int64_t m = floordiv((pl + 1) * w.per - 1, w.tiles + w.fixed);
   const int64_t item = line + w.lanes * m;
   if (item >= w.items || window_first_part(w, m) != pl) return;
@@ -43,61 +50,100 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const __gri
   if (pieces == 1) return;
   const int b = static_cast<int>(item) / w.chunks, j0 = (static_cast<int>(item) - b * w.chunks) * w.group;
   const int rows = min(w.group, p.s_q - j0) * p.h;
+  pdl_wait_primary();
   const int tiles = window_span(window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group), p.window, p.sinks).tiles;
   if (tiles == 0) return;  // the walking part writes its rows
-  // workspace block of piece i, -1 where it holds no tile
+  // this warp's pieces are share, share + kShare, ...; the block of the
+  // workspace that holds the i-th of them, -1 where it has no tile
+  const int mine = (pieces - share + kShare - 1) / kShare;
   auto block_of = [&](int i) {
-    if (i >= pieces) return -1;
-    const WindowPiece piece = window_piece(w, m, pl + i, tiles);
-    return piece.t0 < piece.t1 ? window_row(w, m, pl + i, line) : -1;
+    if (i >= mine) return -1;
+    const WindowPiece piece = window_piece(w, m, pl + share + i * kShare, tiles);
+    return piece.t0 < piece.t1 ? window_row(w, m, pl + share + i * kShare, line) : -1;
   };
   int block = block_of(lane);
-  pdl_wait_primary();
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+  for (int r = blockIdx.y * (kMergeWarps / kShare) + (kShare > 1 ? 0 : warp); r < rows;
+       r += gridDim.y * (kMergeWarps / kShare)) {
+    // lane l has columns 4 l .. 4 l + 3 of each 128
     float mx = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < pieces; i0 += 32) {
-      if (pieces > 32) block = block_of(i0 + lane);
-      const float l = block >= 0 ? p.ws_lse[static_cast<int64_t>(block) * block_rows + r] : -INFINITY;
-      const int n = min(pieces - i0, 32);
-      auto load = [&](int i, float4 (&v)[kMergeAhead]) {
+    float4 acc[4];
 #pragma unroll
-        for (int k = 0; k < kMergeAhead; ++k) {
-          const int at = __shfl_sync(0xffffffffu, block, (i + k) & 31);
-          v[k] = i + k < n && at >= 0
-                     ? reinterpret_cast<const float4*>(p.ws_o + (static_cast<int64_t>(at) * block_rows + r) * kDv)[threadIdx.x]
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      if (mine > 32) block = block_of(i0 + lane);
+      const float l = block >= 0 ? p.ws_lse[static_cast<int64_t>(block) * block_rows + r] : -INFINITY;
+      const int n = min(mine - i0, 32);
+      auto load = [&](int i, float4 (&v)[4]) {
+        const int at = __shfl_sync(0xffffffffu, block, i & 31);
+        const float4* src = reinterpret_cast<const float4*>(p.ws_o + (static_cast<int64_t>(at) * block_rows + r) * kDv) + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = i < n && at >= 0 ? src[32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
       };
-      float4 v[kMergeAhead];
+      float4 v[4], nv[4];
       load(0, v);
       const float mx_new = fmaxf(mx, warp_max_f32(l));
       const float ref = mx_new == -INFINITY ? 0.f : mx_new;
       const float keep = i0 == 0 ? 0.f : __expf(mx - ref);  // what was summed before, at the new reference
       mx = mx_new;
-      const float e = __expf(l - ref);
+      const float e = __expf(l - ref);  // 0 for a piece that is left out
       float part_sum = e;
 #pragma unroll
       for (int sh = 16; sh > 0; sh >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, sh);
       sum = sum * keep + part_sum;
-      acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
-      for (int i = 0; i < n; i += kMergeAhead) {
-        if (i > 0) load(i, v);
 #pragma unroll
-        for (int k = 0; k < kMergeAhead; ++k) {
-          const float f = __shfl_sync(0xffffffffu, e, (i + k) & 31);  // 0 past the last piece
-          acc.x += f * v[k].x; acc.y += f * v[k].y; acc.z += f * v[k].z; acc.w += f * v[k].w;
+      for (int c = 0; c < 4; ++c) {
+        acc[c].x *= keep; acc[c].y *= keep; acc[c].z *= keep; acc[c].w *= keep;
+      }
+      for (int i = 0; i < n; ++i) {
+        load(i + 1, nv);
+        const float f = __shfl_sync(0xffffffffu, e, i);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[c].x += f * v[c].x; acc[c].y += f * v[c].y; acc[c].z += f * v[c].z; acc[c].w += f * v[c].w;
+          v[c] = nv[c];
         }
       }
     }
-    const float lse = sum > 0.f ? (mx + __logf(sum)) : -INFINITY;
+    if constexpr (kShare > 1) {  // the warps' sums, at the row's reference
+      if (lane == 0) s_mx[warp] = mx;
+      __syncthreads();
+      float top = s_mx[0];
+#pragma unroll
+      for (int i = 1; i < kMergeWarps; ++i) top = fmaxf(top, s_mx[i]);
+      const float f = mx == -INFINITY ? 0.f : __expf(mx - top);
+      if (lane == 0) s_sum[warp] = sum * f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        s_acc[warp][lane + 32 * c] = make_float4(acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f);
+      __syncthreads();
+      mx = top;
+      sum = s_sum[0];
+#pragma unroll
+      for (int i = 1; i < kMergeWarps; ++i) sum += s_sum[i];
+    }
+    const float lse = sum > 0.f ? mx + __logf(sum) : -INFINITY;
     float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int j = j0 + r / p.h, head = r % p.h;
     if (p.attn_sink) inv *= attn_sink_factor(lse, p.attn_sink[head]);
     const int64_t tok = static_cast<int64_t>(b) * p.s_q + j;
-    reinterpret_cast<uint2*>(p.out + (tok * p.h + head) * kDv)[threadIdx.x] =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (threadIdx.x == 0) p.lse[(static_cast<int64_t>(b) * p.h + head) * p.s_q + j] = lse;
+    uint2* dst = reinterpret_cast<uint2*>(p.out + (tok * p.h + head) * kDv);
+    if constexpr (kShare > 1) {
+      if (threadIdx.x < kDv / 4) {
+        float4 v = s_acc[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kMergeWarps; ++i) {
+          const float4 x = s_acc[i][threadIdx.x];
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        dst[threadIdx.x] = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+      }
+      __syncthreads();  // the next row's sums
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        dst[lane + 32 * c] = make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
+    }
+    if (share == 0 && lane == 0) p.lse[(static_cast<int64_t>(b) * p.h + head) * p.s_q + j] = lse;
   }
 }
 
@@ -119,7 +165,7 @@ struct WindowCall {
   WindowPlan plan;
 };
 // fixed cost of a piece and cost of a merge, in tiles
-constexpr int kPairFixed = 5, kPairMerge = 3, kOneFixed = 2, kOneMerge = 2;
+constexpr int kPairFixed = 5, kPairMerge = 6, kOneFixed = 2, kOneMerge = 1;
 
 WindowCall window_call(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts, bool bf16, bool ragged) {
   WindowCall c;
@@ -226,8 +272,11 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
 
   cudaLaunchConfig_t cfg = {};
   const MergeOwners owners = merge_owners(call.plan);
-  const int rows = call.plan.group * h_q, fit = 8 * num_sm_parts * head_blocks(h_q) / owners.count;
-  cfg.gridDim = dim3(owners.count, fit < 1 ? 1 : (fit < rows ? fit : rows), 1);
+  const int64_t pieces = (call.plan.tiles + call.plan.per - 1) / call.plan.per + 1;
+  const int rows = call.plan.group * h_q;
+  const bool shared = pieces > kMergePieces && static_cast<int64_t>(rows) * owners.count <= kMergeRows;
+  const int per_block = shared ? 1 : kMergeWarps;
+  cfg.gridDim = dim3(owners.count, (rows + per_block - 1) / per_block, 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -235,7 +284,7 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, window_merge_kernel, prm, call.block_rows,
-                                           owners.step);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared ? window_merge_kernel<kMergeWarps> : window_merge_kernel<1>, prm,
+                                           call.block_rows, owners.step);
   return e == cudaSuccess ? MLA_OK : record_cuda_error("window merge kernel launch", e);
 }
