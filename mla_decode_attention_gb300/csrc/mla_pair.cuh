@@ -304,9 +304,29 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           }
           q_issued = true;
         };
+        // Windowed: every piece's query rows take that way, as a round of the
+        // ring of their own (`round`: of the next load): short pieces gain more
+        // from four boxes in flight than from keys requested before them.
+        [[maybe_unused]] uint32_t round = 0, q_loads = 0;
+        auto load_q_box = [&](int i, int qq) {
+          const uint32_t bar = smem_u32(&bars->q_box[i]);
+          mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 3 ? kChunk : 0));
+          tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * p.h, 2 * i, bar, pol);
+          if (i == 3) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * p.h, bar, pol);
+        };
         while (pc.next()) {
           const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
-          if (first) {
+          if constexpr (kWindow) {
+            // box i lies in ring slots 2i / 3 .. (2i + 1) / 3
+            for (int g = 0; g < 3 && ok; ++g) {
+              if (round > 0) ok = mbar_wait(smem_u32(&bars->kempty[g]), (round - 1) & 1, abort_flag, p.err);
+              if (!ok) break;
+              load_q_box(g == 0 ? 0 : g + 1, q);
+              if (g == 1) load_q_box(1, q);
+            }
+            ++round;
+            if (ok) ++q_loads;
+          } else if (first) {
             first = false;
             if (pw == 0 && lane == 0) issue_first_q(q);
           }
@@ -339,7 +359,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             }
             if constexpr (!kSparse) {
               for (int g = 0; g < kKGroups && ok; ++g) {
-                ok = mbar_wait(smem_u32(&bars->kempty[g]), tc & 1, abort_flag, p.err);
+                ok = mbar_wait(smem_u32(&bars->kempty[g]), (kWindow ? round - 1 : tc) & 1, abort_flag, p.err);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&bars->kfull[g]);
                 mbar_arrive_expect_tx(bar, kKGroupBytes);
@@ -348,6 +368,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
                   tma_load_4d(base + g * kKGroupBytes + h2 * kGroupPage, &tm_qb, 0, 0, 3 * g, y[h2] / 8, bar, pol);
                 issued[g] = static_cast<int32_t>(tc);
               }
+              if constexpr (kWindow) ++round;
             }
             for (int c = pw; kSparse && c < kChunks && ok; c += kIssuers) {
               const int g = c / 3;
@@ -362,6 +383,13 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               const uint32_t dst = base + slot * kKGroupBytes + (c - 3 * g) * kChunk;
               tma_gather4(dst + 4 * lane * 128, &tm_kv, c * 64, y[0], y[1], y[2], y[3], bar);
               issued[slot] = static_cast<int32_t>(round);
+            }
+          }
+        }
+        if (kWindow && !ok && q_loads > 0) {
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t t_start = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&bars->q_box[i]), (q_loads - 1) & 1) && globaltimer_ns() - t_start < 1000000ull) {
             }
           }
         }
@@ -389,7 +417,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         const uint64_t qpol = l2_policy_evict_first();
         while (pc.next()) {
           const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
-          if (item > 0) {
+          if (!kWindow && item > 0) {
             // a later piece's query rows: the RoPE part into kQRope and the
             // latent part two chunks at a time through the P staging buffer
             // (free once the previous piece's last P copy has read it, which
@@ -420,8 +448,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               ++qcp_n;
             }
           }
-          if (item == 0) {
-            // the first piece's latent Q, TMA-staged in the K ring as [8
+          if (kWindow || item == 0) {
+            // the first piece's latent Q (windowed: every piece's), TMA-staged in the K ring as [8
             // chunks][128 rows][128 B] (128-byte swizzle, four two-chunk
             // boxes), goes into TMEM by tcgen05.cp, one K = 16 step (8
             // columns) per copy, box by box as they land; ring slot g (48 KB
@@ -431,7 +459,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             static_assert(kKGroups == 3 && kKGroupBytes == 3 * kQBoxBytes / 2, "query boxes over the K ring slots");
 #pragma unroll 1
             for (int i = 0; i < 4 && ok; ++i) {
-              ok = mbar_wait(smem_u32(&bars->q_box[i]), 0, abort_flag, p.err);
+              ok = mbar_wait(smem_u32(&bars->q_box[i]), kWindow ? item & 1 : 0, abort_flag, p.err);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
