@@ -299,8 +299,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           for (int i = 0; i < 4; ++i) {
             const uint32_t bar = smem_u32(&bars->q_box[i]);
             mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 0 ? kChunk : 0));
-            if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * p.h, bar, pol);
-            tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * p.h, 2 * i, bar, pol);
+            if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * (kWindow ? p.h : kRows), bar, pol);
+            tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * (kWindow ? p.h : kRows), 2 * i, bar, pol);
           }
           q_issued = true;
         };
@@ -311,8 +311,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         auto load_q_box = [&](int i, int qq) {
           const uint32_t bar = smem_u32(&bars->q_box[i]);
           mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 3 ? kChunk : 0));
-          tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * p.h, 2 * i, bar, pol);
-          if (i == 3) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * p.h, bar, pol);
+          tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * (kWindow ? p.h : kRows), 2 * i, bar, pol);
+          if (i == 3) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * (kWindow ? p.h : kRows), bar, pol);
         };
         while (pc.next()) {
           const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
@@ -428,8 +428,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             for (int i = 0; i < 4 && ok; ++i) {
               const uint32_t bar = smem_u32(&bars->q_tma);
               mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 0 ? kChunk : 0));
-              if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, q * p.h, bar, qpol);
-              tma_load_3d(base + kStage, &tm_ql, 0, q * p.h, 2 * i, bar, qpol);
+              if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, q * (kWindow ? p.h : kRows), bar, qpol);
+              tma_load_3d(base + kStage, &tm_ql, 0, q * (kWindow ? p.h : kRows), 2 * i, bar, qpol);
               q_pending = true;
               ok = mbar_wait(bar, qtma_n & 1, abort_flag, p.err);
               if (!ok) break;
@@ -873,6 +873,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             if (!ok) continue;
             const uint32_t b = tc & 1;
             const uint32_t pbuf = base + kPBuf0 + b * kPBufStride;
+            [[maybe_unused]] const bool edge = kWindow && pc.edge(t);
             ok = mbar_wait_cluster(smem_u32(&bars->p_full[b]), (tc >> 1) & 1, abort_flag, p.err);
             if (!ok) continue;
             if (t == t0) {
@@ -888,7 +889,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             if (!ok) continue;
             tc_fence_after();
             if constexpr (kWindow) {
-              if (pc.edge(t)) {  // the row warps have zeroed the rows of keys not seen
+              if (edge) {  // the row warps have zeroed the rows of keys not seen
                 ok = mbar_wait(smem_u32(&bars->v_clean), vc & 1, abort_flag, p.err);
                 ++vc;
                 if (!ok) continue;
@@ -950,21 +951,29 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           const uint32_t side = base + kPBuf0 + b * kPBufStride;
           if constexpr (kWindow) {
             if (pc.edge(t)) {
-              // The rows of keys not seen become zeros before P.V reads them:
-              // their weight 0 times what is there could be NaN.  Thread r =
-              // key r of the tile.  The previous tile's P.V is waited for first:
-              // without it the V barriers could still be a phase behind, and
-              // their parity would pass for this tile's (P(tc - 1) has come, so
-              // pv_done is at most that one phase behind; and neither can run
-              // ahead, since this tile's P.V waits for these rows).
+              // The rows of keys that no token of the item sees become zeros
+              // before P.V reads them: their weight 0 times what is there could
+              // be NaN.  All row threads take 16 keys at a time, eight threads
+              // for a key's 128-byte chunks (a thread per key left most of them
+              // idle: 256 requests over 128 keys 55 us, 50 so).  The previous
+              // tile's P.V is waited for first: without it the V barriers could
+              // still be a phase behind, and their parity would pass for this
+              // tile's (P(tc - 1) has come, so pv_done is at most that one phase
+              // behind; and neither can run ahead, since this tile's P.V waits
+              // for these rows).
+              uint32_t seen[4];
+              pc.tile_masks(t, seen);
               if (ok && tc > 0) ok = mbar_wait(smem_u32(&bars->pv_done[(tc - 1) & 1]), ((tc - 1) >> 1) & 1, abort_flag, p.err);
               for (int hf = 0; hf < 2; ++hf)
                 if (ok) ok = mbar_wait(smem_u32(&bars->vfull[hf]), tc & 1, abort_flag, p.err);
-              if (ok && !pc.any_sees(pc.key_at(t, r))) {
-                const uint32_t row = base + (r >> 6) * kHalfPage + ((r & 63) >> 3) * 4096 + (r & 7) * 128;
 #pragma unroll 1
-                for (int u = 0; u < 64; ++u)
-                  st_shared_v4(row + (u >> 5) * 2 * kHalfPage + ((u >> 3) & 3) * 1024 + (((u + lane) & 7) << 4), 0u, 0u, 0u, 0u);
+              for (int s = 0; ok && s < 8; ++s) {
+                const int k = 16 * s + (r >> 3);  // key of the tile: page, 8-token group, row
+                const uint32_t word = s < 4 ? (s < 2 ? seen[0] : seen[1]) : (s < 6 ? seen[2] : seen[3]);
+                if ((word >> (k & 31)) & 1u) continue;
+                const uint32_t row = base + (k >> 6) * kHalfPage + ((k & 63) >> 3) * 4096 + (k & 7) * 128 + (r & 7) * 16;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) st_shared_v4(row + (c >> 2) * 2 * kHalfPage + (c & 3) * 1024, 0u, 0u, 0u, 0u);
               }
               fence_proxy_async_smem();
               __syncwarp();

@@ -163,6 +163,7 @@ struct Pieces {
   __device__ __forceinline__ int32_t keys() const { return rec()[kSKeys]; }
   __device__ __forceinline__ int32_t page(int32_t e) const { return e; }
   __device__ __forceinline__ bool edge(int) const { return false; }
+  __device__ __forceinline__ void tile_masks(int, uint32_t (&)[4]) const {}
   __device__ __forceinline__ bool whole() const { return rec()[kSNSplits] == 1; }
   __device__ __forceinline__ int64_t split_row() const { return static_cast<int64_t>(rec()[kSSplitOff] + split); }
   __device__ __forceinline__ int rows() const { return p.h; }              // query rows of q
@@ -340,6 +341,17 @@ struct Pieces<true> {
   __device__ __forceinline__ bool edge(int t) const {
     return t == at(offsetof(WorkItem, edge_head)) || t >= at(offsetof(WorkItem, edge_end)) ||
            (t >= at(offsetof(WorkItem, edge_lo)) && t <= at(offsetof(WorkItem, edge_hi)));
+  }
+  // Bit k % 32 of word k / 32: some token of the item sees key k of tile t.
+  __device__ __forceinline__ void tile_masks(int t, uint32_t (&seen)[4]) const {
+    const int32_t most = keys(), lo = window_lo(at(offsetof(WorkItem, least)), p.window);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int32_t x = kPage * page(2 * t + h);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        seen[2 * h + k] = low_bits(most - x - 32 * k) & (low_bits(p.sinks - x - 32 * k) | ~low_bits(lo - x - 32 * k));
+    }
   }
   // Whether any of the item's tokens sees the key at position x.
   __device__ __forceinline__ bool any_sees(int32_t x) const {
