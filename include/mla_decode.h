@@ -441,7 +441,8 @@ int mla_append_kv(const void* kv_new, int64_t token_stride, const int32_t* cache
  *               (b * s_q + j) * token_stride + h * head_stride elements.
  *               Strides are multiples of 8 and leave heads apart
  *               (head_stride >= d, token_stride >= (h_q - 1) * head_stride + d).
- *               out may be q itself with the same strides; otherwise the two
+ *               out may be q itself with the same strides (others are refused);
+ *               otherwise the two
  *               must not overlap.  With the 576-wide absorbed queries of
  *               mla_decode this is the rotation of columns 512 .. 575; before
  *               absorption d is the head's own width.
@@ -484,7 +485,9 @@ int mla_window_workspace_size(int batch, int s_q, int h_q, int window, int sinks
  *               A bad entry, or one past max_pages, sets
  *               MLA_DEVERR_BAD_PAGE; the outputs of tokens that need it are
  *               then unspecified.
- *  Cache slots that a token does not see may hold anything, NaN included.
+ *  Cache slots that none of the request's tokens of the call sees may hold
+ *  anything, NaN included; what is not finite in a slot that one of them sees
+ *  may reach the outputs of all of them.
  *  Lengths above 2^30 count as 2^30.
  *  attn_sink    optional [h_q] fp32, as for mla_sparse_decode.
  *  num_sm_parts from mla_num_sm_parts (any value >= 1 gives the same result up

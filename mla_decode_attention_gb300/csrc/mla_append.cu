@@ -196,7 +196,8 @@ extern "C" int mla_append_kv(const void* kv_new, int64_t token_stride, const int
   if (num_pages <= 0 || num_pages > (int64_t{1} << 25) || max_pages <= 0 ||
       (batch > 1 && block_table_stride < max_pages))
     return MLA_ERR_SHAPE;
-  if (token_stride < (kv_format == MLA_KV_FP8_528 ? kV41HeadDim : kDqk)) return MLA_ERR_SHAPE;
+  if (token_stride < (kv_format == MLA_KV_FP8_528 ? kV41HeadDim : kDqk) || token_stride > kMaxTokenStride)
+    return MLA_ERR_SHAPE;
   if (!aligned16(kv_new) || !aligned16(kv_cache) || token_stride % 8 != 0) return MLA_ERR_ALIGN;
 
   AppendParams p = {};

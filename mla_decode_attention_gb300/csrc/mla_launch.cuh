@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "mla_decode.h"
@@ -93,26 +94,28 @@ bool make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <KvMode kMode, bool kWindow>
-int configure_kernel() {
-  static int state = 0;  // 0 unset, 1 ok, -1 failed
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lock(mu);
-  if (state == 0) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        mla_splitkv_kernel<kMode, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        kWindow ? kSmemBytesWindow : kSmemBytes);
-    state = e == cudaSuccess ? 1 : -1;
-    if (e != cudaSuccess) return record_cuda_error("cudaFuncSetAttribute(split kernel)", e);
-  }
-  return state == 1 ? MLA_OK : record_error("split kernel configuration failed earlier", MLA_ERR_CUDA);
+// Lets a kernel have `bytes` of dynamic shared memory on the current device,
+// once per device (`done`: a bit per device; past 64 devices, every time).
+template <class Kernel>
+int allow_shared_memory(Kernel kernel, int bytes, std::atomic<uint64_t>* done, const char* what) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return record_cuda_error(what, e);
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (done->load(std::memory_order_acquire) & bit) return MLA_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return record_cuda_error(what, e);
+  done->fetch_or(bit, std::memory_order_release);
+  return MLA_OK;
 }
 
 template <KvMode kMode, bool kWindow = false>
 int launch_split(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const SplitParams& prm,
                  cudaStream_t stream, const CUtensorMap* tm_codes = nullptr,
                  const CUtensorMap* tm_scales = nullptr) {
-  int rc = configure_kernel<kMode, kWindow>();
+  static std::atomic<uint64_t> done{0};  // per instantiation
+  const int rc = allow_shared_memory(mla_splitkv_kernel<kMode, kWindow>, kWindow ? kSmemBytesWindow : kSmemBytes, &done,
+                                     "cudaFuncSetAttribute(split kernel)");
   if (rc != MLA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(prm.num_parts * prm.n_hblk, 1, 1);
@@ -161,19 +164,11 @@ int launch_pair(const CUtensorMap& tm_kv, const CUtensorMap& tm_qa, const CUtens
   const uint64_t q_rows = static_cast<uint64_t>(prm.batch) * prm.s_q * prm.h;
   if (!make_q_latent_map(&tm_ql, prm.q, q_rows) || !make_rows_map(&tm_qr, prm.q, q_rows, kDqk * 2, pair::kRows))
     return record_error("cuTensorMapEncodeTiled failed for the query rows", MLA_ERR_CUDA);
-  static int state = 0;  // 0 unset, 1 ok, -1 failed (per instantiation)
-  static std::mutex mu;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (state == 0) {
-      const cudaError_t e = cudaFuncSetAttribute(
-          pair::mla_pair_kernel<kSparse, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-          kWindow ? pair::kSmemBytesWindow : pair::kSmemBytes);
-      state = e == cudaSuccess ? 1 : -1;
-      if (e != cudaSuccess) return record_cuda_error("cudaFuncSetAttribute(pair kernel)", e);
-    }
-    if (state != 1) return record_error("pair kernel configuration failed earlier", MLA_ERR_CUDA);
-  }
+  static std::atomic<uint64_t> done{0};  // per instantiation
+  const int rc = allow_shared_memory(pair::mla_pair_kernel<kSparse, kWindow>,
+                                     kWindow ? pair::kSmemBytesWindow : pair::kSmemBytes, &done,
+                                     "cudaFuncSetAttribute(pair kernel)");
+  if (rc != MLA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(prm.num_parts * 2, 1, 1);
   cfg.blockDim = dim3(kSparse ? pair::kThreadsSparse : pair::kThreads, 1, 1);

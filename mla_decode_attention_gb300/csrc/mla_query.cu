@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kQueryThreads) query_kernel(const __grid_const
   const int b = blockIdx.y, l = threadIdx.x % kRowLanes;
   pdl_wait_primary();
   const int32_t L = p.rope.seqlens[b], fresh = p.rope.new_lens ? p.rope.new_lens[b] : p.rope.s;
-  const uint32_t group = (blockIdx.x * kQueryThreads + threadIdx.x) / kRowLanes;  // of the request
+  const uint32_t group = blockIdx.x * (kQueryThreads / kRowLanes) + threadIdx.x / kRowLanes;  // of the request
   const int j = static_cast<int>(group / p.groups);
   const uint32_t head0 = (group - j * p.groups) * kRows;
   const bool in = j < p.rope.s;
@@ -127,6 +127,12 @@ int launch_query(QueryParams p, cudaStream_t stream) {
   return MLA_OK;
 }
 
+// Heads of a token, and tokens, may be laid out with gaps but not overlap.
+bool heads_apart(int64_t token, int64_t head, int h, int d) {
+  if (head < d || token < d || token > kMaxTokenStride) return false;
+  return h == 1 || (token - d) / (h - 1) >= head;
+}
+
 }  // namespace
 
 }  // namespace mla
@@ -144,10 +150,10 @@ extern "C" int mla_query_norm_rope(const void* q, int64_t q_token_stride, int64_
   if (h_q <= 0 || d < 64 || d > 576 || d % 64 != 0) return MLA_ERR_SHAPE;
   const int64_t rows = static_cast<int64_t>(batch) * s_q * h_q;
   if (rows > (int64_t{1} << 31) - 1) return MLA_ERR_SHAPE;
-  // heads of a token, and tokens, may be laid out with gaps but not overlap
-  if (q_head_stride < d || out_head_stride < d || q_token_stride < (h_q - 1) * q_head_stride + d ||
-      out_token_stride < (h_q - 1) * out_head_stride + d)
+  if (!heads_apart(q_token_stride, q_head_stride, h_q, d) || !heads_apart(out_token_stride, out_head_stride, h_q, d))
     return MLA_ERR_SHAPE;
+  // in place a head's lanes must read what they themselves overwrite
+  if (q == out && (q_token_stride != out_token_stride || q_head_stride != out_head_stride)) return MLA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(out) || (q_token_stride | q_head_stride | out_token_stride | out_head_stride) % 8 != 0)
     return MLA_ERR_ALIGN;
 

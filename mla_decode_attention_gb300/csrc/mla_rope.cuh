@@ -117,6 +117,10 @@ int launch_step(Kernel kernel, const Params& p, int64_t blocks, int blocks_y, in
   return e == cudaSuccess ? MLA_OK : record_cuda_error(what, e);
 }
 
+// Elements from one token slot to the next that the entry points accept: more
+// than the device's memory holds, and 2^24 times it fits 64 bits.
+constexpr int64_t kMaxTokenStride = int64_t{1} << 38;
+
 // Host-side checks of the arguments that the two entry points share.
 inline int check_rope_args(const void* seqlens, int batch, int s, const float* table, int64_t rows, int style,
                            const float* norm_weight, float norm_eps) {

@@ -40,6 +40,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __
                                                                      int block_rows, int owner_step) {
   __shared__ float4 s_acc[kShare > 1 ? kMergeWarps : 1][kDv / 4];
   __shared__ float s_mx[kMergeWarps], s_sum[kMergeWarps];
+  // first of all: a grid whose blocks all had nothing to merge would otherwise
+  // be over before the attention kernel is, and let the kernel after it start
+  pdl_wait_primary();
   const WindowPlan& w = p.plan;
   const int part = blockIdx.x * owner_step, line = part % w.lanes, pl = part / w.lanes;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = kShare > 1 ? warp : 0;
@@ -50,7 +53,6 @@ __global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __
   if (pieces == 1) return;
   const int b = static_cast<int>(item) / w.chunks, j0 = (static_cast<int>(item) - b * w.chunks) * w.group;
   const int rows = min(w.group, p.s_q - j0) * p.h;
-  pdl_wait_primary();
   const int tiles = window_span(window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group), p.window, p.sinks).tiles;
   if (tiles == 0) return;  // the walking part writes its rows
   // this warp's pieces are share, share + kShare, ...; the block of the

@@ -37,7 +37,7 @@ MLA_HD int32_t window_end(const int32_t* seqlens, const int32_t* new_lens, int s
   int32_t n = new_lens ? new_lens[b] : s;
   n = n < 0 ? 0 : (n > s ? s : n);
   int32_t L = seqlens[b];
-  L = L > kWindowMaxLen ? kWindowMaxLen : L;
+  L = L > kWindowMaxLen ? kWindowMaxLen : (L < 0 ? 0 : L);
   const int32_t end = L - n + j + 1;
   return (j >= n || L <= 0 || end < 0) ? 0 : end;
 }
@@ -52,7 +52,7 @@ MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, i
   int32_t n = new_lens ? new_lens[b] : s;
   n = n < 0 ? 0 : (n > s ? s : n);
   int32_t L = seqlens[b];
-  L = L > kWindowMaxLen ? kWindowMaxLen : L;
+  L = L > kWindowMaxLen ? kWindowMaxLen : (L < 0 ? 0 : L);
   const int32_t last = (j0 + group < n ? j0 + group : n) - 1;  // the last token that is not past the new ones
   WindowEnds e;
   e.first = L - n + j0 + 1;

@@ -145,6 +145,13 @@ def test_offsets_past_32_bits():
     assert float(q[1:-1].float().abs().sum()) == 0
 
 
+def test_more_requests_than_one_launch_takes():
+    b = 65535 + 700
+    lens = [1 + i % 90 for i in range(b)]
+    c = case(lens, 1, 2, 64, new=[0 if i % 5 == 0 else 1 for i in range(b)], seed=9)
+    check(c, run(c), torch.full(c["q"].shape, 7.0, dtype=torch.bfloat16))
+
+
 def test_binding_refusals():
     c = case([10, 10], 2, 4, 192, seed=6)
     q, sl = c["q"].to(DEV), c["lens"].to(DEV)

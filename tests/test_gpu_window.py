@@ -139,6 +139,74 @@ def test_parts_that_begin_with_padding(fmt, h):
     parity(fmt, [0, 2000], 1, h, 1500, 1, seed=17)
 
 
+@pytest.mark.parametrize("fmt,h,s", [(BF16, 128, 75), (BF16, 16, 290), (BF16, 48, 150), (BF16, 64, 1), (FP8_656, 128, 75), (FP8_528, 32, 150)])
+@pytest.mark.parametrize("parts", [1, 2])
+def test_parts_that_walk_many_items(fmt, h, s, parts):
+    """More items a part than are planned at a time, a good part of them without
+    a token."""
+    if s > 1:
+        parity(fmt, [s + 40, s - 7], s, h, 70, 5, new=[s, s - 20], seed=21, parts=parts)
+    else:
+        parity(fmt, [(37 * i) % 260 for i in range(150)], 1, h, 70, 5, new=[i % 3 for i in range(150)], seed=22, parts=parts)
+
+
+@pytest.mark.parametrize("fmt,h", [(BF16, 128), (FP8_656, 64)])
+def test_parts_that_walk_many_items_and_cut_the_last(fmt, h):
+    assert binding.mla_window_workspace_size(52, 3, h, 1000, 3, 5) > 0
+    parity(fmt, [300 + 16 * i for i in range(52)], 3, h, 1000, 3, seed=23, parts=5)
+
+
+@pytest.mark.parametrize("fmt,h,first", [(BF16, 128, 58250), (BF16, 16, 58250), (FP8_656, 64, 102295), (FP8_528, 32, 127095)])
+def test_pages_past_32_bits(fmt, h, first):
+    """The request's pages lie on either side of 2^32 bytes."""
+    c = case(fmt, [300, 500], 2, h, 200, 70, seed=24)
+    ref = run(c)
+    n = c["cache"].shape[0]
+    big = torch.empty(first + n, *c["cache"].shape[1:], dtype=c["cache"].dtype, device=DEV)
+    assert big.numel() * big.element_size() > 2 ** 32 > first * big[0].numel() * big.element_size()
+    big[first:] = c["cache"].to(DEV)
+    c["table"] = torch.where(c["table"] < 0, c["table"], c["table"] + first)
+    c["cache"] = big
+    out, lse = run(c)
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("fmt,h", [(BF16, 128), (FP8_656, 16)])
+def test_two_captured_calls_with_cut_items_run_side_by_side(fmt, h):
+    """Two graphs, a workspace each, replayed at once on two streams; the
+    lengths are written between replays."""
+    cases = [case(fmt, [2200, 70, 900], 1, h, 1500, 200, seed=25 + i) for i in range(2)]
+    sides = []
+    for c in cases:
+        buf = binding.WindowBuffers(3, 1, h, 1500, 200, DEV)
+        assert buf.workspace is not None
+        gpu = [c[k].to(DEV) for k in ("q", "cache", "table", "lens")]
+        call = lambda buf=buf, a=gpu: binding.mla_window_decode(  # noqa: E731
+            a[0], a[1], fmt, a[2], a[3], SCALE, 1500, 200, buf.num_sm_parts, buf.workspace, buf.out, buf.lse, buf.err)
+        call()
+        stream = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            call()
+            call()
+        sides.append((buf, gpu[3], stream, graph))
+    for lens in ([2200, 70, 900], [0, 70, 900], [2200, 1, 0]):
+        for buf, sl, _, _ in sides:
+            sl.copy_(torch.tensor(lens, dtype=torch.int32))
+            buf.out.fill_(9.0)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for _, _, stream, graph in sides:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for c, (buf, _, _, _) in zip(cases, sides):
+            c["lens"] = torch.tensor(lens, dtype=torch.int32)
+            assert int(buf.err.item()) == 0
+            check(c, buf.out.cpu(), buf.lse.cpu())
+
+
 @pytest.mark.parametrize("h", [16, 32, 48, 64])
 @pytest.mark.parametrize("fmt", [BF16, FP8_528])
 def test_long_windows_of_blocks_of_tokens(fmt, h):

@@ -39,7 +39,7 @@ def call(name, base, over):
     (dict(table=None), -2), (dict(rows=-1), -2), (dict(eps=0.0), -2), (dict(eps=-1.0), -2), (dict(eps=NAN), -2),
     (dict(eps=float("inf")), -2), (dict(pages=0), -2), (dict(pages=(1 << 25) + 1), -2), (dict(width=0), -2),
     (dict(bts=3), -2), (dict(stride=568), -2), (dict(stride=580), -3), (dict(x=0x10008), -3), (dict(cache=0x50004), -3),
-    (dict(table=0x30004), -3), (dict(w=0x40008), -3), (dict(style=2), -6), (dict(fmt=3), -6),
+    (dict(table=0x30004), -3), (dict(w=0x40008), -3), (dict(style=2), -6), (dict(fmt=3), -6), (dict(stride=1 << 40), -2),
 ])
 def test_append_refuses(over, code):
     assert call("mla_append_kv", APPEND, over) == code
@@ -50,7 +50,8 @@ def test_append_refuses(over, code):
     (dict(d=32), -2), (dict(d=96), -2), (dict(d=640, qh=640, oh=640, qt=1280, ot=1280), -2), (dict(b=1 << 20, s=16, h=128), -2),
     (dict(qh=504), -2), (dict(oh=0), -2), (dict(qt=1016), -2), (dict(ot=512), -2), (dict(eps=0.0), -2),
     (dict(rows=0), -2), (dict(q=0x10002), -3), (dict(out=0x50008), -3), (dict(qt=1028), -3), (dict(oh=516, ot=1032), -3),
-    (dict(style=-1), -6),
+    (dict(style=-1), -6), (dict(out=0x10000, ot=2048), -2), (dict(out=0x10000, oh=520, ot=1040, qt=1040), -2),
+    (dict(qt=1 << 62), -2), (dict(qh=1 << 62), -2), (dict(h=1 << 20, oh=1 << 44, ot=1 << 38), -2),
 ])
 def test_query_refuses(over, code):
     assert call("mla_query_norm_rope", QUERY, over) == code
