@@ -4,13 +4,18 @@
 //
 // Bound by memory: every head is read once and written once.  Eight lanes own
 // a head and hold all of it in registers (d / 64 units of 16 bytes a lane), so
-// the norm's sum is three shuffles and no column is read twice.
+// the norm's sum is three shuffles and no column is read twice.  2048 tokens of
+// 128 heads: 512 columns normed 83 us = 6.5 TB/s (95 % of the copy rate), 576
+// columns rotated alone, out of place, 88 us = 6.9 TB/s.  A decode step of 64
+// tokens of 128 x 576 takes 2.9 us, its bytes at the copy rate 2.8.
 #include "mla_rope.cuh"
 
 namespace mla {
 
 namespace {
 
+// Small blocks, so that one's loads overlap its neighbours' sums (3000 tokens of
+// 64 x 512: 61.5 us; 65 with 256 threads, 79 with 512).
 constexpr int kQueryThreads = 128;
 
 struct QueryParams {
@@ -27,7 +32,7 @@ struct QueryParams {
 
 // kRows heads per eight lanes, one after the other in a token's heads: short
 // heads alone would leave too few bytes in flight (d = 192, b = 128, two tokens
-// of 128 heads: 6.6 us with one, 5.1 with two).
+// of 128 heads: 6.6 us with one, 5.2 with two, 4.5 with the requests along y).
 template <int kUnits, int kRows>
 __global__ void __launch_bounds__(kQueryThreads) query_kernel(const __grid_constant__ QueryParams p) {
   const int b = blockIdx.y, l = threadIdx.x % kRowLanes;

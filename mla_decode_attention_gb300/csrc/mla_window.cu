@@ -166,7 +166,15 @@ struct WindowCall {
   int block_rows;  // query rows of a block = rows of a workspace block
   WindowPlan plan;
 };
-// fixed cost of a piece and cost of a merge, in tiles
+// Fixed cost of a piece, and cost of a merge to the call, in tiles, from sweeps of
+// both (us, cut by this rule / never cut):
+//   two-SM kernel   128 requests x 2 tokens x 128 heads over 4096   284 / 295
+//                   85 requests of 128 heads over 8192  267 / 298;  160 x 128 over 8192  465 / 534
+//                   10 x 128 over 2000  30 / 43
+//   one-SM kernel   200 requests of 64 heads over 4096  233 / 307;  160 x 64 over 2000
+//                   112 / 164;  656-byte cache, 100 x 128 over 2000  174 / 226
+// and where a merge at 3 tiles would have cut and lost: 100 requests of 128 heads
+// over 1000 keys 72 to 80 cut, 66 whole.
 constexpr int kPairFixed = 5, kPairMerge = 6, kOneFixed = 2, kOneMerge = 1;
 
 WindowCall window_call(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts, bool bf16, bool ragged) {

@@ -12,6 +12,12 @@
 // window's first page.  Keys of a tile that a token does not see are masked by
 // position.
 //
+// What a call costs beyond its bytes and products is this: a part begins cold
+// (code, query rows and first keys: 64 tokens of 128 heads over 128 keys take 18
+// us, their bytes 4), and every piece has a cost of its own (its query rows in,
+// its output rows out).  So pieces are few and large, and nothing runs before
+// the kernel that walks them.
+//
 // No schedule is built on the device: an item has at most `tiles` tiles, so the
 // cost line of all items is known without their lengths.  Each item takes
 // fixed + tiles cost units on it, a part walks the units [part * per, (part + 1)

@@ -1,8 +1,8 @@
 // Python module `_step`: argument checks and marshalling of the calls that a
 // serving loop makes for every layer and step (mla_append_kv,
 // mla_query_norm_rope, mla_window_decode).  They run for a few microseconds on
-// the GPU, and the same checks written in Python took longer than that (9 to 10
-// us a call in all on the Grace host, 5 to 6 so).  Each function returns the
+// the GPU, and the same checks written in Python took longer than that (9 to 12
+// us a call in all on the Grace host, 3 so).  Each function returns the
 // status of the C function of the same name; a wrong tensor raises ValueError
 // before anything is launched.
 #include <Python.h>
