@@ -13,16 +13,19 @@ namespace {
 //   lse = ln sum_i e^lse_i,   out = sum_i e^(lse_i - lse) o_i,
 // over the item's pieces (those that hold no tile were not written and are left
 // out).  A cut item belongs to the part with its first tile, which ends inside
-// it, so a part has at most one.  Reads and their latency are all there is, so
-// as many rows as possible are merged at once, a warp each, and a row with many
-// pieces is shared by the eight warps of a block (128 rows of 76 items in two
-// pieces: 18 us with a block per row, 8 rows after one another; 64 rows of 3
-// items in 50 pieces: 19 us with one chain of reads a row).
+// it, so a part has at most one.  All there is to it is the latency of reads from
+// L2, so the blocks are one wave, what does not hang on the lengths is worked out
+// before the attention kernel ends, a warp reads kMergeBatch pieces of a row at
+// once, and rows of many pieces are shared by two to eight warps.  (us a call; the
+// same without a merge; with as many blocks as rows ask for, a warp or a whole
+// block a row: 3 requests of 128 heads over 8192 keys of the 528-byte cache 34 /
+// 29 / 41, 48 of 64 heads over 1000 of the 656-byte cache 36 / 31 / 40, 10 of 128
+// heads over 2000 28 / 24 / 31, two tokens of 128 requests over 4096 280 / 265 /
+// 286.  Three pieces at once: 29 instead of 28 at 10 requests; four waves: 33.)
 constexpr int kMergeWarps = 8;
 constexpr int kMergeThreads = 32 * kMergeWarps;
-// A block shares a row that has more pieces than this, when there are at most
-// this many rows (two blocks an SM; more rows fill the device by themselves).
-constexpr int kMergePieces = 6, kMergeRows = 304;
+constexpr int kMergeBatch = 2;
+constexpr int kMergeBlocksPerSm = 2;
 
 // Parts that may own a cut item: part k * step for k below the count.
 struct MergeOwners {
@@ -34,25 +37,30 @@ MergeOwners merge_owners(const WindowPlan& w) {
   return {w.parts, 1};
 }
 
-// kShare: warps per row, 1 or kMergeWarps.
+// kShare: warps per row.
 template <int kShare>
-__global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __grid_constant__ SplitParams p,
-                                                                     int block_rows, int owner_step) {
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocksPerSm)
+    window_merge_kernel(const __grid_constant__ SplitParams p, int block_rows, int owner_step) {
+  constexpr int kBlockRows = kMergeWarps / kShare;
   __shared__ float4 s_acc[kShare > 1 ? kMergeWarps : 1][kDv / 4];
   __shared__ float s_mx[kMergeWarps], s_sum[kMergeWarps];
-  // first of all: a grid whose blocks all had nothing to merge would otherwise
-  // be over before the attention kernel is, and let the kernel after it start
-  pdl_wait_primary();
   const WindowPlan& w = p.plan;
   const int part = blockIdx.x * owner_step, line = part % w.lanes, pl = part / w.lanes;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = kShare > 1 ? warp : 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % kShare;
   const int64_t m = floordiv((pl + 1) * w.per - 1, w.tiles + w.fixed);
   const int64_t item = line + w.lanes * m;
-  if (item >= w.items || window_first_part(w, m) != pl) return;
   const int pieces = static_cast<int>(window_last_part(w, m) - pl) + 1;
-  if (pieces == 1) return;
+  const bool owner = item < w.items && window_first_part(w, m) == pl && pieces > 1;
   const int b = static_cast<int>(item) / w.chunks, j0 = (static_cast<int>(item) - b * w.chunks) * w.group;
   const int rows = min(w.group, p.s_q - j0) * p.h;
+  const int first = window_row(w, m, pl, line);  // block of the first piece; the others begin their parts
+  // Waited for whether or not there is anything to merge: a grid whose blocks all
+  // had nothing to do would otherwise be over before the attention kernel is, and
+  // let the kernel after it start.  That one may begin now and waits for this
+  // grid (1.5 to 3 us a call between back-to-back calls).
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (!owner) return;
   const int tiles = window_span(window_ends(p.cache_seqlens, p.new_lens, p.s_q, b, j0, w.group), p.window, p.sinks).tiles;
   if (tiles == 0) return;  // the walking part writes its rows
   // this warp's pieces are share, share + kShare, ...; the block of the
@@ -60,12 +68,17 @@ __global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __
   const int mine = (pieces - share + kShare - 1) / kShare;
   auto block_of = [&](int i) {
     if (i >= mine) return -1;
-    const WindowPiece piece = window_piece(w, m, pl + share + i * kShare, tiles);
-    return piece.t0 < piece.t1 ? window_row(w, m, pl + share + i * kShare, line) : -1;
+    const int at = share + i * kShare;
+    if (tiles != w.tiles) {
+      const WindowPiece piece = window_piece(w, m, pl + at, tiles);
+      if (piece.t0 >= piece.t1) return -1;
+    }
+    return at == 0 ? first : 2 * ((pl + at) * w.lanes + line);
   };
   int block = block_of(lane);
-  for (int r = blockIdx.y * (kMergeWarps / kShare) + (kShare > 1 ? 0 : warp); r < rows;
-       r += gridDim.y * (kMergeWarps / kShare)) {
+  for (int r0 = blockIdx.y * kBlockRows; r0 < rows; r0 += gridDim.y * kBlockRows) {
+    const int r = r0 + warp / kShare;
+    const bool in = r < rows;
     // lane l has columns 4 l .. 4 l + 3 of each 128
     float mx = -INFINITY, sum = 0.f;
     float4 acc[4];
@@ -73,16 +86,20 @@ __global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __
     for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < mine; i0 += 32) {
       if (mine > 32) block = block_of(i0 + lane);
-      const float l = block >= 0 ? p.ws_lse[static_cast<int64_t>(block) * block_rows + r] : -INFINITY;
+      const float l = in && block >= 0 ? p.ws_lse[static_cast<int64_t>(block) * block_rows + r] : -INFINITY;
       const int n = min(mine - i0, 32);
-      auto load = [&](int i, float4 (&v)[4]) {
-        const int at = __shfl_sync(0xffffffffu, block, i & 31);
-        const float4* src = reinterpret_cast<const float4*>(p.ws_o + (static_cast<int64_t>(at) * block_rows + r) * kDv) + lane;
+      float4 v[kMergeBatch][4];
+      auto load = [&](int i) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = i < n && at >= 0 ? src[32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < kMergeBatch; ++k) {
+          const int at = __shfl_sync(0xffffffffu, block, (i + k) & 31);
+          const bool real = in && i + k < n && at >= 0;
+          const float4* src = reinterpret_cast<const float4*>(p.ws_o + (static_cast<int64_t>(at) * block_rows + r) * kDv) + lane;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[k][c] = real ? src[32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       };
-      float4 v[4], nv[4];
-      load(0, v);
+      load(0);
       const float mx_new = fmaxf(mx, warp_max_f32(l));
       const float ref = mx_new == -INFINITY ? 0.f : mx_new;
       const float keep = i0 == 0 ? 0.f : __expf(mx - ref);  // what was summed before, at the new reference
@@ -96,22 +113,25 @@ __global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __
       for (int c = 0; c < 4; ++c) {
         acc[c].x *= keep; acc[c].y *= keep; acc[c].z *= keep; acc[c].w *= keep;
       }
-      for (int i = 0; i < n; ++i) {
-        load(i + 1, nv);
-        const float f = __shfl_sync(0xffffffffu, e, i);
+      for (int i = 0; i < n; i += kMergeBatch) {
+        if (i > 0) load(i);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          acc[c].x += f * v[c].x; acc[c].y += f * v[c].y; acc[c].z += f * v[c].z; acc[c].w += f * v[c].w;
-          v[c] = nv[c];
+        for (int k = 0; k < kMergeBatch; ++k) {
+          const float f = i + k < n ? __shfl_sync(0xffffffffu, e, (i + k) & 31) : 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            acc[c].x += f * v[k][c].x; acc[c].y += f * v[k][c].y; acc[c].z += f * v[k][c].z; acc[c].w += f * v[k][c].w;
+          }
         }
       }
     }
-    if constexpr (kShare > 1) {  // the warps' sums, at the row's reference
+    if constexpr (kShare > 1) {  // the row's warps' sums, at the row's reference
       if (lane == 0) s_mx[warp] = mx;
       __syncthreads();
-      float top = s_mx[0];
+      const int w0 = warp - share;
+      float top = s_mx[w0];
 #pragma unroll
-      for (int i = 1; i < kMergeWarps; ++i) top = fmaxf(top, s_mx[i]);
+      for (int i = 1; i < kShare; ++i) top = fmaxf(top, s_mx[w0 + i]);
       const float f = mx == -INFINITY ? 0.f : __expf(mx - top);
       if (lane == 0) s_sum[warp] = sum * f;
 #pragma unroll
@@ -119,33 +139,33 @@ __global__ void __launch_bounds__(kMergeThreads, 2) window_merge_kernel(const __
         s_acc[warp][lane + 32 * c] = make_float4(acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f);
       __syncthreads();
       mx = top;
-      sum = s_sum[0];
+      sum = s_sum[w0];
 #pragma unroll
-      for (int i = 1; i < kMergeWarps; ++i) sum += s_sum[i];
+      for (int i = 1; i < kShare; ++i) sum += s_sum[w0 + i];
     }
     const float lse = sum > 0.f ? mx + __logf(sum) : -INFINITY;
     float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int j = j0 + r / p.h, head = r % p.h;
-    if (p.attn_sink) inv *= attn_sink_factor(lse, p.attn_sink[head]);
+    if (p.attn_sink && in) inv *= attn_sink_factor(lse, p.attn_sink[head]);
     const int64_t tok = static_cast<int64_t>(b) * p.s_q + j;
     uint2* dst = reinterpret_cast<uint2*>(p.out + (tok * p.h + head) * kDv);
     if constexpr (kShare > 1) {
-      if (threadIdx.x < kDv / 4) {
-        float4 v = s_acc[0][threadIdx.x];
+      for (int c = 32 * share + lane; c < kDv / 4 && in; c += 32 * kShare) {
+        float4 v = s_acc[warp - share][c];
 #pragma unroll
-        for (int i = 1; i < kMergeWarps; ++i) {
-          const float4 x = s_acc[i][threadIdx.x];
+        for (int i = 1; i < kShare; ++i) {
+          const float4 x = s_acc[warp - share + i][c];
           v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
         }
-        dst[threadIdx.x] = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+        dst[c] = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
       }
       __syncthreads();  // the next row's sums
-    } else {
+    } else if (in) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         dst[lane + 32 * c] = make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
     }
-    if (share == 0 && lane == 0) p.lse[(static_cast<int64_t>(b) * p.h + head) * p.s_q + j] = lse;
+    if (in && share == 0 && lane == 0) p.lse[(static_cast<int64_t>(b) * p.h + head) * p.s_q + j] = lse;
   }
 }
 
@@ -168,13 +188,13 @@ struct WindowCall {
 };
 // Fixed cost of a piece, and cost of a merge to the call, in tiles, from sweeps of
 // both (us, cut by this rule / never cut):
-//   two-SM kernel   128 requests x 2 tokens x 128 heads over 4096   284 / 295
+//   two-SM kernel   128 requests x 2 tokens x 128 heads over 4096   280 / 295
 //                   85 requests of 128 heads over 8192  267 / 298;  160 x 128 over 8192  465 / 534
-//                   10 x 128 over 2000  30 / 43
-//   one-SM kernel   200 requests of 64 heads over 4096  233 / 307;  160 x 64 over 2000
-//                   112 / 164;  656-byte cache, 100 x 128 over 2000  174 / 226
-// and where a merge at 3 tiles would have cut and lost: 100 requests of 128 heads
-// over 1000 keys 72 to 80 cut, 66 whole.
+//                   10 x 128 over 2000  28 / 43
+//   one-SM kernel   200 requests of 64 heads over 4096  226 / 307;  160 x 64 over 2000
+//                   104 / 164;  656-byte cache, 100 x 128 over 2000  168 / 226
+// and where a merge at 4 tiles would have cut and lost: 90 requests of 128 heads
+// over 1000 keys 60 cut, 54 whole.
 constexpr int kPairFixed = 5, kPairMerge = 6, kOneFixed = 2, kOneMerge = 1;
 
 WindowCall window_call(int batch, int s_q, int h_q, int window, int sinks, int num_sm_parts, bool bf16, bool ragged) {
@@ -282,11 +302,17 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
 
   cudaLaunchConfig_t cfg = {};
   const MergeOwners owners = merge_owners(call.plan);
-  const int64_t pieces = (call.plan.tiles + call.plan.per - 1) / call.plan.per + 1;
+  const int64_t pieces = owners.step > 1 ? owners.step : (call.plan.tiles + call.plan.per - 1) / call.plan.per + 1;
   const int rows = call.plan.group * h_q;
-  const bool shared = pieces > kMergePieces && static_cast<int64_t>(rows) * owners.count <= kMergeRows;
-  const int per_block = shared ? 1 : kMergeWarps;
-  cfg.gridDim = dim3(owners.count, (rows + per_block - 1) / per_block, 1);
+  const int64_t blocks = static_cast<int64_t>(kMergeBlocksPerSm) * num_sm_parts * head_blocks(h_q);  // one wave
+  // as many warps a row as one batch of pieces each takes, while there are any
+  int share = 1;
+  while (share < kMergeWarps && share * kMergeBatch < pieces &&
+         2 * share * static_cast<int64_t>(rows) * owners.count <= blocks * kMergeWarps)
+    share *= 2;
+  const int64_t lines = (static_cast<int64_t>(rows) * share + kMergeWarps - 1) / kMergeWarps;
+  const int64_t fit = blocks / owners.count;
+  cfg.gridDim = dim3(owners.count, static_cast<unsigned>(lines < fit ? lines : (fit > 1 ? fit : 1)), 1);
   cfg.blockDim = dim3(kMergeThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -294,7 +320,10 @@ extern "C" int mla_window_decode(const void* q, const void* kv_cache, int kv_for
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared ? window_merge_kernel<kMergeWarps> : window_merge_kernel<1>, prm,
-                                           call.block_rows, owners.step);
+  auto* kernel = share == 1   ? window_merge_kernel<1>
+                 : share == 2 ? window_merge_kernel<2>
+                 : share == 4 ? window_merge_kernel<4>
+                              : window_merge_kernel<8>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, prm, call.block_rows, owners.step);
   return e == cudaSuccess ? MLA_OK : record_cuda_error("window merge kernel launch", e);
 }
