@@ -39,11 +39,11 @@
 // Windowed attention (kWindow, mla_window.cuh) runs the same loop over pieces
 // that one warp works out, with several tokens of a request in the 64 rows when
 // heads are few.  64 heads: 150 requests over 4000 keys take 155 us from the bf16
-// cache (4.6 TB/s, 67 % of the copy rate) and 233 us from the 656-byte cache:
+// cache (4.6 TB/s, 67 % of the copy rate) and 224 us from the 656-byte cache:
 // there a tile's chain bounds it - slots free, codes arrive, eight chunks
-// converted, scores, softmax, P.V - at 7.2 us a tile, of which the conversion's
-// arithmetic is 1.2 (left out: 196 us).  Rejected: two or four chunks converted
-// between barriers (229 and 260 us; two head blocks 575 -> 612 and 685), a scale
+// converted, scores, softmax, P.V - at 7.0 us a tile, of which the conversion's
+// arithmetic is 1.2.  Rejected (from 233 us): two or four chunks converted
+// between barriers (229 and 260 us; two head blocks 575 -> 612 and 685), scales
 // fetched once a tile (239), output rows in 16-byte pieces by lane exchanges
 // (64 requests over 128 keys 17.4 -> 18.9 us).
 #pragma once
@@ -777,6 +777,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t slot = kv_base + c * kChunkBytes;
               bulk_copy_to_peer(mapa_shared(slot, hb ^ 1), slot, kChunkBytes,
                                 mapa_shared(fbar, hb ^ 1));
+            }
+          }
+          if (t + 1 < t1 && (!share || hb == 0)) {
+            // the next tile's pages into L2, behind this tile's own requests (150
+            // requests of 64 heads over 4000 keys: 233 us, 224 so; before them a
+            // piece of three tiles lost 5 %)
+            constexpr int kPageBytes = kPage * (kMode == KvMode::kPagedFp8V41 ? kFp8V41TokenBytes : kFp8TokenBytes);
+            for (int h2 = 0; h2 < 2; ++h2) {
+              const int32_t nb = page_of(p, bt_row, keys, pc.page(2 * t + 2 + h2));
+              if (nb >= 0) prefetch_l2(p.kv_fp8 + static_cast<int64_t>(nb) * kPageBytes, kPageBytes);
             }
           }
           while (ok && issued < n_req) {  // the RoPE chunk, if still due
