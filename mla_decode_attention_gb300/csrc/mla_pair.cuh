@@ -49,7 +49,10 @@
 // the key ring, scores of keys not seen masked in TMEM on the tiles that have
 // any.  Two tokens of 128 requests over 4096 keys: 279 us = 1.06 PFLOP/s, the
 // dense kernel's rate.  Short windows are bound by what a piece costs besides its
-// tiles: 64 requests over 128 keys 18 us, 256 requests 50.
+// tiles: 64 requests over 128 keys 18 us, 256 requests 50; the output CTA's
+// chain is the longer one (unseen rows zeroed, P.V, the second tile's V in, P.V,
+// rows out).  Only the 8-key groups that hold a seen key loaded, by boxes of their
+// own: 51 for 50, and 106 for 83 over 4096 keys.
 //
 // Waits are bounded (mbar_wait*); after an abort every role keeps walking its
 // schedule without waiting, so the named barriers between warps 4..8 stay
@@ -365,6 +368,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               }
             }
             if constexpr (!kSparse) {
+#pragma unroll 1  // (unrolled, its code gets in the other roles' way: 304 requests over 500 keys 87 us, 85 so)
               for (int g = 0; g < kKGroups && ok; ++g) {
                 ok = mbar_wait(smem_u32(&bars->kempty[g]), (kWindow ? round - 1 : tc) & 1, abort_flag, p.err);
                 if (!ok) break;
@@ -831,6 +835,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               }
             }
             if constexpr (!kSparse) {
+#pragma unroll 1
               for (int hf = 0; hf < 2 && ok; ++hf) {
                 ok = mbar_wait(smem_u32(&bars->vempty[hf]), (tc & 1) ^ 1, abort_flag, p.err);
                 if (!ok) break;
