@@ -38,10 +38,10 @@
 //
 // Windowed attention (kWindow, mla_window.cuh) runs the same loop over pieces
 // that one warp works out, with several tokens of a request in the 64 rows when
-// heads are few.  64 heads: 150 requests over 4000 keys take 155 us from the bf16
-// cache (4.6 TB/s, 67 % of the copy rate) and 224 us from the 656-byte cache:
+// heads are few.  64 heads: 150 requests over 4000 keys take 149 us from the bf16
+// cache (4.8 TB/s, 70 % of the copy rate) and 221 us from the 656-byte cache:
 // there a tile's chain bounds it - slots free, codes arrive, eight chunks
-// converted, scores, softmax, P.V - at 7.0 us a tile, of which the conversion's
+// converted, scores, softmax, P.V - at 6.9 us a tile, of which the conversion's
 // arithmetic is 1.2.  Rejected (from 233 us): two or four chunks converted
 // between barriers (229 and 260 us; two head blocks 575 -> 612 and 685), scales
 // fetched once a tile (239), output rows in 16-byte pieces by lane exchanges
@@ -938,6 +938,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = t0; t < t1 && ok; ++t) {
           const uint32_t par = tile_ctr & 1;
           // S^T = K_tile . Q^T: A = tile chunk (K-major), B = Q chunk (K-major)
+          // (unrolled as far as registers go, with constant descriptor offsets: bf16, 150
+          // requests of 64 heads over 4000 keys 156 us rolled, 149 so; 656-byte cache, 100
+          // x 2 tokens of 128 heads 563 and 535, every other chunk being the peer's)
+          constexpr int kUnrollQk = is_fp8(kMode) ? 2 : kQk;
+#pragma unroll kUnrollQk
           for (int c = 0; c < kQk; ++c) {
             // FP8 chunks converted by the peer complete on its bulk copy
             const bool from_peer = share && c < kChunks - 1 && (c & 1) != hb;
@@ -1040,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int own0 = share ? hb : 0, own_step = share ? 2 : 1;
           [[maybe_unused]] bool seen_dq = true;  // windowed: the same for the key that it converts
           if constexpr (kWindow) seen_dq = pc.any_sees(pc.key_at(t, dq_r));
-#pragma unroll 1
+#pragma unroll 2
           for (int c = own0; c < kChunks - 1; c += own_step) {
             if (lane == 0 && ok) ok = mbar_wait(smem_u32(&sm->raw_full[c]), tile_ctr & 1, abort_flag, p.err);
             ok = __shfl_sync(0xffffffffu, ok, 0);
