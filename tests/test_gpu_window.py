@@ -171,6 +171,28 @@ def test_pages_past_32_bits(fmt, h, first):
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
 
 
+@pytest.mark.parametrize("fmt,h", [(BF16, 128), (BF16, 32), (FP8_528, 64)])
+def test_more_parts_than_the_device_has(fmt, h):
+    parity(fmt, [1500, 70, 900], 3, h, 1100, 40, seed=26, logits=True, parts=300)
+
+
+@pytest.mark.parametrize("h,value", [(128, float("inf")), (64, float("-inf")), (16, torch.finfo(torch.bfloat16).min)])
+def test_infinities_and_lowest_values_in_unseen_slots(h, value):
+    c = case(BF16, [200, 64, 700, 131], 2, h, 100, 3, new=[2, 1, 2, 2], seed=27)
+    c["cache"][~c["live"]] = value
+    check(c, *run(c))
+
+
+def test_queries_of_padding_may_hold_anything():
+    for fmt, h in ((BF16, 128), (BF16, 16), (FP8_656, 48)):
+        c = case(fmt, [200, 64, 700], 5, h, 100, 3, new=[2, 0, 5], seed=28)
+        ref = run(c)
+        for b, n in enumerate(c["new"].tolist()):
+            c["q"][b, n:] = float("nan")
+        out, lse = run(c)
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
 @pytest.mark.parametrize("fmt,h", [(BF16, 128), (FP8_656, 16)])
 def test_two_captured_calls_with_cut_items_run_side_by_side(fmt, h):
     """Two graphs, a workspace each, replayed at once on two streams; the
