@@ -49,10 +49,10 @@
 // the key ring, scores of keys not seen masked in TMEM on the tiles that have
 // any.  Two tokens of 128 requests over 4096 keys: 279 us = 1.06 PFLOP/s, the
 // dense kernel's rate.  Short windows are bound by what a piece costs besides its
-// tiles: 64 requests over 128 keys 18 us, 256 requests 50; the output CTA's
+// tiles: 64 requests over 128 keys 18 us, 256 requests 47; the output CTA's
 // chain is the longer one (unseen rows zeroed, P.V, the second tile's V in, P.V,
 // rows out).  Only the 8-key groups that hold a seen key loaded, by boxes of their
-// own: 51 for 50, and 106 for 83 over 4096 keys.
+// own: slower (51 for 50, and 106 for 83 over 4096 keys).
 //
 // Waits are bounded (mbar_wait*); after an abort every role keeps walking its
 // schedule without waiting, so the named barriers between warps 4..8 stay
@@ -129,7 +129,7 @@ struct Bars {
   uint64_t p_full[2];                              // output CTA, completed by bulk copies
   uint64_t pv_done[2], o_full, o_free, o_drained, o_rescaled;  // output CTA
   uint64_t side_read[2];                           // output CTA: row threads read P's side data
-  uint64_t v_clean;                                // output CTA, windowed: rows of keys not seen are zero
+  uint64_t v_clean[2];                             // output CTA, windowed: rows of keys not seen are zero
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -224,7 +224,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
     mbar_init(smem_u32(&bars->o_free), 4);
     mbar_init(smem_u32(&bars->o_drained), 1);
     mbar_init(smem_u32(&bars->o_rescaled), 4);
-    mbar_init(smem_u32(&bars->v_clean), 4);
+    mbar_init(smem_u32(&bars->v_clean[0]), 4);
+    mbar_init(smem_u32(&bars->v_clean[1]), 4);
     if constexpr (kWindow) {
       WorkList* list = reinterpret_cast<WorkList*>(smem + kWork);
       mbar_init(smem_u32(&list->full), 1);
@@ -900,20 +901,14 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             }
             if (!ok) continue;
             tc_fence_after();
-            if constexpr (kWindow) {
-              if (edge) {  // the row warps have zeroed the rows of keys not seen
-                ok = mbar_wait(smem_u32(&bars->v_clean), vc & 1, abort_flag, p.err);
-                ++vc;
-                if (!ok) continue;
-                tc_fence_after();
-              }
-            }
             const uint64_t pdesc = sw128_desc(pbuf, 16, 1024);
             if constexpr (!kSparse) {
               // paged: V half hf (N = 256: 64-column blocks 1 KB apart, 8-token
               // groups 4 KB apart) into O columns 256 hf ..
               for (int hf = 0; hf < 2 && ok; ++hf) {
                 ok = mbar_wait(smem_u32(&bars->vfull[hf]), tc & 1, abort_flag, p.err);
+                if (kWindow && edge && ok)  // the row warps have zeroed the rows of keys not seen
+                  ok = mbar_wait(smem_u32(&bars->v_clean[hf]), vc & 1, abort_flag, p.err);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vdesc = sw128_desc(base + hf * 2 * kHalfPage, 1024, 4096);
@@ -925,6 +920,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
                               (t != t0 || s != 0) ? 1u : 0u);
                 mma_commit(smem_u32(&bars->vempty[hf]));
               }
+              if (edge) ++vc;
             }
             for (int qd = 0; kSparse && qd < 4 && ok; ++qd) {
               const uint32_t gv = 4 * tc + qd, slot = gv % kVGroups;
@@ -967,7 +963,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               // before P.V reads them: their weight 0 times what is there could
               // be NaN.  All row threads take 16 keys at a time, eight threads
               // for a key's 128-byte chunks (a thread per key left most of them
-              // idle: 256 requests over 128 keys 55 us, 50 so).  The previous
+              // idle: 256 requests over 128 keys 55 us, 50 so), a V half at a time, so
+              // that P.V begins with the first while the second arrives (47).  The previous
               // tile's P.V is waited for first: without it the V barriers could
               // still be a phase behind, and their parity would pass for this
               // tile's (P(tc - 1) has come, so pv_done is at most that one phase
@@ -976,20 +973,22 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               uint32_t seen[4];
               pc.tile_masks(t, seen);
               if (ok && tc > 0) ok = mbar_wait(smem_u32(&bars->pv_done[(tc - 1) & 1]), ((tc - 1) >> 1) & 1, abort_flag, p.err);
-              for (int hf = 0; hf < 2; ++hf)
-                if (ok) ok = mbar_wait(smem_u32(&bars->vfull[hf]), tc & 1, abort_flag, p.err);
 #pragma unroll 1
-              for (int s = 0; ok && s < 8; ++s) {
-                const int k = 16 * s + (r >> 3);  // key of the tile: page, 8-token group, row
-                const uint32_t word = s < 4 ? (s < 2 ? seen[0] : seen[1]) : (s < 6 ? seen[2] : seen[3]);
-                if ((word >> (k & 31)) & 1u) continue;
-                const uint32_t row = base + (k >> 6) * kHalfPage + ((k & 63) >> 3) * 4096 + (k & 7) * 128 + (r & 7) * 16;
+              for (int hf = 0; hf < 2; ++hf) {  // the first V half while the second arrives
+                if (ok) ok = mbar_wait(smem_u32(&bars->vfull[hf]), tc & 1, abort_flag, p.err);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) st_shared_v4(row + (c >> 2) * 2 * kHalfPage + (c & 3) * 1024, 0u, 0u, 0u, 0u);
+                for (int s = 0; s < 8; ++s) {
+                  const int k = 16 * s + (r >> 3);  // key of the tile: page, 8-token group, row
+                  if (!ok || (seen[s >> 1] >> (k & 31)) & 1u) continue;
+                  const uint32_t row = base + hf * 2 * kHalfPage + (k >> 6) * kHalfPage + ((k & 63) >> 3) * 4096 +
+                                       (k & 7) * 128 + (r & 7) * 16;
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) st_shared_v4(row + c * 1024, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->v_clean[hf]));
               }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&bars->v_clean));
             }
           }
           if (ok) ok = mbar_wait_cluster(smem_u32(&bars->p_full[b]), (tc >> 1) & 1, abort_flag, p.err);
