@@ -213,7 +213,9 @@ static_assert(sizeof(WorkItem) == 80 && sizeof(WorkList) <= kWorkBytes && kWorkB
 
 // Called by a whole warp: the part's next batch of items.  Pieces go into the
 // list; tokens that see no key have none: their rows (row0 .. row0 + most - 1 of
-// the item's) are zeroed here by the part that owns the item.
+// the item's) are zeroed here by the part that owns the item.  Without `commit`
+// it goes the same way with a length of its own making, reads nothing that the
+// preceding kernel may still be writing, and leaves nothing that counts.
 __device__ __noinline__ static void plan_batch(const SplitParams& p, WorkList* list, bool commit, int row0, int most) {
   const WindowPlan& w = p.plan;
   const int lane = threadIdx.x & 31, line = list->line, pl = list->pl;
@@ -226,7 +228,8 @@ __device__ __noinline__ static void plan_batch(const SplitParams& p, WorkList* l
     x.j0 = (static_cast<int32_t>(item) - x.b * w.chunks) * w.group;
     x.q = x.b * p.s_q + x.j0;
     x.rows = min(w.group, p.s_q - x.j0) * p.h;
-    const WindowEnds e = window_ends(p.cache_seqlens, p.new_lens, p.s_q, x.b, x.j0, w.group);
+    const RequestLengths len = request_lengths(p.cache_seqlens, p.new_lens, p.s_q, x.b, commit);
+    const WindowEnds e = item_ends(len.L, len.n, p.s_q, x.j0, w.group);
     const WindowSpan span = window_span(e, p.window, p.sinks);
     piece = window_piece(w, mine, pl, span.tiles);
     x.row = piece.cut ? window_row(w, mine, pl, line) : -1;
@@ -261,9 +264,10 @@ __device__ __noinline__ static void plan_batch(const SplitParams& p, WorkList* l
 }
 
 // Called by the planning warp in place of pdl_wait_primary(): the first batch.
-// What it reads is only final once the preceding kernel is done, but the way
-// there is gone twice, once before the wait: that fetches the code, and starts
-// the first item's query rows, length and page slots towards L2.
+// The lengths are only final once the preceding kernel is done, so they are not
+// read before the wait; but the way there is gone twice, once before it with a
+// made-up length: that fetches the code.  The first item's query rows, length
+// and page slots start towards L2 (a prefetch reads nothing).
 __device__ __forceinline__ void plan_first(const SplitParams& p, WorkList* list, int part, int row0, int most) {
   const int lane = threadIdx.x & 31;
   const WindowPlan& w = p.plan;

@@ -54,10 +54,9 @@ MLA_HD int32_t window_end(const int32_t* seqlens, const int32_t* new_lens, int s
 struct WindowEnds {
   int32_t least, most, first, count;
 };
-MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j0, int group) {
-  int32_t n = new_lens ? new_lens[b] : s;
+// Of a request of length L, n of whose s slots hold new tokens.
+MLA_HD WindowEnds item_ends(int32_t L, int32_t n, int s, int j0, int group) {
   n = n < 0 ? 0 : (n > s ? s : n);
-  int32_t L = seqlens[b];
   L = L > kWindowMaxLen ? kWindowMaxLen : (L < 0 ? 0 : L);
   const int32_t last = (j0 + group < n ? j0 + group : n) - 1;  // the last token that is not past the new ones
   WindowEnds e;
@@ -67,6 +66,24 @@ MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, i
   e.least = e.first > 1 ? e.first : 1;
   if (e.count <= 0 || L <= 0 || e.most <= 0) e.least = e.most = e.count = 0;
   return e;
+}
+MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j0, int group) {
+  return item_ends(seqlens[b], new_lens ? new_lens[b] : s, s, j0, group);
+}
+
+// Length of request b and how many of its s slots hold new tokens, read past L1;
+// with `read` false made up, and nothing is read.
+struct RequestLengths {
+  int32_t L, n;
+};
+constexpr int32_t kDryLength = 1 << 20;
+MLA_HD RequestLengths request_lengths(const int32_t* seqlens, const int32_t* new_lens, int s, int b, bool read) {
+  if (!read) return {kDryLength, s};
+#ifdef __CUDA_ARCH__
+  return {__ldcg(seqlens + b), new_lens ? __ldcg(new_lens + b) : s};
+#else
+  return {seqlens[b], new_lens ? new_lens[b] : s};
+#endif
 }
 
 MLA_HD int32_t window_lo(int32_t end, int32_t window) { return end > window ? end - window : 0; }
