@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             blk[h2] = page_of(p, bt_row, keys, pc.page(2 * t + h2));
             if (blk[h2] < 0) {
               if (p.err) atomicOr(p.err, MLA_DEVERR_BAD_PAGE);
-              blk[h2] = 0;  // read a valid page; the bad page's keys are wrong but finite
+              blk[h2] = static_cast<int32_t>(p.num_pages);  // out of range: TMA fills zeros, codes and scales
             }
           }
           // requests 0 .. n_own - 1: raw data of the owned latent chunks;
