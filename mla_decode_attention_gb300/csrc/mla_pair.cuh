@@ -318,7 +318,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         // Windowed: every piece's query rows take that way, as a round of the
         // ring of their own (`round`: of the next load): short pieces gain more
         // from four boxes in flight than from keys requested before them.
-        [[maybe_unused]] uint32_t round = 0, q_loads = 0;
+        [[maybe_unused]] uint32_t round = 0, q_boxes = 0;  // q_boxes: requested so far
         auto load_q_box = [&](int i, int qq) {
           const uint32_t bar = smem_u32(&bars->q_box[i]);
           mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 3 ? kChunk : 0));
@@ -328,15 +328,16 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         while (pc.next()) {
           const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
           if constexpr (kWindow) {
-            // box i lies in ring slots 2i / 3 .. (2i + 1) / 3
+            // box i lies in ring slots 2i / 3 .. (2i + 1) / 3: slot by slot, in the
+            // order that q_box_loads() counts them
             for (int g = 0; g < 3 && ok; ++g) {
               if (round > 0) ok = mbar_wait(smem_u32(&bars->kempty[g]), (round - 1) & 1, abort_flag, p.err);
               if (!ok) break;
               load_q_box(g == 0 ? 0 : g + 1, q);
               if (g == 1) load_q_box(1, q);
+              q_boxes += g == 1 ? 2 : 1;
             }
             ++round;
-            if (ok) ++q_loads;
           } else if (first) {
             first = false;
             if (pw == 0 && lane == 0) issue_first_q(q);
@@ -398,10 +399,12 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             }
           }
         }
-        if (kWindow && !ok && q_loads > 0) {
+        if (kWindow && !ok) {  // the boxes in flight, which the last piece may have requested in part
           for (int i = 0; i < 4; ++i) {
+            const uint32_t loads = q_box_loads(q_boxes, i);
             const uint64_t t_start = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(&bars->q_box[i]), (q_loads - 1) & 1) && globaltimer_ns() - t_start < 1000000ull) {
+            while (loads > 0 && !mbar_try_wait(smem_u32(&bars->q_box[i]), (loads - 1) & 1) &&
+                   globaltimer_ns() - t_start < 1000000ull) {
             }
           }
         }

@@ -191,6 +191,13 @@ MLA_HD int32_t window_row(const WindowPlan& w, int64_t m, int64_t pl, int32_t la
   return static_cast<int32_t>(2 * (pl * w.lanes + lane) + (window_first_item(w, pl) == m ? 0 : 1));
 }
 
+// The two-SM kernel requests every piece's query rows as four boxes, in the order
+// 0, 2, 1, 3: loads of box i among the first n boxes requested.
+MLA_HD uint32_t q_box_loads(uint32_t n, int i) {
+  const uint32_t place = i == 1 ? 2u : (i == 2 ? 1u : static_cast<uint32_t>(i));
+  return (n + 3u - place) / 4u;
+}
+
 // fixed: what a piece costs besides its tiles (query load, epilogue), and
 // merge: what writing partial rows and merging them costs a call, in tiles.
 inline WindowPlan window_plan(int batch, int s_q, int group, int window, int sinks, int parts, bool ragged, int fixed,
