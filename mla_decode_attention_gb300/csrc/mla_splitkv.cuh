@@ -207,6 +207,7 @@ struct WorkList {
   int64_t m;            // the next batch's first item number on the part's cost line
   int32_t line, pl;     // the line, and the part's number on it
   int32_t n, more;      // pieces of the batch; whether another may follow
+  uint32_t batches;     // written so far
 };
 constexpr int kWorkBytes = 2688;
 static_assert(sizeof(WorkItem) == 80 && sizeof(WorkList) <= kWorkBytes && kWorkBytes % 128 == 0, "work list");
@@ -247,6 +248,7 @@ __device__ __noinline__ static void plan_batch(const SplitParams& p, WorkList* l
     list->more = more ? 1 : 0;
     if (commit) {
       list->m = mine + kWorkItems;
+      ++list->batches;
       mbar_arrive(smem_u32(&list->full));
     }
   }
@@ -274,7 +276,7 @@ __device__ __forceinline__ void plan_first(const SplitParams& p, WorkList* list,
   const int line = part % w.lanes, pl = part / w.lanes;
   const int64_t m = window_first_item(w, pl);
   if (lane == 0) {
-    list->line = line; list->pl = pl; list->m = m;
+    list->line = line; list->pl = pl; list->m = m; list->batches = 0;
   }
   __syncwarp();
   plan_batch(p, list, false, row0, most);
@@ -311,7 +313,7 @@ struct Pieces<true> {
   __device__ __forceinline__ bool next() {
     const uint32_t full = list + offsetof(WorkList, full), free = list + offsetof(WorkList, free);
     while (i == n) {
-      // (Every role comes here whatever became of its waits, so these end.)
+      // (Every role comes here for every batch, if need be by walk_list_out(), so these end.)
       if (batch > 0) {
         if (ld_shared_i32(list + offsetof(WorkList, more)) == 0) return false;
         if (warps) __syncwarp();
@@ -587,6 +589,25 @@ static __device__ __noinline__ void convert_unit(uint32_t row, int dq_r, int dq_
   }
 }
 
+extern __shared__ uint8_t smem_raw[];
+__device__ __forceinline__ uint8_t* smem_aligned() {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+
+// Windowed: a role that has left its loop over the pieces after a failed wait goes
+// on through the work list, whose batches need every role's arrival.  (The batch
+// that it was in is the last one written, since the next waits for it; a role that
+// has walked them all finds no more.)  All is worked out here, so that the loops
+// keep their registers.
+__device__ __noinline__ static void walk_list_out(const SplitParams& p) {
+  const int warp = threadIdx.x >> 5;
+  WorkList* list = reinterpret_cast<WorkList*>(smem_aligned() + kSmemWork);
+  Pieces<true> pc(p, list, warp < kProducerWarp);
+  pc.plan_by(warp == kSoftmaxWarp0, static_cast<int>(blockIdx.x) % p.n_hblk * kRowsPerCta, kRowsPerCta);
+  pc.batch = ld_shared_i32(smem_u32(&list->batches));
+  while (pc.next()) pc.i = pc.n;
+}
+
 template <KvMode kMode, bool kWindow = false>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_splitkv_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -594,9 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_codes,
                        const __grid_constant__ CUtensorMap tm_scales,
                        const __grid_constant__ SplitParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* smem = smem_aligned();
   SmemSmall* sm = reinterpret_cast<SmemSmall*>(smem + kSmemSmall);
   const uint32_t smem_base = smem_u32(smem);
   const uint32_t kv_base = smem_base + kSmemKv;
@@ -1030,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kWindow) pc.plan_by(warp == kSoftmaxWarp0, hb * kRowsPerCta, kRowsPerCta);
     uint32_t tile_ctr = 0, item_ctr = 0;
     bool ok = true;
-    while (ok && pc.next()) {
+    while ((!is_fp8(kMode) || ok) && pc.next()) {
       const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
       const int32_t keys = pc.keys();
       const int32_t* idx_row = (kMode == KvMode::kSparseBf16)
@@ -1084,10 +1103,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           seen = window_sees(pc.end_of_row(hb * kRowsPerCta + R * g), p.window, p.sinks, x);
           seen_any = pc.any_sees(x);
         }
-        ok = mbar_wait(smem_u32(&sm->s_full), tile_ctr & 1, abort_flag, p.err);
-        if constexpr (is_fp8(kMode))  // leave together (the barrier above)
+        if (is_fp8(kMode) || ok) ok = mbar_wait(smem_u32(&sm->s_full), tile_ctr & 1, abort_flag, p.err);
+        if constexpr (is_fp8(kMode)) {  // leave together (the barrier above)
           ok = !named_barrier_or(kDequantBarrier, 128 * kSoftmaxGroups, !ok);
-        if (!ok) break;
+          if (!ok) break;
+        } else {  // a warp whose wait failed goes on to its group's barriers; what it computes no longer counts
+          ok = __all_sync(0xffffffffu, ok);
+        }
         tc_fence_after();
         float x[R];
         tmem_ld16(t_s, x);
@@ -1199,7 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bsum += warp_sum_scatter16(tb, lane);
         ++tile_ctr;
       }
-      if (!ok) break;
+      if (is_fp8(kMode) && !ok) break;
       // ---- epilogue: O^T / sum bf16(p) -> out (one split) or fp32 partial
       const int row = lane & (R - 1);
       if (lane < R) {
@@ -1211,10 +1233,14 @@ __global__ void __launch_bounds__(kThreads, 1)
              (sm->red_sum[g][2][row] + sm->red_sum[g][3][row]);
       bsum = (sm->red_bsum[g][0][row] + sm->red_bsum[g][1][row]) +
              (sm->red_bsum[g][2][row] + sm->red_bsum[g][3][row]);
-      ok = mbar_wait(smem_u32(&sm->o_done), item_ctr & 1, abort_flag, p.err);
-      if constexpr (is_fp8(kMode))  // the next piece starts at a shared barrier
+      if (is_fp8(kMode) || ok) ok = mbar_wait(smem_u32(&sm->o_done), item_ctr & 1, abort_flag, p.err);
+      if constexpr (is_fp8(kMode)) {  // the next piece starts at a shared barrier
         ok = !named_barrier_or(kDequantBarrier, 128 * kSoftmaxGroups, !ok);
-      if (!ok) break;
+        if (!ok) break;
+      } else {
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+      }
       tc_fence_after();
       const bool has = lsum > 0.f && bsum > 0.f;
       const bool final_out = pc.whole();
@@ -1269,6 +1295,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---- teardown
+  if constexpr (kWindow) {  // a wait has failed: roles that left their loops
+    if (__any_sync(0xffffffffu, *abort_flag != 0u) && (warp < kProducerWarp || lane == 0)) walk_list_out(p);
+  }
   tc_fence_before();
   __syncthreads();
   if (share) cluster_sync();  // no peer still writes into this CTA's smem

@@ -50,3 +50,40 @@ def test_the_producer_counts_boxes_in_that_order():
     text = " ".join(open(os.path.join(CSRC, "mla_pair.cuh")).read().split())
     assert ("load_q_box(g == 0 ? 0 : g + 1, q); if (g == 1) load_q_box(1, q); q_boxes += g == 1 ? 2 : 1;") in text
     assert "const uint32_t loads = q_box_loads(q_boxes, i);" in text
+
+
+def one_sm_kernel():
+    text = open(os.path.join(CSRC, "mla_splitkv.cuh")).read()
+    return " ".join(text[text.index("mla_splitkv_kernel("):].split())
+
+
+def test_every_role_of_the_one_sm_kernel_comes_for_every_batch():
+    """A role that leaves its loop over the pieces after a failed wait would not
+    arrive at the work list, and the others would wait there for as long as that
+    wait may take.  So it goes through the rest of the list before the teardown."""
+    text = one_sm_kernel()
+    teardown = text[text.index("// ---- teardown"):]
+    walk = teardown.index("walk_list_out(p);")
+    assert "__any_sync(0xffffffffu, *abort_flag != 0u) && (warp < kProducerWarp || lane == 0)" in teardown[:walk]
+    assert walk < teardown.index("__syncthreads();")
+
+
+def test_softmax_warps_leave_together_or_not_at_all():
+    """Without the FP8 caches' barriers of all softmax warps, a warp whose wait
+    failed must reach every barrier of its warpgroup, since a wait may fail for
+    one warp and not for another: the loops have no way out that is not the FP8
+    caches' own, behind a vote of all sixteen."""
+    text = one_sm_kernel()
+    softmax = text[text.index("// Thread = one token row r of the tile"):text.index("// ---- teardown")]
+    assert "while ((!is_fp8(kMode) || ok) && pc.next()) {" in softmax
+    waits = softmax.split("if (is_fp8(kMode) || ok) ok = mbar_wait(")[1:]   # for the scores, for the output
+    assert len(waits) == 2
+    for after in waits:
+        fp8, rest = after.split("} else {", 1)
+        assert "if constexpr (is_fp8(kMode)) {" in fp8 and "named_barrier_or(kDequantBarrier" in fp8 and "if (!ok) break;" in fp8
+        other = rest.split("}", 1)[0]
+        assert "ok = __all_sync(0xffffffffu, ok);" in other and "break" not in other
+    # besides those two: the FP8 conversion's vote, its tile loop, its pieces
+    assert softmax.count("break;") == 5
+    assert "ok = !named_barrier_or(kDequantBarrier, 128 * kSoftmaxGroups, !ok); if (!ok) break; convert_unit" in softmax
+    assert "if (!ok) break; } // windowed" in softmax and "if (is_fp8(kMode) && !ok) break; // ---- epilogue" in softmax
