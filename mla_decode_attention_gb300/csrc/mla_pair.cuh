@@ -1143,7 +1143,10 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
   // ---- teardown
   tc_fence_before();
   __syncthreads();
+  // (after an abort: what this CTA left in flight, then what the peer did)
+  if (*abort_flag) settle_after_abort();
   cluster_sync();  // no peer still copies into or arrives on this CTA's smem
+  if (*abort_flag) settle_after_abort();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

@@ -107,6 +107,14 @@ __device__ __forceinline__ bool mbar_wait_all_roles(uint32_t bar, uint32_t parit
   return true;
 }
 
+// After an abort: a pause far longer than any copy or product that a role may have
+// left in flight takes (microseconds), before the block gives up its memory.
+constexpr uint64_t kSettleNs = 1000000ull;
+__device__ __noinline__ static void settle_after_abort() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < kSettleNs) __nanosleep(1000);
+}
+
 // ---------------------------------------------------------------- fences
 
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -1300,7 +1300,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (share) cluster_sync();  // no peer still writes into this CTA's smem
+  // (after an abort: what this CTA left in flight, then what the peer did)
+  if (*abort_flag) settle_after_abort();
+  if (share) {
+    cluster_sync();  // no peer still writes into this CTA's smem
+    if (*abort_flag) settle_after_abort();
+  }
   if (!kWindow) pdl_launch_dependents();
   if (warp == kMmaWarp) {
     tc_fence_after();

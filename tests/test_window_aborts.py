@@ -87,3 +87,17 @@ def test_softmax_warps_leave_together_or_not_at_all():
     assert softmax.count("break;") == 5
     assert "ok = !named_barrier_or(kDequantBarrier, 128 * kSoftmaxGroups, !ok); if (!ok) break; convert_unit" in softmax
     assert "if (!ok) break; } // windowed" in softmax and "if (is_fp8(kMode) && !ok) break; // ---- epilogue" in softmax
+
+
+@pytest.mark.parametrize("source", ["mla_splitkv.cuh", "mla_pair.cuh"])
+def test_copies_in_flight_land_before_the_block_ends(source):
+    """Not every role counts what it has left in flight (the FP8 producer's codes,
+    query rows, copies into the peer, products on TMEM), so after an abort every
+    block pauses once its own roles have ended, before it lets the peer go, and
+    once more after the peer's have, before it gives up TMEM and ends."""
+    text = " ".join(open(os.path.join(CSRC, source)).read().split())
+    teardown = text[text.index("// ---- teardown"):]
+    order = ["__syncthreads();", "if (*abort_flag) settle_after_abort();", "cluster_sync();", "if (*abort_flag) settle_after_abort();", "tmem_dealloc("]
+    at = 0
+    for step in order:
+        at = teardown.index(step, at) + len(step)
