@@ -495,7 +495,7 @@ int mla_window_workspace_size(int batch, int s_q, int h_q, int window, int sinks
  *  workspace    workspace_bytes bytes, at least mla_window_workspace_size(),
  *               16-byte aligned; NULL when that is 0.
  *  A token that sees no key (padding slots among them) gets out = 0,
- *  lse = -inf.
+ *  lse = -inf; one that sees a key with a NaN gets NaN in both.
  */
 int mla_window_decode(const void* q, const void* kv_cache, int kv_format, int64_t num_pages,
                       const int32_t* block_table, int64_t block_table_stride, int64_t max_pages,

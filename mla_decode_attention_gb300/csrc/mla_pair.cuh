@@ -563,6 +563,9 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           end = pc.end_of_row(r);
           blind = end > 0;
         }
+        // Whether the row has seen a key; windowed, NaN sums (from a key that is not
+        // finite) stay NaN: they are no empty row.
+        auto has = [&] { return kWindow ? end > 0 && !(lsum <= 0.f || bsum <= 0.f) : lsum > 0.f && bsum > 0.f; };
         for (int t = t0; t < t1; ++t, ++tc) {
           const uint32_t sb = tc & 1;
           const uint32_t t_s = tmem + lane_off + kSCol + 128 * sb;
@@ -719,12 +722,10 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           bsum += bs + bs2;
           st_shared_f32(stage + kSideAlpha + 4 * r, alpha);
           if (t == t1 - 1) {
-            float inv_l = bsum > 0.f ? 1.f / bsum : 0.f;
-            if (kWindow && end == 0) inv_l = 0.f;
+            float inv_l = has() ? 1.f / bsum : 0.f;
             // attention sink: applied with 1/l to a final row, by the combine to a split row
             if ((kSparse || kWindow) && p.attn_sink && pc.whole()) {
-              const float lse_t = (lsum > 0.f && bsum > 0.f) ? (m_use + __log2f(lsum)) * 0.69314718055994531f
-                                                             : -INFINITY;
+              const float lse_t = has() ? (m_use + __log2f(lsum)) * 0.69314718055994531f : -INFINITY;
               if (!kWindow || end > 0) inv_l *= attn_sink_factor(lse_t, p.attn_sink[kWindow ? r % p.h : r]);
             }
             st_shared_f32(stage + kSideInvL + 4 * r, inv_l);
@@ -748,8 +749,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           }
         }
         // LSE of row r for this piece
-        const float lse_v = (lsum > 0.f && bsum > 0.f && (!kWindow || end > 0))
-                                ? (m_use + __log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+        const float lse_v = has() ? (m_use + __log2f(lsum)) * 0.69314718055994531f : -INFINITY;
         if (ok) {
           if (pc.whole()) {
             if constexpr (kWindow) {

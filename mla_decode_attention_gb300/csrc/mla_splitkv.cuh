@@ -1242,7 +1242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) continue;
       }
       tc_fence_after();
-      const bool has = lsum > 0.f && bsum > 0.f;
+      // (windowed: NaN sums, from a key that is not finite, stay NaN; they are no empty row)
+      const bool has = kWindow ? !(lsum <= 0.f || bsum <= 0.f) : lsum > 0.f && bsum > 0.f;
       const bool final_out = pc.whole();
       float inv_l = has ? 1.f / bsum : 0.f;
       const float lse_v = has ? (m_use + __log2f(lsum)) * 0.69314718055994531f : NEG_INF;

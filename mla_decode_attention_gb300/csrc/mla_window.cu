@@ -143,8 +143,9 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBlocksPerSm)
 #pragma unroll
       for (int i = 1; i < kShare; ++i) sum += s_sum[w0 + i];
     }
-    const float lse = sum > 0.f ? mx + __logf(sum) : -INFINITY;
-    float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const bool none = sum <= 0.f;  // (a NaN sum, from a key that is not finite, stays NaN)
+    const float lse = none ? -INFINITY : mx + __logf(sum);
+    float inv = none ? 0.f : 1.f / sum;
     const int j = j0 + r / p.h, head = r % p.h;
     if (p.attn_sink && in) inv *= attn_sink_factor(lse, p.attn_sink[head]);
     const int64_t tok = static_cast<int64_t>(b) * p.s_q + j;
