@@ -485,9 +485,10 @@ int mla_window_workspace_size(int batch, int s_q, int h_q, int window, int sinks
  *               A bad entry, or one past max_pages, sets
  *               MLA_DEVERR_BAD_PAGE; the outputs of tokens that need it are
  *               then unspecified.
- *  Cache slots that none of the request's tokens of the call sees may hold
- *  anything, NaN included; what is not finite in a slot that one of them sees
- *  may reach the outputs of all of them.
+ *  Cache slots that a token does not see may hold anything, NaN included,
+ *  without a trace in its outputs, whichever other tokens see them.  (A key
+ *  that is infinite in some columns and whose score is -inf has no weight; what
+ *  it leaves in those columns is unspecified.)
  *  Lengths above 2^30 count as 2^30.
  *  attn_sink    optional [h_q] fp32, as for mla_sparse_decode.
  *  num_sm_parts from mla_num_sm_parts (any value >= 1 gives the same result up

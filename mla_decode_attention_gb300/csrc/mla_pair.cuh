@@ -975,6 +975,7 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               // for these rows).
               uint32_t seen[4];
               pc.tile_masks(t, seen);
+              const uint32_t some = __ballot_sync(0xffffffffu, pc.some_see(pc.key_at(t, 4 * lane + warp - 4)));  // of every fourth key
               if (ok && tc > 0) ok = mbar_wait(smem_u32(&bars->pv_done[(tc - 1) & 1]), ((tc - 1) >> 1) & 1, abort_flag, p.err);
 #pragma unroll 1
               for (int hf = 0; hf < 2; ++hf) {  // the first V half while the second arrives
@@ -987,6 +988,17 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
                                        (k & 7) * 128 + (r & 7) * 16;
 #pragma unroll
                   for (int c = 0; c < 4; ++c) st_shared_v4(row + c * 1024, 0u, 0u, 0u, 0u);
+                }
+                // a key that some tokens see and others do not: what is not finite
+                // in it becomes zero likewise (a token that sees it is NaN by its
+                // score); a lane for each of its 32 units, and the keys, neighbours
+                // as they are, dealt to the warps (4 x 333 tokens of 16 heads 54 us
+                // with each warp at its own 32)
+#pragma unroll 1
+                for (uint32_t m = ok ? some : 0u; m; m &= m - 1) {
+                  const int k = 4 * (__ffs(m) - 1) + warp - 4;
+                  finite_unit(base + hf * 2 * kHalfPage + (k >> 6) * kHalfPage + ((k & 63) >> 3) * 4096 + (k & 7) * 128 +
+                              (lane >> 3) * 1024 + (lane & 7) * 16);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();

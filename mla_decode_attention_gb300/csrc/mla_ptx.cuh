@@ -559,6 +559,16 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                : "memory");
   return v;
 }
+// Two bf16 values, those that are not finite as zeros.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
+  return w & (((w & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u));
+}
+// The same for eight of them in shared memory.
+__device__ __forceinline__ void finite_unit(uint32_t addr) {
+  const uint4 v = ld_shared_v4(addr);
+  const uint4 w = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+  if (((v.x ^ w.x) | (v.y ^ w.y) | (v.z ^ w.z) | (v.w ^ w.w)) != 0u) st_shared_v4(addr, w.x, w.y, w.z, w.w);
+}
 __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");

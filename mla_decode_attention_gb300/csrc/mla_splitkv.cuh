@@ -374,6 +374,11 @@ struct Pieces<true> {
   __device__ __forceinline__ bool any_sees(int32_t x) const {
     return x < keys() && (x < p.sinks || x >= window_lo(at(offsetof(WorkItem, least)), p.window));
   }
+  // Whether some of them see it and others do not.
+  __device__ __forceinline__ bool some_see(int32_t x) const {
+    const int32_t all_lo = window_lo(keys(), p.window);
+    return p.plan.group > 1 && any_sees(x) && !(x < at(offsetof(WorkItem, least)) && (x < p.sinks || x >= all_lo));
+  }
   __device__ __forceinline__ int rows() const { return at(offsetof(WorkItem, rows)); }  // of its request's token slots
   __device__ __forceinline__ int b() const { return at(offsetof(WorkItem, b)); }
   __device__ __forceinline__ int j0() const { return at(offsetof(WorkItem, j0)); }
@@ -606,6 +611,22 @@ __device__ __noinline__ static void walk_list_out(const SplitParams& p) {
   pc.plan_by(warp == kSoftmaxWarp0, static_cast<int>(blockIdx.x) % p.n_hblk * kRowsPerCta, kRowsPerCta);
   pc.batch = ld_shared_i32(smem_u32(&list->batches));
   while (pc.next()) pc.i = pc.n;
+}
+
+// Windowed: what is not finite in two chunks of some of 32 keys becomes zero (`keys`:
+// a bit each; row0: the first key's row of the first chunk).  Called by a whole
+// warp: half of it takes the 16 units of a key, two keys at a time (a thread per
+// key: 16 heads of two tokens over 512 keys 27.2 -> 29.8 us).
+__device__ __noinline__ static void finite_keys(uint32_t keys, uint32_t row0) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t unit = row0 + ((lane >> 3) & 1) * kChunkBytes + (lane & 7) * 16;
+  while (keys) {
+    const int first = __ffs(keys) - 1;
+    keys &= keys - 1;
+    const int second = keys ? __ffs(keys) - 1 : first;
+    keys &= keys - 1;
+    finite_unit(unit + (lane < 16 ? first : second) * 128);
+  }
 }
 
 template <KvMode kMode, bool kWindow = false>
@@ -1094,14 +1115,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        // windowed: whether this warpgroup's token, or any of the item's, sees
-        // the key of this thread's row
-        [[maybe_unused]] bool seen = true, seen_any = true;
+        // windowed: whether this warpgroup's token, any of the item's, or some of
+        // them but not all see the key of this thread's row
+        [[maybe_unused]] bool seen = true, seen_any = true, seen_some = false;
         if constexpr (kWindow) {
           const int32_t x = pc.key_at(t, r);
           // (h is a multiple of 16, so the warpgroup's rows are one token's)
           seen = window_sees(pc.end_of_row(hb * kRowsPerCta + R * g), p.window, p.sinks, x);
           seen_any = pc.any_sees(x);
+          seen_some = pc.some_see(x);
         }
         if (is_fp8(kMode) || ok) ok = mbar_wait(smem_u32(&sm->s_full), tile_ctr & 1, abort_flag, p.err);
         if constexpr (is_fp8(kMode)) {  // leave together (the barrier above)
@@ -1212,6 +1234,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               st_shared_v4(row + kChunkBytes + ((u & 7) << 4), 0u, 0u, 0u, 0u);
             }
           }
+        }
+        if constexpr (kWindow) {
+          // a key that other tokens of the item do not see: what is not finite in it
+          // becomes zero likewise (a token that does see it is NaN by its score)
+          const uint32_t some = __ballot_sync(0xffffffffu, seen_some);
+          if (some) finite_keys(some, kv_base + 2 * g * kChunkBytes + 32 * wq * 128);
         }
         fence_proxy_async_smem();
         tc_fence_before();

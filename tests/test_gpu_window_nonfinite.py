@@ -1,6 +1,7 @@
 """mla_window_decode where keys that are not finite are seen: a token that sees a
 NaN gets what its formula gives, NaN in every column and in lse, and is not taken
-for a token that sees no key (0 and -inf)."""
+for a token that sees no key (0 and -inf); a token that does not see it is as if
+it were not there, whichever tokens share its block of query rows."""
 import numpy as np
 import pytest
 import torch
@@ -114,3 +115,57 @@ def test_infinite_scores(h):
     ro, rl = oracle.attend(q, keys_of(c["cache"], BF16)[table[0, t // 64], t % 64], SCALE)
     rest = np.arange(512) != 7
     assert_parity(out[0, 0][~up][:, rest], ro[:, rest], lse[0, ~up, 0], rl)
+
+
+BLOCKS = [(BF16, 128), (BF16, 64), (BF16, 48), (BF16, 32), (BF16, 16), (FP8_656, 64), (FP8_656, 32), (FP8_656, 16), (FP8_528, 32), (FP8_528, 16)]
+
+
+@pytest.mark.parametrize("fmt,h", BLOCKS)
+@pytest.mark.parametrize("s", [2, 3, 8, 11])
+def test_keys_that_some_tokens_of_a_block_see(fmt, h, s):
+    """NaN in a request's newest key, in an older new one, in the oldest that its
+    first tokens see, in a first token, at page and tile borders."""
+    lens = [300, 129, 200, 64 + s, 500, 257, 700]
+    c = case(fmt, lens, s, h, 60, 3, seed=45, logits=True)
+    bad = [(0, 299), (1, 129 - s + 1), (2, 200 - s - 59), (3, 63 + s), (4, 500 - 60), (5, 256), (5, 255 - s // 2)]
+    for b, t in bad:
+        spoil(c, b, t, NAN)
+    out, lse = run(c)
+    check(c, bad, out, lse)
+    assert not np.any(np.isnan(out[6])) and not np.any(np.isnan(out[:6, 0][[0, 1, 3]]))
+
+
+@pytest.mark.parametrize("fmt,h", BLOCKS)
+def test_a_chunk_with_padding_and_many_bad_keys(fmt, h):
+    c = case(fmt, [170, 150, 131], 40, h, 30, 5, new=[40, 33, 9], seed=46)
+    g = torch.Generator().manual_seed(47)
+    bad = sorted({(b, int(t)) for b, (L, n) in enumerate([(170, 40), (150, 33), (131, 9)])
+                  for t in torch.randint(L - n - 29, L, (6,), generator=g)})
+    for i, (b, t) in enumerate(bad):
+        spoil(c, b, t, NAN, 83 * i % 512)
+    check(c, bad, *run(c))
+    check(c, bad, *run(c, 3))
+
+
+@pytest.mark.parametrize("fmt,h", [k for k in BLOCKS if k[1] < 64])
+def test_blocks_of_tokens_that_are_cut(fmt, h):
+    """Long windows: the keys that some tokens see are in the first and last of
+    many pieces."""
+    c = case(fmt, [1900, 1500, 64], 11, h, 1200, 3, seed=48, logits=True)
+    bad = [(0, 1899), (0, 1895), (1, 1500 - 1200 - 5), (2, 60)]
+    for b, t in bad:
+        spoil(c, b, t, NAN)
+    check(c, bad, *run(c))
+
+
+@pytest.mark.parametrize("h", [16, 48, 64])
+@pytest.mark.parametrize("value", [INF, -INF])
+def test_infinite_keys_stay_with_the_tokens_that_see_them(h, value):
+    c = case(BF16, [300, 200], 4, h, 90, 0, seed=49)
+    ref = run(c)
+    for b, t in [(0, 298), (1, 200 - 4 - 89)]:
+        for column in range(0, 512, 37):
+            spoil(c, b, t, value, column)
+    out, lse = run(c)
+    for b, j in [(0, 0), (0, 1), (1, 1), (1, 2), (1, 3)]:
+        assert np.array_equal(out[b, j], ref[0][b, j]) and np.array_equal(lse[b, :, j], ref[1][b, :, j])
