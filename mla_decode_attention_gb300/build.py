@@ -5,12 +5,16 @@ Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc, then
 linked into one shared library next to this file.  The build fails when any
 kernel spills registers (the ptxas report of every kernel is checked, as the
 FlashMLA build does after compiling; ``MLA_SKIP_REG_SPILL_CHECK=1`` skips
-the check).  ``python -m
-mla_decode_attention_gb300.build`` runs it.
+the check).  The library needs nvcc alone; the module, which takes torch
+tensors, needs torch, its headers and Python's, and is built where torch is
+installed, once the library is in place.  ``python -m
+mla_decode_attention_gb300.build`` builds both, with ``--library`` the library
+alone.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import re
 import shutil
@@ -106,13 +110,32 @@ def spill_report(ptxas_log: str) -> list[str]:
     return out
 
 
-def build(verbose: bool = False) -> str:
+def _link(objs: list[str]) -> str:
+    lib = os.path.join(HERE, LIB_NAME)
+    tmp = lib + ".tmp"
+    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, lib)
+    return lib
+
+
+def build_step() -> str:
+    """The Python module alone; the library is beside it."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    _link_step(_compile_step())
+    return os.path.join(HERE, _step_module())
+
+
+def build(verbose: bool = False, step: bool = True) -> str:
+    """The library and, where torch is installed (and with ``step``), the Python
+    module.  An error in the module's build is raised once the library is built."""
+    step = step and importlib.util.find_spec("torch") is not None
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        step = ex.submit(_compile_step)
+        module = ex.submit(_compile_step) if step else None
         results = list(ex.map(_compile, _sources()))
-        step_obj = step.result()
-    objs = [o for o, _ in results]
     log = "\n".join(l for _, l in results)
     with open(os.path.join(BUILD_DIR, "ptxas.log"), "w") as f:
         f.write(log)
@@ -122,16 +145,11 @@ def build(verbose: bool = False) -> str:
     if spills and os.environ.get("MLA_SKIP_REG_SPILL_CHECK") != "1":
         raise RuntimeError("register spilling detected, build failed (set "
                            "MLA_SKIP_REG_SPILL_CHECK=1 to skip this check):\n" + "\n".join(spills))
-    lib = os.path.join(HERE, LIB_NAME)
-    tmp = lib + ".tmp"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib)
-    _link_step(step_obj)
+    lib = _link([o for o, _ in results])
+    if module:
+        _link_step(module.result())
     return lib
 
 
 if __name__ == "__main__":
-    print(build(verbose="-v" in sys.argv))
+    print(build(verbose="-v" in sys.argv, step="--library" not in sys.argv))
