@@ -310,8 +310,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
           for (int i = 0; i < 4; ++i) {
             const uint32_t bar = smem_u32(&bars->q_box[i]);
             mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 0 ? kChunk : 0));
-            if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * (kWindow ? p.h : kRows), bar, pol);
-            tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * (kWindow ? p.h : kRows), 2 * i, bar, pol);
+            if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * kRows, bar, pol);
+            tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * kRows, 2 * i, bar, pol);
           }
           q_issued = true;
         };
@@ -322,8 +322,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
         auto load_q_box = [&](int i, int qq) {
           const uint32_t bar = smem_u32(&bars->q_box[i]);
           mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 3 ? kChunk : 0));
-          tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * (kWindow ? p.h : kRows), 2 * i, bar, pol);
-          if (i == 3) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * (kWindow ? p.h : kRows), bar, pol);
+          tma_load_3d(base + i * kQBoxBytes, &tm_ql, 0, qq * p.h, 2 * i, bar, pol);
+          if (i == 3) tma_load_2d(base + kQRope, &tm_qr, kDv, qq * p.h, bar, pol);
         };
         while (pc.next()) {
           const int q = pc.q, t0 = pc.t0, t1 = pc.t1;
@@ -443,8 +443,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
             for (int i = 0; i < 4 && ok; ++i) {
               const uint32_t bar = smem_u32(&bars->q_tma);
               mbar_arrive_expect_tx(bar, kQBoxBytes + (i == 0 ? kChunk : 0));
-              if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, q * (kWindow ? p.h : kRows), bar, qpol);
-              tma_load_3d(base + kStage, &tm_ql, 0, q * (kWindow ? p.h : kRows), 2 * i, bar, qpol);
+              if (i == 0) tma_load_2d(base + kQRope, &tm_qr, kDv, q * kRows, bar, qpol);
+              tma_load_3d(base + kStage, &tm_ql, 0, q * kRows, 2 * i, bar, qpol);
               q_pending = true;
               ok = mbar_wait(bar, qtma_n & 1, abort_flag, p.err);
               if (!ok) break;

@@ -346,8 +346,7 @@ struct Pieces<true> {
   __device__ __forceinline__ int32_t end_of_row(int r) const {
     if (r >= rows()) return 0;
     const int j = p.plan.group == 1 ? 0 : r / p.h;
-    const int32_t e = at(offsetof(WorkItem, first)) + j;
-    return j < at(offsetof(WorkItem, count)) && e > 0 ? e : 0;
+    return item_end(at(offsetof(WorkItem, first)), at(offsetof(WorkItem, count)), j);
   }
   __device__ __forceinline__ int32_t page(int32_t e) const {
     return e < at(offsetof(WorkItem, head_pages)) ? e : e + at(offsetof(WorkItem, skip));

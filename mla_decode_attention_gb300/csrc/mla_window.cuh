@@ -37,17 +37,6 @@ namespace mla {
 constexpr int kWindowPage = 64;
 constexpr int32_t kWindowMaxLen = 1 << 30;  // longer lengths are taken as this
 
-// Token j of request b: one past its position, or 0 for padding (slots past
-// new_lens[b], positions before the first).
-MLA_HD int32_t window_end(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j) {
-  int32_t n = new_lens ? new_lens[b] : s;
-  n = n < 0 ? 0 : (n > s ? s : n);
-  int32_t L = seqlens[b];
-  L = L > kWindowMaxLen ? kWindowMaxLen : (L < 0 ? 0 : L);
-  const int32_t end = L - n + j + 1;
-  return (j >= n || L <= 0 || end < 0) ? 0 : end;
-}
-
 // Of the tokens j0 .. j0 + group - 1: the least and the largest end among those
 // that are no padding (both 0 when there is none); token j0 + j has end first + j
 // when j < count and that is positive, else it is padding.
@@ -69,6 +58,14 @@ MLA_HD WindowEnds item_ends(int32_t L, int32_t n, int s, int j0, int group) {
 }
 MLA_HD WindowEnds window_ends(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j0, int group) {
   return item_ends(seqlens[b], new_lens ? new_lens[b] : s, s, j0, group);
+}
+
+// End (one past the position) of token j of an item, 0 for padding.
+MLA_HD int32_t item_end(int32_t first, int32_t count, int32_t j) { return j < count && first + j > 0 ? first + j : 0; }
+// Of token j of request b, as the item of all its tokens has it.
+MLA_HD int32_t window_end(const int32_t* seqlens, const int32_t* new_lens, int s, int b, int j) {
+  const WindowEnds e = window_ends(seqlens, new_lens, s, b, 0, s);
+  return item_end(e.first, e.count, j);
 }
 
 // Length of request b and how many of its s slots hold new tokens, read past L1;

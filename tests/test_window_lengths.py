@@ -18,6 +18,7 @@ extern "C" void lengths(const int* lens, const int* fresh, int s, int b, int rea
   const RequestLengths r = request_lengths(lens, fresh, s, b, read != 0);
   out[0] = r.L; out[1] = r.n;
 }
+extern "C" int end(int first, int count, int j) { return item_end(first, count, j); }
 extern "C" void ends(int L, int n, int s, int j0, int group, int* out) {
   const WindowEnds e = item_ends(L, n, s, j0, group);
   out[0] = e.least; out[1] = e.most; out[2] = e.first; out[3] = e.count;
@@ -66,3 +67,7 @@ def test_ends_of_items(lib):
                         lib.ends(L, n, s, j0, group, out)
                         real = [int(p) + 1 for p in pos[j0:j0 + group] if p >= 0]
                         assert list(out)[:2] == ([min(real), max(real)] if real else [0, 0]), (L, s, n, j0, group)
+                        # the query rows of the item: of each token, and of rows past the last one
+                        for j in range(group):
+                            p = int(pos[j0 + j]) if j0 + j < s else -1
+                            assert lib.end(out[2], out[3], j) == p + 1, (L, s, n, j0, group, j)
