@@ -414,7 +414,8 @@ int mla_combine(const void* metadata, int batch, int s_q, int h_q, int num_sm_pa
  *  kv_cache     as for mla_decode; token at position p goes to slot p mod 64 of
  *               page block_table[b, p / 64].  Nothing else of the cache is
  *               written.  FP8 formats: scale = absmax / 448 of each 128 columns
- *               (1 where all are 0), or the smallest power of two at or above
+ *               (1 where all are 0; at least the least float where one is
+ *               not), or the smallest power of two at or above
  *               that of each 32 columns; codes = column / scale rounded to
  *               nearest even.  A non-finite column makes no more than its own
  *               token's row non-finite.

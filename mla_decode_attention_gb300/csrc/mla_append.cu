@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       float m = fmaxf(abs_max8(x), abs_max8(y));
 #pragma unroll
       for (int o = 1; o < kRowLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float sc = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+      // (at least the least float: a quotient that rounds to 0 would make NaN of 0 / 0)
+      const float sc = m > 0.f ? fmaxf(__fdiv_rn(m, 448.f), __uint_as_float(1u)) : 1.f;
       (tile == 0 ? scales.x : tile == 1 ? scales.y : tile == 2 ? scales.z : scales.w) = sc;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
