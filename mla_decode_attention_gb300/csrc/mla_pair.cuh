@@ -148,6 +148,19 @@ constexpr int kWork = kEpi + 4 * 4096;              // windowed: the list of pie
 constexpr int kSmemBytesWindow = kSmemBytes + kWorkBytes;
 static_assert(kSmemBytesWindow <= 232448 && kWork % 16 == 0, "shared memory per CTA");
 
+// Windowed: what is not finite in a V half of some of a tile's keys (bit i of `keys`:
+// key 4 i + the row warp's number) becomes zero.  Called by a whole row warp: a lane
+// for each of a key's 32 units, and the keys, neighbours as they are, dealt to the
+// warps (4 x 333 tokens of 16 heads 51 us, 54 with each warp at its own 32).  Out of
+// line: in the loop, items of one token, which never come here, lost 2 %.
+__device__ __noinline__ static void finite_value_keys(uint32_t keys, uint32_t half) {
+  const uint32_t lane = threadIdx.x & 31, at = half + (lane >> 3) * 1024 + (lane & 7) * 16;
+  for (; keys; keys &= keys - 1) {
+    const uint32_t k = 4 * (__ffs(keys) - 1) + (threadIdx.x >> 5) - 4;
+    finite_unit(at + (k >> 6) * kHalfPage + ((k & 63) >> 3) * 4096 + (k & 7) * 128);
+  }
+}
+
 // Sparse: the index list entries of key slots 128 t + 4 lane .. + 3 of
 // sequence q (-1 past its n_slots = topk or topk_length); validated by the caller.
 __device__ __forceinline__ void load_idx4(const SplitParams& p, int q, int t, int lane, int n_slots,
@@ -975,7 +988,8 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
               // for these rows).
               uint32_t seen[4];
               pc.tile_masks(t, seen);
-              const uint32_t some = __ballot_sync(0xffffffffu, pc.some_see(pc.key_at(t, 4 * lane + warp - 4)));  // of every fourth key
+              uint32_t some = 0;  // keys 4 i + warp - 4 that some tokens see and others do not
+              if (p.plan.group > 1) some = __ballot_sync(0xffffffffu, pc.some_see(pc.key_at(t, 4 * lane + warp - 4)));
               if (ok && tc > 0) ok = mbar_wait(smem_u32(&bars->pv_done[(tc - 1) & 1]), ((tc - 1) >> 1) & 1, abort_flag, p.err);
 #pragma unroll 1
               for (int hf = 0; hf < 2; ++hf) {  // the first V half while the second arrives
@@ -989,17 +1003,9 @@ __global__ void __maxnreg__(kSparse ? 128 : 224)
 #pragma unroll
                   for (int c = 0; c < 4; ++c) st_shared_v4(row + c * 1024, 0u, 0u, 0u, 0u);
                 }
-                // a key that some tokens see and others do not: what is not finite
-                // in it becomes zero likewise (a token that sees it is NaN by its
-                // score); a lane for each of its 32 units, and the keys, neighbours
-                // as they are, dealt to the warps (4 x 333 tokens of 16 heads 54 us
-                // with each warp at its own 32)
-#pragma unroll 1
-                for (uint32_t m = ok ? some : 0u; m; m &= m - 1) {
-                  const int k = 4 * (__ffs(m) - 1) + warp - 4;
-                  finite_unit(base + hf * 2 * kHalfPage + (k >> 6) * kHalfPage + ((k & 63) >> 3) * 4096 + (k & 7) * 128 +
-                              (lane >> 3) * 1024 + (lane & 7) * 16);
-                }
+                // what is not finite in them becomes zero likewise (a token that sees
+                // it is NaN by its score)
+                if (some && ok) finite_value_keys(some, base + hf * 2 * kHalfPage);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->v_clean[hf]));

@@ -373,10 +373,10 @@ struct Pieces<true> {
   __device__ __forceinline__ bool any_sees(int32_t x) const {
     return x < keys() && (x < p.sinks || x >= window_lo(at(offsetof(WorkItem, least)), p.window));
   }
-  // Whether some of them see it and others do not.
+  // Whether some of them see it and others do not (no key, of a single token).
   __device__ __forceinline__ bool some_see(int32_t x) const {
     const int32_t all_lo = window_lo(keys(), p.window);
-    return p.plan.group > 1 && any_sees(x) && !(x < at(offsetof(WorkItem, least)) && (x < p.sinks || x >= all_lo));
+    return any_sees(x) && !(x < at(offsetof(WorkItem, least)) && (x < p.sinks || x >= all_lo));
   }
   __device__ __forceinline__ int rows() const { return at(offsetof(WorkItem, rows)); }  // of its request's token slots
   __device__ __forceinline__ int b() const { return at(offsetof(WorkItem, b)); }
@@ -1114,15 +1114,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        // windowed: whether this warpgroup's token, any of the item's, or some of
-        // them but not all see the key of this thread's row
-        [[maybe_unused]] bool seen = true, seen_any = true, seen_some = false;
+        // windowed: whether this warpgroup's token, or any of the item's, sees
+        // the key of this thread's row
+        [[maybe_unused]] bool seen = true, seen_any = true;
         if constexpr (kWindow) {
           const int32_t x = pc.key_at(t, r);
           // (h is a multiple of 16, so the warpgroup's rows are one token's)
           seen = window_sees(pc.end_of_row(hb * kRowsPerCta + R * g), p.window, p.sinks, x);
           seen_any = pc.any_sees(x);
-          seen_some = pc.some_see(x);
         }
         if (is_fp8(kMode) || ok) ok = mbar_wait(smem_u32(&sm->s_full), tile_ctr & 1, abort_flag, p.err);
         if constexpr (is_fp8(kMode)) {  // leave together (the barrier above)
@@ -1237,8 +1236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kWindow) {
           // a key that other tokens of the item do not see: what is not finite in it
           // becomes zero likewise (a token that does see it is NaN by its score)
-          const uint32_t some = __ballot_sync(0xffffffffu, seen_some);
-          if (some) finite_keys(some, kv_base + 2 * g * kChunkBytes + 32 * wq * 128);
+          if (p.plan.group > 1) {
+            const uint32_t some = __ballot_sync(0xffffffffu, pc.some_see(pc.key_at(t, r)));
+            if (some) finite_keys(some, kv_base + 2 * g * kChunkBytes + 32 * wq * 128);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
