@@ -5,12 +5,14 @@
 // Bound by memory for prompts (a row is read once and written once) and by
 // latency for a decode step.  Eight lanes own a token and hold its row in
 // registers (nine units of 16 bytes a lane), so the norm and the FP8 scales are
-// shuffles among neighbouring lanes.  65536 rows: bf16 cache 28 us = 5.9 TB/s (87
-// % of the copy rate); 656-byte cache 38 us (52 %) and 528-byte cache 27 us (64
-// %), where encoding a row takes longer than moving it.  (Quotients by the
-// reciprocal, with a division only next to a border between two codes: 36.6 us;
-// not worth its second path.)  A decode step takes 3 to 5 us whatever its rows:
-// launch, then lengths, page entry, row, one after the other.
+// shuffles among neighbouring lanes.  65536 rows: bf16 cache 28 us = 6.0 TB/s (88
+// % of the copy rate); 656-byte cache 37.5 us (53 %) and 528-byte cache 27 us (66
+// %).  There 28 % (95 registers a thread) and 39 % of the warps are resident, too
+// few for one block's loads to overlap another's encoding; the arithmetic itself is
+// not the bound (quotients by the reciprocal, with a division only next to a border
+// between two codes: 36.6 of then 37.9 us; 64 registers a thread: 34.8, but 5.6
+// instead of 5.0 for a decode step; neither kept).  A decode step takes 3 to 5 us
+// whatever its rows: launch, then lengths, page entry, row, one after the other.
 #include "mla_rope.cuh"
 #include "mla_splitkv.cuh"
 

@@ -47,12 +47,14 @@
 // Windowed attention (kWindow, mla_window.cuh): the same two loops over pieces
 // that a row warp of each CTA works out, the query rows of every piece through
 // the key ring, scores of keys not seen masked in TMEM on the tiles that have
-// any.  Two tokens of 128 requests over 4096 keys: 279 us = 1.06 PFLOP/s, the
-// dense kernel's rate.  Short windows are bound by what a piece costs besides its
-// tiles: 64 requests over 128 keys 18 us, 256 requests 47; the output CTA's
-// chain is the longer one (unseen rows zeroed, P.V, the second tile's V in, P.V,
-// rows out).  Only the 8-key groups that hold a seen key loaded, by boxes of their
-// own: slower (51 for 50, and 106 for 83 over 4096 keys).
+// any.  Two tokens of 128 requests over 4096 keys: 277 us a call = 1.07 PFLOP/s (57
+// % of the bf16 rate), 15 us of it partial rows and their merge; without a window,
+// two tokens of 128 requests over 1k to 16k keys, this kernel runs at 1.10 to 1.17.
+// Short windows are bound by what a piece costs besides its tiles: 64 requests over
+// 128 keys 18 us, 256 requests 47; the output CTA's chain is the longer one (unseen
+// rows zeroed, P.V, the second tile's V in, P.V, rows out).  Only the 8-key groups
+// that hold a seen key loaded, by boxes of their own: slower (51 for 50, and 106 for
+// 83 over 4096 keys).
 //
 // Waits are bounded (mbar_wait*); after an abort every role keeps walking its
 // schedule without waiting, so the named barriers between warps 4..8 stay

@@ -38,14 +38,20 @@
 //
 // Windowed attention (kWindow, mla_window.cuh) runs the same loop over pieces
 // that one warp works out, with several tokens of a request in the 64 rows when
-// heads are few.  64 heads: 150 requests over 4000 keys take 149 us from the bf16
-// cache (4.8 TB/s, 70 % of the copy rate) and 221 us from the 656-byte cache:
-// there a tile's chain bounds it - slots free, codes arrive, eight chunks
-// converted, scores, softmax, P.V - at 6.9 us a tile, of which the conversion's
-// arithmetic is 1.2.  Rejected (from 233 us): two or four chunks converted
+// heads are few.  64 heads: 150 requests over 4000 keys take 158 us from the bf16
+// cache (4.5 TB/s, 67 % of the copy rate: shared memory holds one tile, whose chunks
+// are requested one by one as P.V of the tile before frees them), 230 us from the
+// 656-byte cache and 226 us from the 528-byte one: there a tile's chain bounds it -
+// slots free, codes arrive, eight chunks converted, scores, softmax, P.V - at 6.9 us
+// a tile, of which the conversion's arithmetic is 1.2.  Rejected (from 233 us): two or four chunks converted
 // between barriers (229 and 260 us; two head blocks 575 -> 612 and 685), scales
 // fetched once a tile (239), output rows in 16-byte pieces by lane exchanges
 // (64 requests over 128 keys 17.4 -> 18.9 us).
+//
+// Waits are bounded (mbar_wait*).  After an abort the producers and the MMA thread
+// leave their loops; softmax warps leave together (FP8 caches, by a vote) or go on
+// to the end without waiting and without writing; the work list is walked out, and
+// the block pauses for what is still in flight before it ends.
 #pragma once
 
 #include <cuda.h>
