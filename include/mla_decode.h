@@ -74,6 +74,8 @@ extern "C" {
 #define MLA_DEVERR_TIMEOUT 4u    /* an internal wait ran out (kernel bailed)  */
 #define MLA_DEVERR_METADATA 8u   /* metadata built for another shape (nothing *
                                   * was computed), or for other lengths      */
+#define MLA_DEVERR_BAD_RANGE 16u /* packed sequences that do not follow each   *
+                                  * other within the tensor's rows             */
 
 /* -------------------------------------------------------- KV cache formats */
 #define MLA_KV_BF16 0    /* [num_pages, 64, 576] bf16, 1152 B per token        */
@@ -505,6 +507,116 @@ int mla_window_decode(const void* q, const void* kv_cache, int kv_format, int64_
                       int h_q, int window, int sinks, float softmax_scale, const float* attn_sink,
                       int num_sm_parts, void* workspace, size_t workspace_bytes, void* out,
                       float* lse, uint32_t* err, cudaStream_t stream);
+
+/* ============================================================== prompts
+ *
+ * What a layer does with many new tokens at once.  Absorbed, a pair of query head
+ * and key costs 2 * (576 + 512) flops; with keys and values projected up per head it
+ * is 2 * (192 + 128), so prompts and long chunks run as ordinary attention per head:
+ * what is cached already is read back (mla_gather_kv), projected up by the caller's
+ * product, attended (mla_prefill), and where that is done in several pieces the
+ * pieces are joined (mla_merge_states).
+ *
+ * Packed sequences, common to the first two: sequence i owns rows cu[i] .. cu[i + 1] - 1
+ * of a packed tensor; cu is [batch + 1] int32 in device memory, cu[0] >= 0, no entry
+ * below the one before, the last at most the tensor's rows.  Sequences may be empty.
+ * Rows before the first sequence and behind the last are left as they were.
+ */
+
+/*
+ * Reads cached tokens back: out row cu_seqlens[i] + t = the cached row of request i's
+ * token starts[i] + t as bf16.
+ *
+ *  kv_cache, kv_format, num_pages, block_table, block_table_stride, max_pages: as for
+ *               mla_append_kv.
+ *  starts       optional [batch] int32 (NULL: zeros): the first token read of
+ *               each request; any position, not only a page's first.
+ *  rows         rows of out, at most 2^27.
+ *  out          [rows, 576] bf16 ([rows, 512] for MLA_KV_FP8_528), rows out_stride
+ *               elements apart (a multiple of 8).  MLA_KV_BF16: the row as it is.
+ *               MLA_KV_FP8_656: code * scale in fp32, rounded once; the position columns
+ *               as they are.  MLA_KV_FP8_528: code * scale, which is exact but where
+ *               it leaves bf16's range.
+ *  A position outside [0, 64 * max_pages), or a page entry outside [0, num_pages), sets
+ *  MLA_DEVERR_BAD_PAGE and its row is written as zeros.  With cu_seqlens that are not
+ *  as described, which rows are written is unspecified (none outside out).
+ *  out must not overlap the cache.
+ */
+int mla_gather_kv(const void* kv_cache, int kv_format, int64_t num_pages, const int32_t* block_table,
+                  int64_t block_table_stride, int64_t max_pages, const int32_t* cu_seqlens,
+                  const int32_t* starts, int batch, int64_t rows, void* out, int64_t out_stride,
+                  uint32_t* err, cudaStream_t stream);
+
+/*
+ * Size in bytes of mla_prefill's workspace for these arguments: 0, or fp32 partial
+ * outputs and LSEs when few blocks of query rows are cut along their keys to fill the
+ * device.  One workspace serves one call at a time.
+ */
+int mla_prefill_workspace_size(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k,
+                               int num_sm_parts, size_t* bytes);
+
+/*
+ * Attention of packed sequences, keys and values per head.  Query row r of sequence i
+ * attends, per head, to the sequence's own keys:
+ *     s_t = softmax_scale * (q[0:128] . k_t + q[128:192] . k_rope_t)
+ * and with causal != 0, of n queries and m keys, query j sees keys t <= j + m - n (the
+ * last sees all; the first n - m of a longer one see none); otherwise all m.
+ *
+ *  q            [total_q, h_q, 192] bf16, [total_q, h_q, 128] without k_rope
+ *  k            [total_k, h_k, 128] bf16; query head h uses key head h / (h_q / h_k)
+ *  k_rope       optional (NULL): [total_k, 64] bf16 position columns shared by all
+ *               heads (k_rope_head_stride = 0), or [total_k, h_k, 64]
+ *  v            [total_k, h_k, 128] bf16
+ *  out          [total_q, h_q, 128] bf16
+ *  lse          [h_q, total_q] fp32, ln sum e^s
+ *  Each tensor by its strides in elements from token to token and from head to head
+ *  (multiples of 8, at least the row's width; rows of out do not overlap), so keys and values may
+ *  lie beside each other in a projection's output, and the position columns in rows
+ *  of mla_gather_kv.
+ *  cu_seqlens_q, cu_seqlens_k: packed sequences (above) of q and out, and of k, k_rope
+ *               and v.  Others set MLA_DEVERR_BAD_RANGE; the rows they name are then taken as far
+ *               as they exist, and outputs are unspecified.
+ *  h_q / h_k    a whole number of 1 .. 128.  total_q, total_k: at most 2^27 rows.
+ *  num_sm_parts from mla_num_sm_parts for up to 64 heads (any value >= 1 gives the same
+ *               result up to rounding).
+ *  workspace    workspace_bytes bytes, at least mla_prefill_workspace_size(), 16-byte
+ *               aligned; NULL when that is 0.
+ *  A query that sees no key gets out = 0, lse = -inf.  What a query does not see leaves
+ *  no trace in its outputs, NaN and infinities included.  One that sees a key with a
+ *  NaN gets NaN in its whole row and lse, one that sees a value that is not finite gets it in
+ *  that column.  out must not overlap the inputs.
+ */
+int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                int64_t k_token_stride, int64_t k_head_stride, const void* k_rope,
+                int64_t k_rope_token_stride, int64_t k_rope_head_stride, const void* v,
+                int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_seqlens_q,
+                const int32_t* cu_seqlens_k, int batch, int64_t total_q, int64_t total_k, int h_q,
+                int h_k, float softmax_scale, int causal, int num_sm_parts, void* workspace,
+                size_t workspace_bytes, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                float* lse, uint32_t* err, cudaStream_t stream);
+
+/*
+ * Joins attention outputs over n disjoint sets of keys (mla_combine's formula, for states
+ * that a caller holds):
+ *     lse = ln sum_i e^lse_i,   out = sum_i e^(lse_i - lse) parts_i
+ *
+ *  parts        n x [tokens, h_q, d], bf16 or (parts_fp32 != 0) fp32, by strides in
+ *               elements from part to part, token to token, head to head (multiples of
+ *               16 bytes); d a multiple of 8 up to 512
+ *  lses         n x [h_q, tokens] fp32 by strides (mla_decode's [batch, h_q, 1] and
+ *               mla_prefill's [h_q, total_q] both fit)
+ *  out, lse     [tokens, h_q, d] bf16 and [h_q, tokens] fp32, by strides
+ *  tokens * h_q <= 2^31.  A part with lse_i = -inf has no weight and its row is not
+ *  read; a row without any other gets out = 0, lse = -inf.  out may be one of the parts itself with
+ *  the same strides, and lse its lse; otherwise outputs must not overlap inputs.  Sums are fp32,
+ *  each output rounded once.
+ */
+int mla_merge_states(const void* parts, int parts_fp32, int64_t part_stride, int64_t token_stride,
+                     int64_t head_stride, const float* lses, int64_t lse_part_stride,
+                     int64_t lse_head_stride, int64_t lse_token_stride, int n, int64_t tokens,
+                     int h_q, int d, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                     float* lse, int64_t out_lse_head_stride, int64_t out_lse_token_stride,
+                     cudaStream_t stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

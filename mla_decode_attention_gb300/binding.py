@@ -27,6 +27,7 @@ MLA_DEVERR_BAD_PAGE = 1
 MLA_DEVERR_BAD_INDEX = 2
 MLA_DEVERR_TIMEOUT = 4
 MLA_DEVERR_METADATA = 8
+MLA_DEVERR_BAD_RANGE = 16
 
 META_HEADER_WORDS = 16
 META_PART_WORDS = 8
@@ -68,6 +69,12 @@ _SIGS = {
     "mla_window_workspace_size": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "mla_window_decode": (_i, [_vp, _vp, _i, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp,
                                _i, _vp, _sz, _vp, _vp, _vp, _vp]),
+    "mla_gather_kv": (_i, [_vp, _i, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i64, _vp, _i64, _vp, _vp]),
+    "mla_prefill_workspace_size": (_i, [_i64, _i64, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "mla_prefill": (_i, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i64, _i64, _i, _i,
+                         _f, _i, _i, _vp, _sz, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "mla_merge_states": (_i, [_vp, _i, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _i, _i64, _i, _i, _vp, _i64, _i64, _vp, _i64,
+                              _i64, _vp]),
 }
 
 _lib = None
@@ -414,6 +421,51 @@ def mla_window_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_format: int, b
         raise MlaError("mla_window_decode", status)
 
 
+# ---------------------------------------------------------------- prompts
+
+def mla_gather_kv(kv_cache: torch.Tensor, kv_format: int, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                  out: torch.Tensor, starts: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Reads cached tokens back: row cu_seqlens[i] + t of out [rows, 576] bf16 ([rows, 512] for MLA_KV_FP8_528; unit
+    column stride) is request i's cached row of token starts[i] + t (starts [batch] int32; zeros when None).
+    cu_seqlens [batch + 1] int32; kv_cache, block_table: as for mla_append_kv.  Rows of no request stay as they were."""
+    status = (_step or _load_step()).gather_kv(kv_cache, kv_format, block_table, cu_seqlens, out, starts, err, stream)
+    if status != 0:
+        raise MlaError("mla_gather_kv", status)
+
+
+def mla_prefill_workspace_size(total_q: int, total_k: int, batch: int, h_q: int, h_k: int, num_sm_parts: int) -> int:
+    n = _sz()
+    _check("mla_prefill_workspace_size",
+           lib().mla_prefill_workspace_size(total_q, total_k, batch, h_q, h_k, num_sm_parts, ctypes.byref(n)))
+    return n.value
+
+
+def mla_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                softmax_scale: float, causal: bool, num_sm_parts: int, workspace: Optional[torch.Tensor], out: torch.Tensor,
+                lse: torch.Tensor, k_rope: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                stream=None) -> None:
+    """Attention of packed sequences, keys and values per head: q [total_q, h_q, 192] bf16, k and v [total_k, h_k, 128],
+    k_rope [total_k, 64] (shared by the heads) or [total_k, h_k, 64]; without k_rope q is [total_q, h_q, 128].  Any
+    strides of whole 16 bytes with unit column stride; query head h uses key head h // (h_q // h_k).  cu_seqlens_q,
+    cu_seqlens_k [batch + 1] int32; causal: a sequence's last query sees all its keys, the one before one less.  out
+    [total_q, h_q, 128] bf16, lse [h_q, total_q] float32 (0 and -inf for a query that sees no key).  workspace:
+    mla_prefill_workspace_size() bytes (None when that is 0), float32."""
+    status = (_step or _load_step()).prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, softmax_scale, causal, num_sm_parts,
+                                             workspace, out, lse, k_rope, err, stream)
+    if status != 0:
+        raise MlaError("mla_prefill", status)
+
+
+def mla_merge_states(parts: torch.Tensor, lses: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, stream=None) -> None:
+    """Joins attention outputs over disjoint sets of keys: parts [n, tokens, h_q, d] bf16 or float32 (unit column
+    stride), lses [n, h_q, tokens] float32 -> out [tokens, h_q, d] bf16, lse [h_q, tokens] float32.  out and lse may be
+    parts[i] and lses[i] themselves.  A part whose lse is -inf is not read."""
+    status = (_step or _load_step()).merge_states(parts, lses, out, lse, stream)
+    if status != 0:
+        raise MlaError("mla_merge_states", status)
+
+
 def mla_check_wait_timeout(err: torch.Tensor, stream=None) -> None:
     """Runs the library's bounded wait on a barrier nothing completes; the
     kernel ORs MLA_DEVERR_TIMEOUT into err (uint32 device word) after ~2 s."""
@@ -455,4 +507,18 @@ class WindowBuffers:
         self.workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=dev) if nbytes else None
         self.out = torch.empty(batch, s_q, h_q, 512, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(batch, h_q, s_q, dtype=torch.float32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+class PrefillBuffers:
+    """Device buffers of mla_prefill for one shape: workspace (None when the shape needs none), out, lse, err."""
+
+    def __init__(self, total_q: int, total_k: int, batch: int, h_q: int, h_k: int, device="cuda", num_sm_parts=None):
+        dev = torch.device(device)
+        idx = dev.index if dev.index is not None else torch.cuda.current_device()
+        self.num_sm_parts = num_sm_parts or mla_num_sm_parts(idx, 64)
+        nbytes = mla_prefill_workspace_size(total_q, total_k, batch, h_q, h_k, self.num_sm_parts)
+        self.workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=dev) if nbytes else None
+        self.out = torch.empty(total_q, h_q, 128, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(h_q, total_q, dtype=torch.float32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)

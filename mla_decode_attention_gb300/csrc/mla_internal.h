@@ -20,7 +20,19 @@ inline bool heads_supported(int h) {
 }
 inline int head_blocks(int h) { return (h + kHeadsPerCta - 1) / kHeadsPerCta; }
 
+// Most rows of a packed tensor (all its sequences together).
+constexpr int64_t kMaxPackedRows = int64_t{1} << 27;
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether rows of `width` elements, `token` apart from token to token and `head` from
+// head to head, do not overlap: heads lie within a token, or tokens within a head.
+inline bool rows_apart(int64_t tokens, int64_t heads, int64_t token, int64_t head, int64_t width) {
+  if (token < 0 || head < 0) return false;
+  const bool by_token = (heads == 1 || head >= width) && (tokens == 1 || token >= (heads - 1) * head + width);
+  const bool by_head = (tokens == 1 || token >= width) && (heads == 1 || head >= (tokens - 1) * token + width);
+  return by_token || by_head;
+}
 
 // Records a failed CUDA call for mla_last_error(); returns MLA_ERR_CUDA.
 int record_cuda_error(const char* where, cudaError_t e);

@@ -2,34 +2,13 @@
 // configuration, the cluster launches.
 #pragma once
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <atomic>
-#include <mutex>
-
-#include "mla_decode.h"
-#include "mla_internal.h"
+#include "mla_host.cuh"
 #include "mla_splitkv.cuh"
 #include "mla_pair.cuh"
 
 namespace mla {
 
 namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
 
 // 2-D bf16 row-major tensor [rows, cols] (cols = 576, or 512 for V4.1
 // queries) with row stride `stride_bytes`; boxes of [box_rows x 64 columns]
@@ -92,21 +71,6 @@ bool make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Lets a kernel have `bytes` of dynamic shared memory on the current device,
-// once per device (`done`: a bit per device; past 64 devices, every time).
-template <class Kernel>
-int allow_shared_memory(Kernel kernel, int bytes, std::atomic<uint64_t>* done, const char* what) {
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return record_cuda_error(what, e);
-  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
-  if (done->load(std::memory_order_acquire) & bit) return MLA_OK;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return record_cuda_error(what, e);
-  done->fetch_or(bit, std::memory_order_release);
-  return MLA_OK;
 }
 
 template <KvMode kMode, bool kWindow = false>

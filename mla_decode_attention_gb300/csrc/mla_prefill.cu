@@ -1,0 +1,213 @@
+// Entry points of the attention of packed sequences (mla_prefill.cuh).
+#include "mla_host.cuh"
+#include "mla_merge.cuh"
+#include "mla_prefill.cuh"
+
+namespace mla {
+
+namespace {
+
+using prefill::kKeys;
+using prefill::kNope;
+using prefill::kRope;
+using prefill::kRows;
+using prefill::kValue;
+
+// Parts that each block of query rows' keys are cut into: enough for the device when
+// there are few blocks, each part at least kLeastTiles key tiles on average (a part
+// costs its query rows, its fp32 rows and their merge).  Known without the lengths, so
+// that a workspace fits whatever they are.
+constexpr int kLeastTiles = 4, kMostSplits = 32;
+int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {
+  const int64_t per = 2 * (kRows / (h_q / h_k));
+  const int64_t blocks = (total_q + batch * (per - 1)) / per * h_k;
+  const int64_t tiles = total_k / batch / kKeys;
+  int64_t s = blocks > 0 ? num_sm_parts / blocks : 1;
+  if (s > tiles / kLeastTiles) s = tiles / kLeastTiles;
+  if (s > kMostSplits) s = kMostSplits;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+int check_sizes(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {
+  if (batch <= 0 || batch > (1 << 24) || total_q < 0 || total_q > kMaxPackedRows || total_k < 0 || total_k > kMaxPackedRows)
+    return MLA_ERR_SHAPE;
+  if (h_q <= 0 || h_k <= 0 || h_q % h_k != 0 || h_q / h_k > kRows || h_q > (1 << 16) || num_sm_parts <= 0) return MLA_ERR_SHAPE;
+  return MLA_OK;
+}
+
+// A tensor of packed rows seen as [tokens][heads][sub][cols]; boxes of `box_tokens`
+// tokens x 1 head x `sub` x 64 columns with 128-byte swizzle, three- or (sub > 0)
+// four-dimensional.
+bool make_packed_map(CUtensorMap* m, const void* base, int cols, int sub, int heads, int64_t tokens, int64_t sub_stride,
+                     int64_t head_stride, int64_t token_stride, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t box[4];
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  int n = 0, s = 0;
+  dims[n] = static_cast<cuuint64_t>(cols);
+  box[n++] = 64u;
+  if (sub > 0) {
+    dims[n] = static_cast<cuuint64_t>(sub);
+    box[n++] = static_cast<cuuint32_t>(sub);
+    strides[s++] = static_cast<cuuint64_t>(sub_stride) * 2u;
+  }
+  dims[n] = static_cast<cuuint64_t>(heads);
+  box[n++] = 1u;
+  strides[s++] = static_cast<cuuint64_t>(head_stride) * 2u;
+  dims[n] = static_cast<cuuint64_t>(tokens);
+  box[n++] = static_cast<cuuint32_t>(box_tokens);
+  strides[s++] = static_cast<cuuint64_t>(token_stride) * 2u;
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(n), const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kHasRope>
+int launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& rope, const CUtensorMap& v,
+                   const prefill::Params& p, int blocks, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};  // per instantiation
+  const int rc = allow_shared_memory(prefill::mla_prefill_kernel<kHasRope>, prefill::kSmemBytes, &done,
+                                     "cudaFuncSetAttribute(prefill kernel)");
+  if (rc != MLA_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(prefill::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = prefill::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill::mla_prefill_kernel<kHasRope>, q, k, rope, v, p);
+  return e == cudaSuccess ? MLA_OK : record_cuda_error("prefill kernel launch", e);
+}
+
+// Strides that TMA takes: whole 16-byte units, rows that do not begin before the
+// last has ended (a dimension of one has none).
+bool stride_ok(int64_t stride, int64_t count, int64_t width) {
+  return count <= 1 || (stride >= width && stride <= kMaxTokenStride);
+}
+
+}  // namespace
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_prefill_workspace_size(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts,
+                                          size_t* bytes) {
+  if (!bytes) return MLA_ERR_NULL;
+  const int rc = check_sizes(total_q, total_k, batch, h_q, h_k, num_sm_parts);
+  if (rc != MLA_OK) return rc;
+  const int splits = splits_of(total_q, total_k, batch, h_q, h_k, num_sm_parts);
+  *bytes = splits > 1 ? static_cast<size_t>(splits) * total_q * h_q * (kValue + 1) * sizeof(float) : 0;
+  return MLA_OK;
+}
+
+extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                           int64_t k_head_stride, const void* k_rope, int64_t k_rope_token_stride, int64_t k_rope_head_stride,
+                           const void* v, int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_k, int batch, int64_t total_q, int64_t total_k, int h_q, int h_k,
+                           float softmax_scale, int causal, int num_sm_parts, void* workspace, size_t workspace_bytes, void* out,
+                           int64_t out_token_stride, int64_t out_head_stride, float* lse, uint32_t* err, cudaStream_t stream) {
+  const int rc = check_sizes(total_q, total_k, batch, h_q, h_k, num_sm_parts);
+  if (rc != MLA_OK) return rc;
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 1e30f)) return MLA_ERR_SHAPE;
+  if (total_q == 0) return MLA_OK;
+  if (!q || !cu_seqlens_q || !cu_seqlens_k || !out || !lse || (total_k > 0 && (!k || !v))) return MLA_ERR_NULL;
+  const int d_qk = k_rope ? kNope + kRope : kNope;
+  if (!stride_ok(q_token_stride, total_q, d_qk) || !stride_ok(q_head_stride, h_q, d_qk) ||
+      !stride_ok(k_token_stride, total_k, kNope) || !stride_ok(k_head_stride, h_k, kNope) ||
+      !stride_ok(v_token_stride, total_k, kValue) || !stride_ok(v_head_stride, h_k, kValue) ||
+      (k_rope && (!stride_ok(k_rope_token_stride, total_k, kRope) ||
+                  (k_rope_head_stride != 0 && !stride_ok(k_rope_head_stride, h_k, kRope)))) ||
+      out_token_stride > kMaxTokenStride || out_head_stride > kMaxTokenStride ||
+      !rows_apart(total_q, h_q, out_token_stride, out_head_stride, kValue))
+    return MLA_ERR_SHAPE;
+  // a dimension of one has no stride of its own: any that TMA takes
+  const auto st = [](int64_t stride, int64_t count, int64_t width) { return count > 1 ? stride : width; };
+  const int64_t q_token = st(q_token_stride, total_q, 192), q_head = st(q_head_stride, h_q, 192);
+  const int64_t k_token = st(k_token_stride, total_k, kNope), k_head = st(k_head_stride, h_k, kNope);
+  const int64_t v_token = st(v_token_stride, total_k, kValue), v_head = st(v_head_stride, h_k, kValue);
+  const bool rope_per_head = k_rope && k_rope_head_stride != 0 && h_k > 1;
+  const int64_t rope_token = st(k_rope_token_stride, total_k, kRope), rope_head = rope_per_head ? k_rope_head_stride : kRope;
+  const int64_t out_token = st(out_token_stride, total_q, kValue), out_head = st(out_head_stride, h_q, kValue);
+  const int64_t strides = q_token | q_head | k_token | k_head | v_token | v_head | out_token | out_head | (k_rope ? rope_token | rope_head : 0);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(k_rope) || !aligned16(v) || !aligned16(out) || !aligned16(workspace) ||
+      strides % 8 != 0)
+    return MLA_ERR_ALIGN;
+  const int splits = splits_of(total_q, total_k, batch, h_q, h_k, num_sm_parts);
+  const int64_t ws_rows = static_cast<int64_t>(splits) * total_q * h_q;
+  if (splits > 1) {
+    if (!workspace) return MLA_ERR_NULL;
+    if (workspace_bytes < static_cast<size_t>(ws_rows) * (kValue + 1) * sizeof(float)) return MLA_ERR_SHAPE;
+  }
+
+  const int group = h_q / h_k, tokens = kRows / group;
+  CUtensorMap m_q, m_k, m_rope, m_v;
+  bool ok = make_packed_map(&m_q, q, d_qk, group, h_k, total_q, q_head, q_head * group, q_token, tokens);
+  if (total_k > 0) {
+    ok = ok && make_packed_map(&m_k, k, kNope, 0, h_k, total_k, 0, k_head, k_token, kKeys) &&
+         make_packed_map(&m_v, v, kValue, 0, h_k, total_k, 0, v_head, v_token, kKeys);
+    m_rope = m_k;
+    if (k_rope) ok = ok && make_packed_map(&m_rope, k_rope, kRope, 0, rope_per_head ? h_k : 1, total_k, 0, rope_head, rope_token, kKeys);
+  } else {
+    m_k = m_v = m_rope = m_q;  // not read: no item has a key tile
+  }
+  if (!ok) return record_error("cuTensorMapEncodeTiled failed for q, k, k_rope or v", MLA_ERR_CUDA);
+
+  prefill::Params p = {};
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.batch = batch;
+  p.total_q = static_cast<int>(total_q);
+  p.total_k = static_cast<int>(total_k);
+  p.h_k = h_k;
+  p.group = group;
+  p.tokens = tokens;
+  p.causal = causal != 0;
+  p.rope_per_head = rope_per_head;
+  p.splits = splits;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.out_token = out_token;
+  p.out_head = out_head;
+  p.lse = lse;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_lse = splits > 1 ? p.ws_o + ws_rows * kValue : nullptr;
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.v_token = v_token;
+  p.v_head = v_head;
+  p.err = err;
+  const int64_t per = 2 * tokens, items = (total_q + batch * (per - 1)) / per * h_k * splits;
+  const int blocks = static_cast<int>(items < num_sm_parts ? items : num_sm_parts);
+  const int status = k_rope ? launch_prefill<true>(m_q, m_k, m_rope, m_v, p, blocks, stream)
+                            : launch_prefill<false>(m_q, m_k, m_rope, m_v, p, blocks, stream);
+  if (status != MLA_OK || splits == 1) return status;
+
+  merge::Params g = {};
+  g.parts = p.ws_o;
+  g.part_stride = total_q * h_q * kValue;
+  g.token_stride = static_cast<int64_t>(h_q) * kValue;
+  g.head_stride = kValue;
+  g.lses = p.ws_lse;
+  g.lse_part = h_q * total_q;
+  g.lse_head = total_q;
+  g.lse_token = 1;
+  g.n = splits;
+  g.heads = h_q;
+  g.d = kValue;
+  g.tokens = total_q;
+  g.rows_from = cu_seqlens_q;           // rows of no sequence stay as they were
+  g.rows_to = cu_seqlens_q + batch;
+  g.out = p.out;
+  g.out_token = out_token;
+  g.out_head = out_head;
+  g.lse = lse;
+  g.out_lse_head = total_q;
+  g.out_lse_token = 1;
+  return merge::launch_type<true>(g, stream);
+}

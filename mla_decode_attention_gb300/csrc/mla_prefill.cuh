@@ -1,0 +1,729 @@
+// Attention of packed sequences with keys and values per head (sm_103a): what a
+// prompt's tokens run before absorption pays.
+//
+//   s = scale * (q[0:128] . k + q[128:192] . k_rope),  out = sum softmax(s) v,
+//   lse = ln sum e^s
+//
+// over the keys t of the query's own sequence, causal to the sequences' ends or all
+// of them.  Absorbed, a pair of query head and key costs 2 * (576 + 512) flops; here 2
+// * (192 + 128).
+//
+// A block works on two tiles of 128 query rows and walks the sequence's keys in tiles
+// of 128.  A row is one (token, query head of the key head's group) pair, token by
+// token, so the heads that share keys fill a tile together.  TMEM holds S0, S1 (the
+// tiles' scores, overwritten by their probabilities in bf16) and O0, O1: all 512
+// columns.  While the softmax warps of one tile turn S into P, the tensor cores work on the
+// other tile's products; per key tile they need 2 * (768 + 512) cycles (192 columns of
+// q.k, 128 of p.v), the exponentials about half of that.
+//
+// The query rows stay in shared memory (96 KB); keys and values come through one ring of
+// 16 KB chunks [128 tokens x 64 columns] in the order K(0), V(0), K(1), V(1), ..., a
+// chunk of position columns shared by all heads being loaded by each block as K's
+// third.
+//
+// Roles (512 threads):
+//   warps 0..3, 4..7 : softmax of tile 0, of tile 1: thread r = query row r = TMEM lane r
+//   warps 8..11      : outputs of both tiles (O / l -> bf16, or an fp32 partial)
+//   warp 12          : lane 0 issues every product
+//   warp 13          : lane 0 issues every TMA load
+//   warp 14          : works out the block's next item of work from the lengths
+//   warp 15          : values that must not reach a product (see fix_values)
+//
+// Values of keys that a row does not see have weight 0, but 0 times what is not finite
+// is NaN.  Tiles with keys that some row of the block does not see (at most three an
+// item) therefore pass through warp 15 before the products may read them: what lies behind the
+// sequence's end becomes zeros, and in what some rows see and others do not, values
+// that are not finite do; the output warps then add those to the rows that see them.
+//
+// Waits are bounded; after one has run out every role leaves, and the block pauses
+// before it frees TMEM and ends.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstddef>
+
+#include "mla_decode.h"
+#include "mla_internal.h"
+#include "mla_ptx.cuh"
+
+namespace mla {
+namespace prefill {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 128;    // query rows of a tile
+constexpr int kKeys = 128;    // keys of a tile
+constexpr int kNope = 128, kRope = 64, kValue = 128;
+constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
+constexpr int kSmemData = 14 * kChunk;
+constexpr int kEdges = 4;     // more value tiles than the ring holds
+// Probabilities are taken against a reference that follows the row's maximum only
+// when that has grown by 2^8: sums and outputs stay far from fp32's limits, and O is
+// rescaled in the first few tiles alone.
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
+constexpr uint32_t kIdescPv = idesc_bf16(128, 128, false, true);
+constexpr uint32_t kIdescPvHalf = idesc_bf16(128, 64, false, true);
+// TMEM columns
+constexpr uint32_t kColS = 0, kColO = 256;
+
+struct Params {
+  const int32_t* cu_q;   // [batch + 1]
+  const int32_t* cu_k;
+  int batch, total_q, total_k;
+  int h_k, group;        // key heads, query heads of each
+  int tokens;            // tokens of a tile: 128 / group
+  int causal;
+  int rope_per_head;     // k_rope has a head dimension
+  int splits;
+  float scale_log2;      // softmax_scale * log2 e
+  __nv_bfloat16* out;
+  int64_t out_token, out_head;  // strides in elements
+  float* lse;            // [h_q, total_q]
+  float* ws_o;           // splits > 1: [splits, total_q, h_q, 128]
+  float* ws_lse;         // [splits, h_q, total_q]
+  const __nv_bfloat16* v;
+  int64_t v_token, v_head;
+  uint32_t* err;
+};
+
+// One piece of work: up to two tiles of query rows of one sequence and key head, and
+// the key tiles [first, first + n) of each.
+struct Item {
+  int32_t q_row;      // first token (of the packed rows)
+  int32_t n_tok;      // tokens, at most 2 * Params::tokens; 0: no more work
+  int32_t seen0;      // keys that the first token sees; one more per token up to k_len (causal)
+  int32_t k_row;      // the sequence's first key (of the packed rows)
+  int32_t k_len;
+  int32_t head;       // key head
+  int32_t split;
+  int32_t first;      // first key tile
+  int32_t n[2];       // key tiles of each tile of query rows
+  uint32_t odd;       // a value that is not finite was taken out
+};
+
+struct Shared {
+  uint64_t full[10], empty[10];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], sums_full[2], sums_free[2];
+  uint64_t item_full[2], item_empty[2];
+  uint64_t edge[kEdges];
+  Item items[2];
+  uint32_t tmem;
+  uint32_t abort;
+  float inv[2][kRows];  // 1 / (sum of a row's probabilities); 0 for a row that sees no key
+};
+constexpr int kSmemBytes = kSmemData + 1024 /* alignment */ + static_cast<int>(sizeof(Shared));
+static_assert(kSmemBytes <= 232448, "shared memory of a block");
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Keys that token `at` of an item sees.
+__device__ __forceinline__ int seen_by(const Item& it, int at, int causal) {
+  if (!causal) return it.k_len;
+  const int n = it.seen0 + at;
+  return n < 0 ? 0 : (n > it.k_len ? it.k_len : n);
+}
+
+// Whether some row of the item does not see a key of tile t (of the sequence's).
+__device__ __forceinline__ bool edge_tile(const Item& it, int t, int causal) {
+  return (t + 1) * kKeys > seen_by(it, 0, causal);
+}
+
+// Finds item `index` of the call (lanes of one warp together; `base`, `before`: where
+// the last search ended, sequences and items before them).  Items of a sequence lie
+// head by head, a head's blocks of query rows from the last (the most keys) to the
+// first, a block's splits beside each other.
+__device__ inline bool find_item(const Params& p, int64_t index, int& base, int64_t& before, Item& out, int lane) {
+  const int per = 2 * p.tokens, per_block = p.h_k * p.splits;
+  if (index < before) {
+    base = 0;
+    before = 0;
+  }
+  for (; base < p.batch; base += 32) {
+    const int i = base + lane;
+    int q0 = 0, q1 = 0, blocks = 0;
+    bool bad = false;
+    if (i < p.batch) {
+      q0 = p.cu_q[i];
+      q1 = p.cu_q[i + 1];
+      bad = q0 < 0 || q1 < q0 || q1 > p.total_q;
+      if (bad) {  // rows that exist, none twice as often as the lengths say
+        q0 = q0 < 0 ? 0 : (q0 > p.total_q ? p.total_q : q0);
+        q1 = q1 < q0 ? q0 : (q1 > p.total_q ? p.total_q : q1);
+      }
+      blocks = (q1 - q0 + per - 1) / per;
+    }
+    int64_t upto = static_cast<int64_t>(blocks) * per_block;
+    const int64_t mine = upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (bad && p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
+    const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+    const uint32_t hit = __ballot_sync(0xffffffffu, index < before + upto);
+    if (hit == 0u) {
+      before += all;
+      continue;
+    }
+    const int who = __ffs(hit) - 1;
+    if (lane == who) {
+      const int64_t local = index - before - (upto - mine);
+      const int per_head = blocks * p.splits;
+      const int head = static_cast<int>(local / per_head), rem = static_cast<int>(local % per_head);
+      const int block = blocks - 1 - rem / p.splits;
+      int k0 = p.cu_k[i], k1 = p.cu_k[i + 1];
+      if (k0 < 0 || k1 < k0 || k1 > p.total_k) {
+        if (p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
+        k0 = k0 < 0 ? 0 : (k0 > p.total_k ? p.total_k : k0);
+        k1 = k1 < k0 ? k0 : (k1 > p.total_k ? p.total_k : k1);
+      }
+      Item it;
+      const int at = block * per, q_len = q1 - q0;
+      it.q_row = q0 + at;
+      it.n_tok = q_len - at < per ? q_len - at : per;
+      it.k_row = k0;
+      it.k_len = k1 - k0;
+      it.seen0 = it.k_len - q_len + at + 1;
+      it.head = head;
+      it.split = rem % p.splits;
+      int tiles[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int last = (it.n_tok < (x + 1) * p.tokens ? it.n_tok : (x + 1) * p.tokens) - 1;  // the tile's last token
+        tiles[x] = last >= x * p.tokens ? (seen_by(it, last, p.causal) + kKeys - 1) / kKeys : 0;
+      }
+      const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+      it.first = static_cast<int>(static_cast<int64_t>(most) * it.split / p.splits);
+      const int end = static_cast<int>(static_cast<int64_t>(most) * (it.split + 1) / p.splits);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int e = tiles[x] < end ? tiles[x] : end;
+        it.n[x] = e > it.first ? e - it.first : 0;
+      }
+      it.odd = 0u;
+      out = it;
+    }
+    return true;
+  }
+  return false;
+}
+
+// Zeros what is not finite in a unit of eight values in shared memory; whether there was any.
+__device__ __forceinline__ bool take_out(uint32_t addr) {
+  const uint4 v = ld_shared_v4(addr);
+  const uint4 w = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+  const bool any = ((v.x ^ w.x) | (v.y ^ w.y) | (v.z ^ w.z) | (v.w ^ w.w)) != 0u;
+  if (any) st_shared_v4(addr, w.x, w.y, w.z, w.w);
+  return any;
+}
+
+// x * 0 + acc for two bf16: NaN from the first value that is not finite on.
+__device__ __forceinline__ uint32_t note_odd(uint32_t x, uint32_t acc) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  return r;
+}
+
+// The value tile at `lo`, `hi` (its two chunks) before products read it: rows from
+// `valid` on become zeros; in rows `seen` .. valid - 1, which some query rows see and
+// others do not, values that are not finite do.  Returns whether there were any.
+// A row's eight 16-byte units lie swizzled within its 128 bytes, so units are taken
+// as they come.
+__device__ inline bool fix_values(uint32_t lo, uint32_t hi, int seen, int valid, int lane) {
+  bool odd = false;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t at = c == 0 ? lo : hi;
+    for (int u = valid * 8 + lane; u < kKeys * 8; u += 32) st_shared_v4(at + 16 * u, 0u, 0u, 0u, 0u);
+    if (seen >= valid) continue;
+    uint32_t acc = 0u;
+    int u = seen * 8 + lane;
+    for (; u + 96 < valid * 8; u += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(at + 16 * (u + 32 * i));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc = note_odd(v[i].w, note_odd(v[i].z, note_odd(v[i].y, note_odd(v[i].x, acc))));
+    }
+    for (; u < valid * 8; u += 32) {
+      const uint4 v = ld_shared_v4(at + 16 * u);
+      acc = note_odd(v.w, note_odd(v.z, note_odd(v.y, note_odd(v.x, acc))));
+    }
+    if (__any_sync(0xffffffffu, (acc & 0x7F807F80u) != 0u)) {  // (a sum of zeros otherwise)
+      for (int w = seen * 8 + lane; w < valid * 8; w += 32) odd |= take_out(at + 16 * w);
+    }
+  }
+  return __any_sync(0xffffffffu, odd);
+}
+
+// kHasRope: 192 columns of q and k (three chunks a key tile, a ring of 8), else 128
+// (two chunks, a ring of 10).
+template <bool kHasRope>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_rope, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ Params p) {
+  constexpr int kQk = kHasRope ? 3 : 2;    // chunks of a tile's keys
+  constexpr int kPer = kQk + 2;            // of its keys and values
+  constexpr int kRing = 14 - 2 * kQk;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_base = base, ring = base + 2 * kQk * kChunk;
+  Shared* sm = reinterpret_cast<Shared*>(smem_raw + (base - smem_u32(smem_raw)) + kSmemData);
+  volatile uint32_t* abort_flag = &sm->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar(sm->full[i]), 1);
+      mbar_init(bar(sm->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(sm->q_full[i]), 1);
+      mbar_init(bar(sm->q_empty[i]), 1);
+      mbar_init(bar(sm->s_full[i]), 1);
+      mbar_init(bar(sm->p_ready[i]), 4);
+      mbar_init(bar(sm->o_full[i]), 1);
+      mbar_init(bar(sm->o_free[i]), 4);
+      mbar_init(bar(sm->sums_full[i]), 4);
+      mbar_init(bar(sm->sums_free[i]), 4);
+      mbar_init(bar(sm->item_full[i]), 1);
+      mbar_init(bar(sm->item_empty[i]), 15);  // warps 0..13 and 15
+    }
+    for (int i = 0; i < kEdges; ++i) mbar_init(bar(sm->edge[i]), 1);
+    sm->abort = 0u;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    if (kHasRope) tma_prefetch_desc(&tm_rope);
+  }
+  if (warp == 12) tmem_alloc(smem_u32(&sm->tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+
+  // The next item for this role, or false: no more (or an abort).  All lanes of a warp.
+  uint32_t it_n = 0;
+  const Item* it = sm->items;
+  auto next_item = [&]() -> bool {
+    const uint32_t slot = it_n & 1;
+    bool ok = mbar_wait(bar(sm->item_full[slot]), (it_n >> 1) & 1, abort_flag, p.err);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    it = &sm->items[slot];
+    return it->n_tok > 0;
+  };
+  auto done_item = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(sm->item_empty[it_n & 1]));
+    ++it_n;
+  };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+    const uint32_t t_s = t_lane + kColS + 128 * x, t_o = t_lane + kColO + 128 * x;
+    const int my_tok = r / p.group, my_sub = r % p.group;
+    const float sc = p.scale_log2;
+    uint32_t tiles = 0, items = 0;
+    bool ok = true;
+    while (ok && next_item()) {
+      const int n = it->n[x];
+      const int at = x * p.tokens + my_tok;
+      const int seen = seen_by(*it, at, p.causal);
+      const bool row = my_tok < p.tokens && at < it->n_tok;
+      float m = 0.f, lsum = 0.f, bsum = 0.f;
+      for (int i = 0; i < n; ++i, ++tiles) {
+        const int t = it->first + i;
+        ok = mbar_wait(bar(sm->s_full[x]), tiles & 1, abort_flag, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        float s[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, s[j]);
+        tmem_wait_ld();
+        if (edge_tile(*it, t, p.causal)) {
+          const int lim = seen - t * kKeys;
+#pragma unroll
+          for (int j = 0; j < 128; ++j) s[j >> 5][j & 31] = j < lim ? s[j >> 5][j & 31] : -INFINITY;
+        }
+        float u0 = fmaxf(s[0][0], s[0][1]), u1 = fmaxf(s[1][0], s[1][1]), u2 = fmaxf(s[2][0], s[2][1]), u3 = fmaxf(s[3][0], s[3][1]);
+#pragma unroll
+        for (int j = 2; j < 32; j += 2) {
+          u0 = fmax3(u0, s[0][j], s[0][j + 1]);
+          u1 = fmax3(u1, s[1][j], s[1][j + 1]);
+          u2 = fmax3(u2, s[2][j], s[2][j + 1]);
+          u3 = fmax3(u3, s[3][j], s[3][j + 1]);
+        }
+        const float top = fmax3(fmaxf(u0, u1), u2, u3) * sc;
+        if (i == 0) {
+          m = top == -INFINITY ? 0.f : top;
+        } else {
+          const bool move = top > m + kRescaleLog2;
+          if (__any_sync(0xffffffffu, move)) {
+            // (this tile's scores were issued after the last tile's p.v and have completed, so O holds every tile before)
+            const float alpha = move ? fast_exp2(m - top) : 1.f;
+            m = move ? top : m;
+            lsum *= alpha;
+            bsum *= alpha;
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+              float o[16];
+              tmem_ld16(t_o + 16 * j, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= alpha;
+              tmem_st16(t_o + 16 * j, o);
+            }
+          }
+        }
+        const float neg_m = -m;
+        float l0 = 0.f, l1 = 0.f;
+        uint32_t pk[4][16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float x0, x1;
+            asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5};"
+                " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+                : "=f"(x0), "=f"(x1) : "f"(s[j][2 * k]), "f"(s[j][2 * k + 1]), "f"(sc), "f"(neg_m));
+            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+            pk[j][k] = pack_bf16x2(e0, e1);
+            asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
+                : "+f"(l0), "+f"(l1) : "f"(e0), "f"(e1));
+          }
+          tmem_st16u(t_s + 16 * j, pk[j]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm->p_ready[x]));
+        // the rounded probabilities' sum, by which O is divided: off the products' way
+        float b0 = 0.f, b1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
+                : "+f"(b0), "+f"(b1)
+                : "f"(__uint_as_float(pk[j][k] << 16)), "f"(__uint_as_float(pk[j][k] & 0xFFFF0000u)));
+        lsum += l0 + l1;
+        bsum += b0 + b1;
+      }
+      if (!ok) break;
+      if (n > 0) {
+        const bool has = !(lsum <= 0.f);  // (NaN: a key that is not finite, no empty row)
+        if (row) {
+          const int64_t h = static_cast<int64_t>(it->head) * p.group + my_sub, tok = it->q_row + at;
+          const float l = has ? (m + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+          if (p.splits == 1)
+            p.lse[h * p.total_q + tok] = l;
+          else
+            p.ws_lse[(it->split * static_cast<int64_t>(p.h_k) * p.group + h) * p.total_q + tok] = l;
+        }
+        ok = mbar_wait(bar(sm->sums_free[x]), (items & 1) ^ 1, abort_flag, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        sm->inv[x][r] = has ? 1.f / bsum : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm->sums_full[x]));
+        ++items;
+      }
+      done_item();
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // ------------------------------------------------------------ outputs
+    const int r = threadIdx.x & 127;
+    const int my_tok = r / p.group, my_sub = r % p.group;
+    uint32_t items[2] = {0u, 0u};
+    bool ok = true;
+    while (ok && next_item()) {
+#pragma unroll 1
+      for (int x = 0; x < 2 && ok; ++x) {
+        const int at = x * p.tokens + my_tok;
+        const bool row = my_tok < p.tokens && at < it->n_tok;
+        const int64_t h = static_cast<int64_t>(it->head) * p.group + my_sub, tok = it->q_row + at;
+        const int64_t part = (static_cast<int64_t>(it->split) * p.total_q + tok) * p.h_k * p.group + h;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.out_token + h * p.out_head);
+        float4* ws = reinterpret_cast<float4*>(p.ws_o + part * kValue);
+        float inv = 0.f;
+        if (it->n[x] > 0) {
+          const uint32_t par = items[x] & 1;
+          ++items[x];
+          ok = mbar_wait(bar(sm->sums_full[x]), par, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          inv = sm->inv[x][r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sm->sums_free[x]));
+          ok = mbar_wait(bar(sm->o_full[x]), par, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        } else if (row) {  // no key: the softmax warps have nothing to say
+          if (p.splits == 1)
+            p.lse[h * p.total_q + tok] = -INFINITY;
+          else
+            p.ws_lse[(static_cast<int64_t>(it->split) * p.h_k * p.group + h) * p.total_q + tok] = -INFINITY;
+        }
+        const uint32_t t_o = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO + 128 * x;
+        // values that warp 15 took out, for the rows that see them
+        const bool odd = it->n[x] > 0 && *reinterpret_cast<const volatile uint32_t*>(&it->odd) != 0u;
+        int from = 0, upto = 0;
+        if (odd) {
+          const int low = seen_by(*it, 0, p.causal), end = (it->first + it->n[x]) * kKeys, mine = seen_by(*it, at, p.causal);
+          from = low > it->first * kKeys ? low : it->first * kKeys;
+          upto = mine < end ? mine : end;
+        }
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          float o[32];
+          if (it->n[x] > 0) {
+            tmem_ld32(t_o + 32 * j, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
+          if (odd && row && inv != 0.f) {
+            for (int t = from; t < upto; ++t) {
+              const __nv_bfloat16* v = p.v + static_cast<int64_t>(it->k_row + t) * p.v_token + it->head * p.v_head + 32 * j;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float f = __bfloat162float(v[k]);
+                if (!(fabsf(f) < INFINITY)) o[k] += f;
+              }
+            }
+          }
+          if (row) {
+            if (p.splits == 1) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                dst[4 * j + k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                            pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) ws[8 * j + k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+        }
+        if (it->n[x] > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sm->o_free[x]));
+        }
+      }
+      if (!ok) break;
+      done_item();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 12) {
+      // ---------------------------------------------------------- products
+      uint32_t chunk = 0;                 // of the ring: the item's first
+      uint32_t items[2] = {0u, 0u}, tiles[2] = {0u, 0u};
+      bool ok = true;
+      while (next_item()) {
+        if (lane == 0) {
+          const int n = it->n[0] > it->n[1] ? it->n[0] : it->n[1];
+          int k_here = 0;                 // key tiles that have been waited for
+          auto wait_full = [&](uint32_t c) {
+            ok = mbar_wait(bar(sm->full[c % kRing]), (c / kRing) & 1, abort_flag, p.err);
+            return ok;
+          };
+          // S(x) = Q(x) . K(i)^T
+          auto scores = [&](int x, int i) {
+            const uint32_t c0 = chunk + i * kPer;
+            if (i == 0 && !(ok = mbar_wait(bar(sm->q_full[x]), items[x] & 1, abort_flag, p.err))) return false;
+#pragma unroll
+            for (int c = 0; c < kQk; ++c) {
+              if (i >= k_here && !wait_full(c0 + c)) return false;
+              if (c == 0) tc_fence_after();
+              const uint64_t a = sw128_desc(q_base + (x * kQk + c) * kChunk, 16, 1024);
+              const uint64_t b = sw128_desc(ring + (c0 + c) % kRing * kChunk, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ss(tmem + kColS + 128 * x, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), kIdesc128, (c | k) != 0);
+            }
+            k_here = i + 1;
+            mma_commit(bar(sm->s_full[x]));
+            if (i == it->n[x] - 1) mma_commit(bar(sm->q_empty[x]));
+            return true;
+          };
+          auto release = [&](uint32_t c0, int count) {
+            for (int c = 0; c < count; ++c) mma_commit(bar(sm->empty[(c0 + c) % kRing]));
+          };
+          if (it->n[0] > 0) ok = scores(0, 0);
+          if (ok && it->n[1] > 0) ok = scores(1, 0);
+          if (ok && n > 0) release(chunk, kQk);
+          for (int i = 0; i < n && ok; ++i) {
+            const uint32_t v0 = chunk + i * kPer + kQk, s0 = v0 % kRing, s1 = (v0 + 1) % kRing;
+            const int last_x = i < it->n[1] ? 1 : 0;
+            bool v_here = false;
+#pragma unroll 1
+            for (int x = 0; x < 2 && ok; ++x) {
+              if (i >= it->n[x]) continue;
+              if (i == 0 && !(ok = mbar_wait(bar(sm->o_free[x]), (items[x] & 1) ^ 1, abort_flag, p.err))) break;
+              if (!v_here && !(wait_full(v0) && wait_full(v0 + 1))) break;
+              v_here = true;
+              if (!(ok = mbar_wait(bar(sm->p_ready[x]), tiles[x] & 1, abort_flag, p.err))) break;
+              ++tiles[x];
+              tc_fence_after();
+              // O(x) += P(x) . V(i); the chunks lie behind each other but where the ring wraps
+              const uint64_t b = sw128_desc(ring + s0 * kChunk, kChunk, 1024);
+              const uint32_t o = tmem + kColO + 128 * x, a = tmem + kColS + 128 * x;
+              if (s1 == s0 + 1) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_bf16_ts(o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPv, (i | k) != 0);
+              } else {
+                const uint64_t b1 = sw128_desc(ring + s1 * kChunk, kChunk, 1024);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  mma_bf16_ts(o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
+                  mma_bf16_ts(o + 64, a + 8 * k, b1 + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
+                }
+              }
+              if (i == it->n[x] - 1) {
+                mma_commit(bar(sm->o_full[x]));
+                ++items[x];
+              }
+              if (x == last_x) release(v0, 2);
+              if (i + 1 < it->n[x] && !scores(x, i + 1)) break;
+            }
+            if (ok && i + 1 < n) release(chunk + (i + 1) * kPer, kQk);
+          }
+          chunk += n * kPer;
+        }
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+        if (!ok) break;
+        done_item();
+      }
+    } else if (warp == 13) {
+      // ------------------------------------------------------------- loads
+      uint32_t chunk = 0, edges = 0, items[2] = {0u, 0u};
+      const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+      bool ok = true;
+      while (next_item()) {
+        if (lane == 0) {
+          const int n = it->n[0] > it->n[1] ? it->n[0] : it->n[1];
+          auto queries = [&](int x) {
+            if (it->n[x] == 0) return true;
+            if (!(ok = mbar_wait(bar(sm->q_empty[x]), (items[x] & 1) ^ 1, abort_flag, p.err))) return false;
+            ++items[x];
+            const uint32_t b = bar(sm->q_full[x]);
+            mbar_arrive_expect_tx(b, kQk * 128u * p.group * p.tokens);
+#pragma unroll
+            for (int c = 0; c < kQk; ++c)
+              tma_load_4d(q_base + (x * kQk + c) * kChunk, &tm_q, 64 * c, 0, it->head, it->q_row + x * p.tokens, b, once);
+            return true;
+          };
+          auto wait_empty = [&](uint32_t c) {
+            ok = mbar_wait(bar(sm->empty[c % kRing]), ((c / kRing) & 1) ^ 1, abort_flag, p.err);
+            return ok;
+          };
+          ok = queries(0);
+          for (int i = 0; i < n && ok; ++i) {
+            const int t = it->first + i, row = it->k_row + t * kKeys;
+            for (int c = 0; c < kQk && ok; ++c, ++chunk) {
+              if (!wait_empty(chunk)) break;
+              const uint32_t b = bar(sm->full[chunk % kRing]), to = ring + chunk % kRing * kChunk;
+              mbar_arrive_expect_tx(b, kChunk);
+              if (c < 2)
+                tma_load_3d(to, &tm_k, 64 * c, it->head, row, b, keep);
+              else
+                tma_load_3d(to, &tm_rope, 0, p.rope_per_head ? it->head : 0, row, b, keep);
+            }
+            if (ok && i == 0) ok = queries(1);
+            const bool edge = edge_tile(*it, t, p.causal);
+            const uint32_t e = bar(sm->edge[edges % kEdges]);
+            if (ok && edge && wait_empty(chunk) && wait_empty(chunk + 1)) {
+              mbar_arrive_expect_tx(e, 2 * kChunk);
+              ++edges;
+            }
+            for (int c = 0; c < 2 && ok; ++c, ++chunk) {
+              if (!edge && !wait_empty(chunk)) break;
+              // an edge tile's values complete on a barrier of warp 15's, which then completes the chunk's
+              const uint32_t b = edge ? e : bar(sm->full[chunk % kRing]);
+              if (!edge) mbar_arrive_expect_tx(b, kChunk);
+              tma_load_3d(ring + chunk % kRing * kChunk, &tm_v, 64 * c, it->head, row, b, keep);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
+        if (!ok) break;
+        done_item();
+      }
+    } else if (warp == 14) {
+      // ------------------------------------------------------------- items
+      int cursor = 0;
+      int64_t before = 0, index = blockIdx.x;
+      for (uint32_t k = 0;; ++k, index += gridDim.x) {
+        Item* slot = &sm->items[k & 1];
+        bool ok = mbar_wait(bar(sm->item_empty[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag, p.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const bool more = find_item(p, index, cursor, before, *slot, lane);
+        if (!more && lane == 0) slot->n_tok = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm->item_full[k & 1]));
+        if (!more) break;
+      }
+    } else {
+      // ------------------------------------- values that must not be multiplied
+      uint32_t chunk = 0, edges = 0;
+      bool ok = true;
+      while (ok && next_item()) {
+        const int n = it->n[0] > it->n[1] ? it->n[0] : it->n[1];
+        const int low = seen_by(*it, 0, p.causal);
+        for (int i = 0; i < n; ++i) {
+          const int t = it->first + i;
+          if (!edge_tile(*it, t, p.causal)) continue;
+          ok = mbar_wait(bar(sm->edge[edges % kEdges]), (edges / kEdges) & 1, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++edges;
+          const uint32_t s0 = (chunk + i * kPer + kQk) % kRing, s1 = (chunk + i * kPer + kQk + 1) % kRing;
+          const int valid = it->k_len - t * kKeys < kKeys ? it->k_len - t * kKeys : kKeys;
+          const int seen = low - t * kKeys > 0 ? low - t * kKeys : 0;
+          const bool odd = fix_values(ring + s0 * kChunk, ring + s1 * kChunk, seen, valid, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (odd) *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n & 1].odd) = 1u;
+            mbar_arrive(bar(sm->full[s0]));
+            mbar_arrive(bar(sm->full[s1]));
+          }
+        }
+        if (!ok) break;
+        chunk += n * kPer;
+        done_item();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) settle_after_abort();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace prefill
+}  // namespace mla

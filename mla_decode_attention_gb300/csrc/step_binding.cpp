@@ -1,6 +1,7 @@
 // Python module `_step`: argument checks and marshalling of the calls that a
 // serving loop makes for every layer and step (mla_append_kv,
-// mla_query_norm_rope, mla_window_decode).  They run for a few microseconds on
+// mla_query_norm_rope, mla_window_decode, mla_gather_kv, mla_prefill,
+// mla_merge_states).  They run for a few microseconds on
 // the GPU, and the same checks written in Python took longer than that (9 to 12
 // us a call in all on the Grace host, 3 so).  Each function returns the
 // status of the C function of the same name; a wrong tensor raises ValueError
@@ -254,10 +255,131 @@ PyObject* window_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A bfloat16 tensor [n, heads, d] with unit column stride.
+void packed(const at::Tensor& t, int64_t n, int64_t heads, int64_t d, const char* name, int device) {
+  on(t, device, name);
+  if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || t.size(0) != n || t.size(1) != heads || t.size(2) != d || t.stride(2) != 1)
+    refuse("%s must be a bfloat16 tensor [%lld, %lld, %lld] with unit column stride", name, static_cast<long long>(n),
+           static_cast<long long>(heads), static_cast<long long>(d));
+}
+
+// The starts of packed sequences; their number.
+const int32_t* starts_of(PyObject* o, const char* name, int device, int64_t* batch) {
+  const at::Tensor& t = tensor(o, name);
+  on(t, device, name);
+  if (t.scalar_type() != at::kInt || t.dim() != 1 || t.size(0) < 2 || !t.is_contiguous())
+    refuse("%s must be a contiguous int32 tensor [batch + 1]", name);
+  *batch = t.size(0) - 1;
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// kv_cache, kv_format, block_table, cu_seqlens, out, starts, err, stream
+PyObject* gather_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const at::Tensor &cache = tensor(a[0], "kv_cache"), &out = tensor(a[4], "out");
+    const int device = device_of(cache, "kv_cache"), format = narrow(a[1], "kv_format");
+    const int64_t d = cache_columns(cache, format, device);
+    on(out, device, "out");
+    if (out.scalar_type() != at::kBFloat16 || out.dim() != 2 || out.size(1) != d || out.stride(1) != 1)
+      refuse("out must be a bfloat16 tensor [rows, %d] with unit column stride", static_cast<int>(d));
+    int64_t b = 0;
+    const int32_t* cu = starts_of(a[3], "cu_seqlens", device, &b);
+    const Table bt = block_table(a[2], b, device);
+    const auto* starts = static_cast<const int32_t*>(vector(a[5], at::kInt, b, "starts", device, true));
+    auto* err = static_cast<uint32_t*>(vector(a[6], at::kInt, 1, "err", device, true));
+    const cudaStream_t stream = stream_of(a[7], device);
+    return launch(device, [&] {
+      return mla_gather_kv(cache.data_ptr(), format, cache.size(0), bt.data, bt.stride, bt.width, cu, starts, size(b), out.size(0),
+                           out.data_ptr(), out.size(0) > 1 ? out.stride(0) : d, err, stream);
+    });
+  });
+}
+
+// q, k, v, cu_seqlens_q, cu_seqlens_k, softmax_scale, causal, num_sm_parts, workspace, out, lse, k_rope, err, stream
+PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&] {
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &out = tensor(a[9], "out");
+    const int device = device_of(q, "q");
+    const bool has_rope = a[11] != Py_None;
+    if (q.dim() != 3 || k.dim() != 3) refuse("q and k must be [rows, heads, columns]");
+    const int64_t nq = q.size(0), h = q.size(1), nk = k.size(0), h_k = k.size(1);
+    packed(q, nq, h, has_rope ? 192 : 128, "q", device);
+    packed(k, nk, h_k, 128, "k", device);
+    packed(v, nk, h_k, 128, "v", device);
+    packed(out, nq, h, 128, "out", device);
+    const void* rope = nullptr;
+    int64_t rope_token = 0, rope_head = 0;
+    if (has_rope) {
+      const at::Tensor& r = tensor(a[11], "k_rope");
+      on(r, device, "k_rope");
+      const bool shared = r.dim() == 2;
+      if (r.scalar_type() != at::kBFloat16 || (r.dim() != 2 && r.dim() != 3) || r.size(0) != nk || r.size(r.dim() - 1) != 64 ||
+          r.stride(r.dim() - 1) != 1 || (!shared && r.size(1) != h_k))
+        refuse("k_rope must be a bfloat16 tensor [%lld, 64] or [%lld, %lld, 64] with unit column stride", static_cast<long long>(nk),
+               static_cast<long long>(nk), static_cast<long long>(h_k));
+      rope = r.data_ptr();
+      rope_token = r.stride(0);
+      rope_head = shared || h_k == 1 ? 0 : r.stride(1);
+    }
+    int64_t b = 0, b_k = 0;
+    const int32_t* cu_q = starts_of(a[3], "cu_seqlens_q", device, &b);
+    const int32_t* cu_k = starts_of(a[4], "cu_seqlens_k", device, &b_k);
+    if (b != b_k) refuse("cu_seqlens_q and cu_seqlens_k must be of one length");
+    auto* lse = static_cast<float*>(vector(a[10], at::kFloat, h * nq, "lse", device));
+    auto* err = static_cast<uint32_t*>(vector(a[12], at::kInt, 1, "err", device, true));
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    if (a[8] != Py_None) {
+      const at::Tensor& w = tensor(a[8], "workspace");
+      on(w, device, "workspace");
+      if (!w.is_contiguous()) refuse("workspace must be contiguous");
+      ws = w.data_ptr();
+      ws_bytes = w.nbytes();
+    }
+    const float scale = real(a[5]);
+    const int causal = PyObject_IsTrue(a[6]), parts = narrow(a[7], "num_sm_parts");
+    if (causal < 0) throw Refused();
+    const cudaStream_t stream = stream_of(a[13], device);
+    return launch(device, [&] {
+      return mla_prefill(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1), rope, rope_token, rope_head,
+                         v.data_ptr(), v.stride(0), v.stride(1), cu_q, cu_k, size(b), nq, nk, size(h), size(h_k), scale, causal, parts,
+                         ws, ws_bytes, out.data_ptr(), out.stride(0), out.stride(1), lse, err, stream);
+    });
+  });
+}
+
+// parts, lses, out, lse, stream
+PyObject* merge_states(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&] {
+    const at::Tensor &x = tensor(a[0], "parts"), &ls = tensor(a[1], "lses"), &out = tensor(a[2], "out"), &lse = tensor(a[3], "lse");
+    const int device = device_of(x, "parts");
+    on(ls, device, "lses");
+    on(lse, device, "lse");
+    if ((x.scalar_type() != at::kBFloat16 && x.scalar_type() != at::kFloat) || x.dim() != 4 || x.stride(3) != 1)
+      refuse("parts must be a bfloat16 or float32 tensor [n, tokens, h_q, d] with unit column stride");
+    const int64_t parts = x.size(0), tokens = x.size(1), h = x.size(2), d = x.size(3);
+    if (ls.scalar_type() != at::kFloat || ls.dim() != 3 || ls.size(0) != parts || ls.size(1) != h || ls.size(2) != tokens)
+      refuse("lses must be a float32 tensor [n, h_q, tokens]");
+    if (lse.scalar_type() != at::kFloat || lse.dim() != 2 || lse.size(0) != h || lse.size(1) != tokens)
+      refuse("lse must be a float32 tensor [h_q, tokens]");
+    packed(out, tokens, h, d, "out", device);
+    const cudaStream_t stream = stream_of(a[4], device);
+    return launch(device, [&] {
+      return mla_merge_states(x.data_ptr(), x.scalar_type() == at::kFloat, x.stride(0), x.stride(1), x.stride(2),
+                              static_cast<const float*>(ls.data_ptr()), ls.stride(0), ls.stride(1), ls.stride(2), size(parts), tokens,
+                              size(h), size(d), out.data_ptr(), out.stride(0), out.stride(1), static_cast<float*>(lse.data_ptr()),
+                              lse.stride(0), lse.stride(1), stream);
+    });
+  });
+}
+
 PyMethodDef methods[] = {
     {"append_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(append_kv)), METH_FASTCALL, nullptr},
     {"query_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(query_norm_rope)), METH_FASTCALL, nullptr},
     {"window_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(window_decode)), METH_FASTCALL, nullptr},
+    {"gather_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(gather_kv)), METH_FASTCALL, nullptr},
+    {"prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prefill)), METH_FASTCALL, nullptr},
+    {"merge_states", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(merge_states)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -451,3 +451,58 @@ def window_decode(q, kv_rows, block_table, cache_seqlens, new_lens, softmax_scal
                 o = o * sink_factor(l, np.asarray(attn_sink, dtype=np.float64))[:, None]
             out[bi, j], lse[bi, :, j] = o, l
     return out, lse
+
+
+# --------------------------------------------------------------------- prompts
+#
+# Cached rows read back, attention of packed sequences with keys and values per
+# head, and outputs over several sets of keys joined, from their definitions.
+
+def gather_rows(kv_rows, block_table, cu_seqlens, starts=None):
+    """kv_rows [pages, 64, d]: rows of tokens starts[i] + t of every request i, t < cu[i + 1] - cu[i], one request after
+    another (starts: zeros when None)."""
+    out = []
+    for i in range(len(cu_seqlens) - 1):
+        t = np.arange(cu_seqlens[i + 1] - cu_seqlens[i]) + (0 if starts is None else int(starts[i]))
+        out.append(kv_rows[np.asarray(block_table)[i, t // 64], t % 64])
+    return np.concatenate(out) if out else kv_rows[:0, 0]
+
+
+def packed_attention(q, k, v, cu_q, cu_k, softmax_scale, causal, k_rope=None):
+    """q [nq, h, d], k and v [nk, h_k, 128], k_rope [nk, 64] or [nk, h_k, 64] (the key's columns behind k's), all
+    float64.  Query j of a sequence of n, over m keys, sees keys t <= j + m - n (causal) or all.  Returns out [nq, h,
+    128], lse [h, nq], and the sums of weights times |v| (what a weight's relative error can change at most).  Rows of
+    no sequence are NaN."""
+    nq, h, _ = q.shape
+    h_k = k.shape[1]
+    out, lse, size = np.full((nq, h, v.shape[2]), np.nan), np.full((h, nq), np.nan), np.full((nq, h, v.shape[2]), np.nan)
+    for a, z, c, e in zip(cu_q[:-1], cu_q[1:], cu_k[:-1], cu_k[1:]):
+        n, m = z - a, e - c
+        see = np.arange(m)[None] <= (np.arange(n)[:, None] + m - n if causal else np.full((n, 1), m))
+        for j in range(h):
+            kv = j // (h // h_k)
+            key = k[c:e, kv]
+            if k_rope is not None:
+                key = np.concatenate([key, k_rope[c:e] if k_rope.ndim == 2 else k_rope[c:e, kv]], 1)
+            s = np.where(see, (q[a:z, j] @ key.T) * softmax_scale, -np.inf)
+            top = s.max(1, initial=-np.inf)
+            w = np.exp(s - np.where(np.isneginf(top), 0.0, top)[:, None])
+            total = w.sum(1)
+            some = total > 0
+            w = w / np.where(some, total, 1.0)[:, None]
+            with np.errstate(divide="ignore"):
+                lse[j, a:z] = np.where(some, np.where(some, top, 0.0) + np.log(total), -np.inf)
+            out[a:z, j], size[a:z, j] = w @ v[c:e, kv], w @ np.abs(v[c:e, kv])
+    return out, lse, size
+
+
+def merge_states(parts, lses):
+    """parts [n, tokens, h, d], lses [n, h, tokens]: outputs over disjoint sets of keys -> over all of them."""
+    top = lses.max(0)
+    ref = np.where(np.isneginf(top), 0.0, top)
+    w = np.exp(lses - ref)
+    total = w.sum(0)
+    with np.errstate(divide="ignore"):
+        lse = ref + np.log(total)
+    w = w / np.where(total > 0, total, 1.0)
+    return np.einsum("nht,nthd->thd", w, np.where(np.isneginf(lses).transpose(0, 2, 1)[..., None], 0.0, parts)), lse
