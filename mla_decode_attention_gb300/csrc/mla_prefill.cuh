@@ -263,6 +263,32 @@ __device__ inline bool fix_values(uint32_t lo, uint32_t hi, int seen, int valid,
   return __any_sync(0xffffffffu, odd);
 }
 
+// One lane of the warp, the same whenever the whole warp asks.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred e; elect.sync _|e, 0xffffffff; selp.u32 %0, 1, 0, e; }" : "=r"(r));
+  return r;
+}
+// Products and commits by the lane whose `leader` is set, in code that all lanes run.
+__device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(leader)
+      : "memory");
+}
+
 // kHasRope: 192 columns of q and k (three chunks a key tile, a ring of 8), else 128
 // (two chunks, a ring of 10).
 template <bool kHasRope>
@@ -361,15 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 128; ++j) s[j >> 5][j & 31] = j < lim ? s[j >> 5][j & 31] : -INFINITY;
         }
-        float u0 = fmaxf(s[0][0], s[0][1]), u1 = fmaxf(s[1][0], s[1][1]), u2 = fmaxf(s[2][0], s[2][1]), u3 = fmaxf(s[3][0], s[3][1]);
+        float u[8];
 #pragma unroll
-        for (int j = 2; j < 32; j += 2) {
-          u0 = fmax3(u0, s[0][j], s[0][j + 1]);
-          u1 = fmax3(u1, s[1][j], s[1][j + 1]);
-          u2 = fmax3(u2, s[2][j], s[2][j + 1]);
-          u3 = fmax3(u3, s[3][j], s[3][j + 1]);
+        for (int j = 0; j < 8; ++j) {
+          const float* v = s[j >> 1] + 16 * (j & 1);
+          u[j] = fmax3(v[0], v[1], v[2]);
+#pragma unroll
+          for (int k = 3; k < 15; k += 2) u[j] = fmax3(u[j], v[k], v[k + 1]);
+          u[j] = fmaxf(u[j], v[15]);
         }
-        const float top = fmax3(fmaxf(u0, u1), u2, u3) * sc;
+        const float top = fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmaxf(u[6], u[7])) * sc;
         if (i == 0) {
           m = top == -INFINITY ? 0.f : top;
         } else {
@@ -392,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float neg_m = -m;
-        float l0 = 0.f, l1 = 0.f;
+        float l[4][2] = {};  // (one chain of additions would take as long as the exponentials)
         uint32_t pk[4][16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -405,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
             pk[j][k] = pack_bf16x2(e0, e1);
             asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
-                : "+f"(l0), "+f"(l1) : "f"(e0), "f"(e1));
+                : "+f"(l[k & 3][0]), "+f"(l[k & 3][1]) : "f"(e0), "f"(e1));
           }
           tmem_st16u(t_s + 16 * j, pk[j]);
         }
@@ -414,16 +441,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm->p_ready[x]));
         // the rounded probabilities' sum, by which O is divided: off the products' way
-        float b0 = 0.f, b1 = 0.f;
+        float b[4][2] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
-                : "+f"(b0), "+f"(b1)
+                : "+f"(b[k & 3][0]), "+f"(b[k & 3][1])
                 : "f"(__uint_as_float(pk[j][k] << 16)), "f"(__uint_as_float(pk[j][k] & 0xFFFF0000u)));
-        lsum += l0 + l1;
-        bsum += b0 + b1;
+        lsum += (l[0][0] + l[0][1]) + (l[1][0] + l[1][1]) + ((l[2][0] + l[2][1]) + (l[3][0] + l[3][1]));
+        bsum += (b[0][0] + b[0][1]) + (b[1][0] + b[1][1]) + ((b[2][0] + b[2][1]) + (b[3][0] + b[3][1]));
       }
       if (!ok) break;
       if (n > 0) {
@@ -535,82 +562,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 12) {
       // ---------------------------------------------------------- products
+      // All lanes walk the same path and one of them issues: descriptors stay in uniform
+      // registers (with one lane alone in the loop a product took 124 cycles to issue,
+      // twice what the tensor cores need for it).
       uint32_t chunk = 0;                 // of the ring: the item's first
       uint32_t items[2] = {0u, 0u}, tiles[2] = {0u, 0u};
+      const uint32_t leader = elect_one();
       bool ok = true;
-      while (next_item()) {
-        if (lane == 0) {
-          const int n = it->n[0] > it->n[1] ? it->n[0] : it->n[1];
-          int k_here = 0;                 // key tiles that have been waited for
-          auto wait_full = [&](uint32_t c) {
-            ok = mbar_wait(bar(sm->full[c % kRing]), (c / kRing) & 1, abort_flag, p.err);
-            return ok;
-          };
-          // S(x) = Q(x) . K(i)^T
-          auto scores = [&](int x, int i) {
-            const uint32_t c0 = chunk + i * kPer;
-            if (i == 0 && !(ok = mbar_wait(bar(sm->q_full[x]), items[x] & 1, abort_flag, p.err))) return false;
+      auto wait = [&](uint64_t& b, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, p.err));
+        return ok;
+      };
+      while (ok && next_item()) {
+        const int n0 = __shfl_sync(0xffffffffu, it->n[0], 0), n1 = __shfl_sync(0xffffffffu, it->n[1], 0);
+        const int n = n0 > n1 ? n0 : n1;
+        int k_here = 0;                   // key tiles that have been waited for
+        auto wait_full = [&](uint32_t c) { return wait(sm->full[c % kRing], (c / kRing) & 1); };
+        // S(x) = Q(x) . K(i)^T
+        auto scores = [&](int x, int i) {
+          const uint32_t c0 = chunk + i * kPer;
+          if (i == 0 && !wait(sm->q_full[x], items[x] & 1)) return false;
 #pragma unroll
-            for (int c = 0; c < kQk; ++c) {
-              if (i >= k_here && !wait_full(c0 + c)) return false;
-              if (c == 0) tc_fence_after();
-              const uint64_t a = sw128_desc(q_base + (x * kQk + c) * kChunk, 16, 1024);
-              const uint64_t b = sw128_desc(ring + (c0 + c) % kRing * kChunk, 16, 1024);
+          for (int c = 0; c < kQk; ++c) {
+            if (i >= k_here && !wait_full(c0 + c)) return false;
+            if (c == 0) tc_fence_after();
+            const uint64_t a = sw128_desc(q_base + (x * kQk + c) * kChunk, 16, 1024);
+            const uint64_t b = sw128_desc(ring + (c0 + c) % kRing * kChunk, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16_ss(tmem + kColS + 128 * x, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), kIdesc128, (c | k) != 0);
-            }
-            k_here = i + 1;
-            mma_commit(bar(sm->s_full[x]));
-            if (i == it->n[x] - 1) mma_commit(bar(sm->q_empty[x]));
-            return true;
-          };
-          auto release = [&](uint32_t c0, int count) {
-            for (int c = 0; c < count; ++c) mma_commit(bar(sm->empty[(c0 + c) % kRing]));
-          };
-          if (it->n[0] > 0) ok = scores(0, 0);
-          if (ok && it->n[1] > 0) ok = scores(1, 0);
-          if (ok && n > 0) release(chunk, kQk);
-          for (int i = 0; i < n && ok; ++i) {
-            const uint32_t v0 = chunk + i * kPer + kQk, s0 = v0 % kRing, s1 = (v0 + 1) % kRing;
-            const int last_x = i < it->n[1] ? 1 : 0;
-            bool v_here = false;
-#pragma unroll 1
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (i >= it->n[x]) continue;
-              if (i == 0 && !(ok = mbar_wait(bar(sm->o_free[x]), (items[x] & 1) ^ 1, abort_flag, p.err))) break;
-              if (!v_here && !(wait_full(v0) && wait_full(v0 + 1))) break;
-              v_here = true;
-              if (!(ok = mbar_wait(bar(sm->p_ready[x]), tiles[x] & 1, abort_flag, p.err))) break;
-              ++tiles[x];
-              tc_fence_after();
-              // O(x) += P(x) . V(i); the chunks lie behind each other but where the ring wraps
-              const uint64_t b = sw128_desc(ring + s0 * kChunk, kChunk, 1024);
-              const uint32_t o = tmem + kColO + 128 * x, a = tmem + kColS + 128 * x;
-              if (s1 == s0 + 1) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mma_bf16_ts(o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPv, (i | k) != 0);
-              } else {
-                const uint64_t b1 = sw128_desc(ring + s1 * kChunk, kChunk, 1024);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  mma_bf16_ts(o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
-                  mma_bf16_ts(o + 64, a + 8 * k, b1 + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
-                }
-              }
-              if (i == it->n[x] - 1) {
-                mma_commit(bar(sm->o_full[x]));
-                ++items[x];
-              }
-              if (x == last_x) release(v0, 2);
-              if (i + 1 < it->n[x] && !scores(x, i + 1)) break;
-            }
-            if (ok && i + 1 < n) release(chunk + (i + 1) * kPer, kQk);
+            for (int k = 0; k < 4; ++k)
+              mma_ss_if(leader, tmem + kColS + 128 * x, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), kIdesc128, (c | k) != 0);
           }
-          chunk += n * kPer;
+          k_here = i + 1;
+          commit_if(leader, bar(sm->s_full[x]));
+          if (i == (x == 0 ? n0 : n1) - 1) commit_if(leader, bar(sm->q_empty[x]));
+          return true;
+        };
+        auto release = [&](uint32_t c0, int count) {
+          for (int c = 0; c < count; ++c) commit_if(leader, bar(sm->empty[(c0 + c) % kRing]));
+        };
+        // O(x) += P(x) . V(i); the chunks lie behind each other but where the ring wraps
+        auto values = [&](int x, int i) {
+          const uint32_t v0 = chunk + i * kPer + kQk, s0 = v0 % kRing, s1 = (v0 + 1) % kRing;
+          if (i == 0 && !wait(sm->o_free[x], (items[x] & 1) ^ 1)) return false;
+          if ((x == 0 || i >= n0) && !(wait_full(v0) && wait_full(v0 + 1))) return false;
+          if (!wait(sm->p_ready[x], tiles[x] & 1)) return false;
+          ++tiles[x];
+          tc_fence_after();
+          const uint64_t b = sw128_desc(ring + s0 * kChunk, kChunk, 1024);
+          const uint32_t o = tmem + kColO + 128 * x, a = tmem + kColS + 128 * x;
+          if (s1 == s0 + 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma_ts_if(leader, o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPv, (i | k) != 0);
+          } else {
+            const uint64_t b1 = sw128_desc(ring + s1 * kChunk, kChunk, 1024);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              mma_ts_if(leader, o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
+              mma_ts_if(leader, o + 64, a + 8 * k, b1 + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
+            }
+          }
+          if (i == (x == 0 ? n0 : n1) - 1) {
+            commit_if(leader, bar(sm->o_full[x]));
+            ++items[x];
+          }
+          if (x == (i < n1 ? 1 : 0)) release(v0, 2);
+          return true;
+        };
+        if (n0 > 0) ok = scores(0, 0);
+        if (ok && n1 > 0) ok = scores(1, 0);
+        if (ok && n > 0) release(chunk, kQk);
+        for (int i = 0; i < n && ok; ++i) {
+          if (i < n0 && !(values(0, i) && (i + 1 >= n0 || scores(0, i + 1)))) break;
+          if (i < n1 && !(values(1, i) && (i + 1 >= n1 || scores(1, i + 1)))) break;
+          if (i + 1 < n) release(chunk + (i + 1) * kPer, kQk);
         }
-        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
         if (!ok) break;
+        chunk += n * kPer;
         done_item();
       }
     } else if (warp == 13) {
