@@ -35,38 +35,48 @@ int check_sizes(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, i
   return MLA_OK;
 }
 
-// A tensor of packed rows seen as [tokens][heads][sub][cols]; boxes of `box_tokens`
-// tokens x 1 head x `sub` x 64 columns with 128-byte swizzle, three- or (sub > 0)
-// four-dimensional.
-bool make_packed_map(CUtensorMap* m, const void* base, int cols, int sub, int heads, int64_t tokens, int64_t sub_stride,
-                     int64_t head_stride, int64_t token_stride, int box_tokens) {
+// A bf16 tensor of `n` dimensions with 64-column rows in the first, `strides` elements
+// apart in the others; boxes of `box` rows with 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int n, const int64_t* dims, const int64_t* strides, const int* box) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[4], strides[3];
-  cuuint32_t box[4];
-  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  int n = 0, s = 0;
-  dims[n] = static_cast<cuuint64_t>(cols);
-  box[n++] = 64u;
-  if (sub > 0) {
-    dims[n] = static_cast<cuuint64_t>(sub);
-    box[n++] = static_cast<cuuint32_t>(sub);
-    strides[s++] = static_cast<cuuint64_t>(sub_stride) * 2u;
+  cuuint64_t d[5] = {64u}, st[4];
+  cuuint32_t b[5] = {64u};
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  for (int i = 0; i < n; ++i) {
+    d[i + 1] = static_cast<cuuint64_t>(dims[i]);
+    st[i] = static_cast<cuuint64_t>(strides[i]) * 2u;
+    b[i + 1] = static_cast<cuuint32_t>(box[i]);
   }
-  dims[n] = static_cast<cuuint64_t>(heads);
-  box[n++] = 1u;
-  strides[s++] = static_cast<cuuint64_t>(head_stride) * 2u;
-  dims[n] = static_cast<cuuint64_t>(tokens);
-  box[n++] = static_cast<cuuint32_t>(box_tokens);
-  strides[s++] = static_cast<cuuint64_t>(token_stride) * 2u;
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(n), const_cast<void*>(base), dims, strides, box, estr,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(n + 1), const_cast<void*>(base), d, st, b, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Query rows as [tokens][key heads][group][chunks][64]: boxes of a chunk of `box` tokens
+// of a key head's group, which land token by token.
+bool make_query_map(CUtensorMap* m, const void* base, int cols, int group, int h_k, int64_t tokens, int64_t head, int64_t token, int box_tokens) {
+  const int64_t dims[4] = {group, tokens, cols / 64, h_k}, strides[4] = {head, token, 64, head * group};
+  const int box[4] = {group, box_tokens, 1, 1};
+  return make_map(m, base, 4, dims, strides, box);
+}
+
+// Keys or values as [heads][2 chunks][tokens][64]: boxes of `chunks` chunks of 128 tokens of a head.
+bool make_key_map(CUtensorMap* m, const void* base, int heads, int64_t tokens, int64_t head, int64_t token, int chunks) {
+  const int64_t dims[3] = {tokens, 2, heads}, strides[3] = {token, 64, head};
+  const int box[3] = {kKeys, chunks, 1};
+  return make_map(m, base, 3, dims, strides, box);
+}
+
+// Position columns as [heads][tokens][64].
+bool make_rope_map(CUtensorMap* m, const void* base, int heads, int64_t tokens, int64_t head, int64_t token) {
+  const int64_t dims[2] = {tokens, heads}, strides[2] = {token, head};
+  const int box[2] = {kKeys, 1};
+  return make_map(m, base, 2, dims, strides, box);
+}
+
 template <bool kHasRope>
-int launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& rope, const CUtensorMap& v,
-                   const prefill::Params& p, int blocks, cudaStream_t stream) {
+int launch_prefill(const prefill::Maps& maps, const prefill::Params& p, int blocks, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};  // per instantiation
   const int rc = allow_shared_memory(prefill::mla_prefill_kernel<kHasRope>, prefill::kSmemBytes, &done,
                                      "cudaFuncSetAttribute(prefill kernel)");
@@ -81,7 +91,7 @@ int launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill::mla_prefill_kernel<kHasRope>, q, k, rope, v, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill::mla_prefill_kernel<kHasRope>, maps, p);
   return e == cudaSuccess ? MLA_OK : record_cuda_error("prefill kernel launch", e);
 }
 
@@ -147,15 +157,14 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   }
 
   const int group = h_q / h_k, tokens = kRows / group;
-  CUtensorMap m_q, m_k, m_rope, m_v;
-  bool ok = make_packed_map(&m_q, q, d_qk, group, h_k, total_q, q_head, q_head * group, q_token, tokens);
+  prefill::Maps maps;
+  bool ok = make_query_map(&maps.q, q, d_qk, group, h_k, total_q, q_head, q_token, tokens);
+  maps.k = maps.v = maps.rope = maps.k1 = maps.v1 = maps.q;  // (without keys not read: no item has a key tile)
   if (total_k > 0) {
-    ok = ok && make_packed_map(&m_k, k, kNope, 0, h_k, total_k, 0, k_head, k_token, kKeys) &&
-         make_packed_map(&m_v, v, kValue, 0, h_k, total_k, 0, v_head, v_token, kKeys);
-    m_rope = m_k;
-    if (k_rope) ok = ok && make_packed_map(&m_rope, k_rope, kRope, 0, rope_per_head ? h_k : 1, total_k, 0, rope_head, rope_token, kKeys);
-  } else {
-    m_k = m_v = m_rope = m_q;  // not read: no item has a key tile
+    ok = ok && make_key_map(&maps.k, k, h_k, total_k, k_head, k_token, 2) && make_key_map(&maps.v, v, h_k, total_k, v_head, v_token, 2);
+    if (k_rope)
+      ok = ok && make_rope_map(&maps.rope, k_rope, rope_per_head ? h_k : 1, total_k, rope_head, rope_token) &&
+           make_key_map(&maps.k1, k, h_k, total_k, k_head, k_token, 1) && make_key_map(&maps.v1, v, h_k, total_k, v_head, v_token, 1);
   }
   if (!ok) return record_error("cuTensorMapEncodeTiled failed for q, k, k_rope or v", MLA_ERR_CUDA);
 
@@ -184,8 +193,7 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   p.err = err;
   const int64_t per = 2 * tokens, items = (total_q + batch * (per - 1)) / per * h_k * splits;
   const int blocks = static_cast<int>(items < num_sm_parts ? items : num_sm_parts);
-  const int status = k_rope ? launch_prefill<true>(m_q, m_k, m_rope, m_v, p, blocks, stream)
-                            : launch_prefill<false>(m_q, m_k, m_rope, m_v, p, blocks, stream);
+  const int status = k_rope ? launch_prefill<true>(maps, p, blocks, stream) : launch_prefill<false>(maps, p, blocks, stream);
   if (status != MLA_OK || splits == 1) return status;
 
   merge::Params g = {};

@@ -57,11 +57,11 @@ constexpr int kKeys = 128;    // keys of a tile
 constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
 constexpr int kSmemData = 14 * kChunk;
-constexpr int kEdges = 4;     // more value tiles than the ring holds
+constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring holds parts of
 // Probabilities are taken against a reference that follows the row's maximum only
 // when that has grown by 2^8: sums and outputs stay far from fp32's limits, and O is
 // rescaled in the first few tiles alone.
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kRescaleLog2 = 8.f, kMoveSum = 256.f;
 constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescPv = idesc_bf16(128, 128, false, true);
 constexpr uint32_t kIdescPvHalf = idesc_bf16(128, 64, false, true);
@@ -88,6 +88,11 @@ struct Params {
   uint32_t* err;
 };
 
+struct Maps {
+  CUtensorMap q, k, rope, v;  // boxes of one chunk of query rows, both chunks of keys, of position columns, of values
+  CUtensorMap k1, v1;         // one chunk of keys, of values: where both would run past the ring's end
+};
+
 // One piece of work: up to two tiles of query rows of one sequence and key head, and
 // the key tiles [first, first + n) of each.
 struct Item {
@@ -104,10 +109,10 @@ struct Item {
 };
 
 struct Shared {
-  uint64_t full[10], empty[10];
+  uint64_t k_full[kDepth], k_empty[kDepth], v_full[kDepth], v_empty[kDepth];  // of a key tile's chunks
   uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], sums_full[2], sums_free[2];
   uint64_t item_full[2], item_empty[2];
-  uint64_t edge[kEdges];
+  uint64_t edge[kDepth];
   Item items[2];
   uint32_t tmem;
   uint32_t abort;
@@ -269,17 +274,23 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{ .reg .pred e; elect.sync _|e, 0xffffffff; selp.u32 %0, 1, 0, e; }" : "=r"(r));
   return r;
 }
+// Shared-memory operands (128-byte swizzle, 8-row groups 1024 bytes apart) by the lower
+// half of their descriptors; the upper is the same for all of them.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
 // Products and commits by the lane whose `leader` is set, in code that all lanes run.
-__device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      "{ .reg .pred p, q; .reg .b64 a, b; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; mov.b64 a, {%1, %6}; mov.b64 b, {%2, %6};"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader),
+      "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts_if(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts_if(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      "{ .reg .pred p, q; .reg .b64 b; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; mov.b64 b, {%2, %6};"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p; }" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader),
+      "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar) {
@@ -289,13 +300,21 @@ __device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar) {
       : "memory");
 }
 
+// 5-D tiled load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w, int32_t v,
+                                            uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // kHasRope: 192 columns of q and k (three chunks a key tile, a ring of 8), else 128
 // (two chunks, a ring of 10).
 template <bool kHasRope>
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_rope, const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ Params p) {
+    mla_prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   constexpr int kQk = kHasRope ? 3 : 2;    // chunks of a tile's keys
   constexpr int kPer = kQk + 2;            // of its keys and values
   constexpr int kRing = 14 - 2 * kQk;
@@ -308,9 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(bar(sm->full[i]), 1);
-      mbar_init(bar(sm->empty[i]), 1);
+    for (int i = 0; i < kDepth; ++i) {
+      mbar_init(bar(sm->k_full[i]), kHasRope ? 2 : 1);
+      mbar_init(bar(sm->k_empty[i]), 1);
+      mbar_init(bar(sm->v_full[i]), 1);
+      mbar_init(bar(sm->v_empty[i]), 1);
+      mbar_init(bar(sm->edge[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(sm->q_full[i]), 1);
@@ -324,13 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm->item_full[i]), 1);
       mbar_init(bar(sm->item_empty[i]), 15);  // warps 0..13 and 15
     }
-    for (int i = 0; i < kEdges; ++i) mbar_init(bar(sm->edge[i]), 1);
     sm->abort = 0u;
     fence_mbarrier_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-    if (kHasRope) tma_prefetch_desc(&tm_rope);
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+    if (kHasRope) {
+      tma_prefetch_desc(&maps.rope);
+      tma_prefetch_desc(&maps.k1);
+      tma_prefetch_desc(&maps.v1);
+    }
   }
   if (warp == 12) tmem_alloc(smem_u32(&sm->tmem), 512);
   tc_fence_before();
@@ -378,64 +403,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        float s[4][32];
+        const bool edge = edge_tile(*it, t, p.causal);
+        const int lim = seen - t * kKeys;
+        float l[4][2];  // (one chain of additions would take as long as the exponentials)
+        uint32_t pk[4][16];
+        for (bool again = true; again;) {
+          float s[4][32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, s[j]);
-        tmem_wait_ld();
-        if (edge_tile(*it, t, p.causal)) {
-          const int lim = seen - t * kKeys;
+          for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, s[j]);
+          tmem_wait_ld();
+          if (edge) {
 #pragma unroll
-          for (int j = 0; j < 128; ++j) s[j >> 5][j & 31] = j < lim ? s[j >> 5][j & 31] : -INFINITY;
-        }
-        float u[8];
+            for (int j = 0; j < 128; ++j) s[j >> 5][j & 31] = j < lim ? s[j >> 5][j & 31] : -INFINITY;
+          }
+          if (i == 0) {
+            float u[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float* v = s[j >> 1] + 16 * (j & 1);
-          u[j] = fmax3(v[0], v[1], v[2]);
+            for (int j = 0; j < 8; ++j) {
+              const float* v = s[j >> 1] + 16 * (j & 1);
+              u[j] = fmax3(v[0], v[1], v[2]);
 #pragma unroll
-          for (int k = 3; k < 15; k += 2) u[j] = fmax3(u[j], v[k], v[k + 1]);
-          u[j] = fmaxf(u[j], v[15]);
-        }
-        const float top = fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmaxf(u[6], u[7])) * sc;
-        if (i == 0) {
-          m = top == -INFINITY ? 0.f : top;
-        } else {
-          const bool move = top > m + kRescaleLog2;
-          if (__any_sync(0xffffffffu, move)) {
-            // (this tile's scores were issued after the last tile's p.v and have completed, so O holds every tile before)
-            const float alpha = move ? fast_exp2(m - top) : 1.f;
-            m = move ? top : m;
-            lsum *= alpha;
-            bsum *= alpha;
+              for (int k = 3; k < 15; k += 2) u[j] = fmax3(u[j], v[k], v[k + 1]);
+              u[j] = fmaxf(u[j], v[15]);
+            }
+            const float top = fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmaxf(u[6], u[7])) * sc;
+            m = top == -INFINITY ? 0.f : top;
+          }
+          const float neg_m = -m;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x0, x1;
+              asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5};"
+                  " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+                  : "=f"(x0), "=f"(x1) : "f"(s[j][2 * k]), "f"(s[j][2 * k + 1]), "f"(sc), "f"(neg_m));
+              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+              pk[j][k] = pack_bf16x2(e0, e1);
+              asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
+                  : "+f"(l[k & 3][0]), "+f"(l[k & 3][1]) : "f"(e0), "f"(e1));
+            }
+          }
+          l[0][0] = (l[0][0] + l[0][1]) + (l[1][0] + l[1][1]) + ((l[2][0] + l[2][1]) + (l[3][0] + l[3][1]));
+          // The row maximum of a later tile is looked for only where its probabilities sum
+          // past the bound, which one of them above it needs; the warp then takes
+          // the pass again where a reference moves.
+          again = false;
+          if (__any_sync(0xffffffffu, i > 0 && !(l[0][0] <= kMoveSum))) {
+            float top = -INFINITY;
 #pragma unroll 1
             for (int j = 0; j < 8; ++j) {
-              float o[16];
-              tmem_ld16(t_o + 16 * j, o);
+              float v[16];
+              tmem_ld16(t_s + 16 * j, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= alpha;
-              tmem_st16(t_o + 16 * j, o);
+              for (int k = 0; k < 16; ++k) top = fmaxf(top, 16 * j + k < lim ? v[k] : -INFINITY);
+            }
+            top *= sc;
+            const bool move = top > m + kRescaleLog2;
+            again = __any_sync(0xffffffffu, move);
+            if (again) {
+              // (this tile's scores were issued after the last tile's p.v and have completed: O holds every tile before)
+              const float alpha = move ? fast_exp2(m - top) : 1.f;
+              m = move ? top : m;
+              lsum *= alpha;
+              bsum *= alpha;
+#pragma unroll 1
+              for (int j = 0; j < 8; ++j) {
+                float o[16];
+                tmem_ld16(t_o + 16 * j, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                tmem_st16(t_o + 16 * j, o);
+              }
             }
           }
         }
-        const float neg_m = -m;
-        float l[4][2] = {};  // (one chain of additions would take as long as the exponentials)
-        uint32_t pk[4][16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x0, x1;
-            asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5};"
-                " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
-                : "=f"(x0), "=f"(x1) : "f"(s[j][2 * k]), "f"(s[j][2 * k + 1]), "f"(sc), "f"(neg_m));
-            const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-            pk[j][k] = pack_bf16x2(e0, e1);
-            asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
-                : "+f"(l[k & 3][0]), "+f"(l[k & 3][1]) : "f"(e0), "f"(e1));
-          }
-          tmem_st16u(t_s + 16 * j, pk[j]);
-        }
+        for (int j = 0; j < 4; ++j) tmem_st16u(t_s + 16 * j, pk[j]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -449,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
                 : "+f"(b[k & 3][0]), "+f"(b[k & 3][1])
                 : "f"(__uint_as_float(pk[j][k] << 16)), "f"(__uint_as_float(pk[j][k] & 0xFFFF0000u)));
-        lsum += (l[0][0] + l[0][1]) + (l[1][0] + l[1][1]) + ((l[2][0] + l[2][1]) + (l[3][0] + l[3][1]));
+        lsum += l[0][0];
         bsum += (b[0][0] + b[0][1]) + (b[1][0] + b[1][1]) + ((b[2][0] + b[2][1]) + (b[3][0] + b[3][1]));
       }
       if (!ok) break;
@@ -565,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // All lanes walk the same path and one of them issues: descriptors stay in uniform
       // registers (with one lane alone in the loop a product took 124 cycles to issue,
       // twice what the tensor cores need for it).
-      uint32_t chunk = 0;                 // of the ring: the item's first
+      uint32_t tile = 0;                  // key tiles of all items so far
       uint32_t items[2] = {0u, 0u}, tiles[2] = {0u, 0u};
       const uint32_t leader = elect_one();
       bool ok = true;
@@ -574,75 +622,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
       };
       while (ok && next_item()) {
-        const int n0 = __shfl_sync(0xffffffffu, it->n[0], 0), n1 = __shfl_sync(0xffffffffu, it->n[1], 0);
+        const int n0 = __reduce_max_sync(0xffffffffu, it->n[0]), n1 = __reduce_max_sync(0xffffffffu, it->n[1]);
         const int n = n0 > n1 ? n0 : n1;
-        int k_here = 0;                   // key tiles that have been waited for
-        auto wait_full = [&](uint32_t c) { return wait(sm->full[c % kRing], (c / kRing) & 1); };
-        // S(x) = Q(x) . K(i)^T
-        auto scores = [&](int x, int i) {
-          const uint32_t c0 = chunk + i * kPer;
-          if (i == 0 && !wait(sm->q_full[x], items[x] & 1)) return false;
+        // S(x) = Q(x) . K^T of tile t; `first` of the item, `fresh`: nobody has waited for the keys
+        auto scores = [&](int x, uint32_t t, bool first, bool fresh, bool last) {
+          if (first && !wait(sm->q_full[x], items[x] & 1)) return false;
+          if (fresh && !wait(sm->k_full[t % kDepth], (t / kDepth) & 1)) return false;
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < kQk; ++c) {
-            if (i >= k_here && !wait_full(c0 + c)) return false;
-            if (c == 0) tc_fence_after();
-            const uint64_t a = sw128_desc(q_base + (x * kQk + c) * kChunk, 16, 1024);
-            const uint64_t b = sw128_desc(ring + (c0 + c) % kRing * kChunk, 16, 1024);
+            const uint32_t a = desc_lo(q_base + (x * kQk + c) * kChunk, 16), b = desc_lo(ring + (t * kPer + c) % kRing * kChunk, 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss_if(leader, tmem + kColS + 128 * x, a + static_cast<uint64_t>(2 * k), b + static_cast<uint64_t>(2 * k), kIdesc128, (c | k) != 0);
+            for (int k = 0; k < 4; ++k) mma_ss_if(leader, tmem + kColS + 128 * x, a + 2 * k, b + 2 * k, kIdesc128, (c | k) != 0);
           }
-          k_here = i + 1;
           commit_if(leader, bar(sm->s_full[x]));
-          if (i == (x == 0 ? n0 : n1) - 1) commit_if(leader, bar(sm->q_empty[x]));
+          if (last) commit_if(leader, bar(sm->q_empty[x]));
           return true;
         };
-        auto release = [&](uint32_t c0, int count) {
-          for (int c = 0; c < count; ++c) commit_if(leader, bar(sm->empty[(c0 + c) % kRing]));
-        };
-        // O(x) += P(x) . V(i); the chunks lie behind each other but where the ring wraps
-        auto values = [&](int x, int i) {
-          const uint32_t v0 = chunk + i * kPer + kQk, s0 = v0 % kRing, s1 = (v0 + 1) % kRing;
-          if (i == 0 && !wait(sm->o_free[x], (items[x] & 1) ^ 1)) return false;
-          if ((x == 0 || i >= n0) && !(wait_full(v0) && wait_full(v0 + 1))) return false;
+        // O(x) += P(x) . V of tile t; the chunks lie behind each other but where the ring ends
+        auto values = [&](int x, uint32_t t, bool first, bool fresh, bool last, bool done) {
+          if (first && !wait(sm->o_free[x], (items[x] & 1) ^ 1)) return false;
+          if (fresh && !wait(sm->v_full[t % kDepth], (t / kDepth) & 1)) return false;
           if (!wait(sm->p_ready[x], tiles[x] & 1)) return false;
           ++tiles[x];
           tc_fence_after();
-          const uint64_t b = sw128_desc(ring + s0 * kChunk, kChunk, 1024);
+          const uint32_t s0 = (t * kPer + kQk) % kRing, b = desc_lo(ring + s0 * kChunk, kChunk);
           const uint32_t o = tmem + kColO + 128 * x, a = tmem + kColS + 128 * x;
-          if (s1 == s0 + 1) {
+          if (s0 + 1 < kRing) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mma_ts_if(leader, o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPv, (i | k) != 0);
+            for (int k = 0; k < 8; ++k) mma_ts_if(leader, o, a + 8 * k, b + 128 * k, kIdescPv, !first || k != 0);
           } else {
-            const uint64_t b1 = sw128_desc(ring + s1 * kChunk, kChunk, 1024);
+            const uint32_t b1 = desc_lo(ring, kChunk);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              mma_ts_if(leader, o, a + 8 * k, b + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
-              mma_ts_if(leader, o + 64, a + 8 * k, b1 + static_cast<uint64_t>(128 * k), kIdescPvHalf, (i | k) != 0);
+              mma_ts_if(leader, o, a + 8 * k, b + 128 * k, kIdescPvHalf, !first || k != 0);
+              mma_ts_if(leader, o + 64, a + 8 * k, b1 + 128 * k, kIdescPvHalf, !first || k != 0);
             }
           }
-          if (i == (x == 0 ? n0 : n1) - 1) {
+          if (last) {
             commit_if(leader, bar(sm->o_full[x]));
             ++items[x];
           }
-          if (x == (i < n1 ? 1 : 0)) release(v0, 2);
+          if (done) commit_if(leader, bar(sm->v_empty[t % kDepth]));
           return true;
         };
-        if (n0 > 0) ok = scores(0, 0);
-        if (ok && n1 > 0) ok = scores(1, 0);
-        if (ok && n > 0) release(chunk, kQk);
-        for (int i = 0; i < n && ok; ++i) {
-          if (i < n0 && !(values(0, i) && (i + 1 >= n0 || scores(0, i + 1)))) break;
-          if (i < n1 && !(values(1, i) && (i + 1 >= n1 || scores(1, i + 1)))) break;
-          if (i + 1 < n) release(chunk + (i + 1) * kPer, kQk);
+        if (n0 > 0) ok = scores(0, tile, true, true, n0 == 1);
+        if (ok && n1 > 0) ok = scores(1, tile, true, n0 == 0, n1 == 1);
+        if (ok && n > 0) commit_if(leader, bar(sm->k_empty[tile % kDepth]));
+        for (int i = 0; i < n && ok; ++i, ++tile) {
+          if (i < n0) {
+            if (!values(0, tile, i == 0, true, i == n0 - 1, i >= n1)) break;
+            if (i + 1 < n0 && !scores(0, tile + 1, false, true, i + 2 == n0)) break;
+          }
+          if (i < n1) {
+            if (!values(1, tile, i == 0, i >= n0, i == n1 - 1, true)) break;
+            if (i + 1 < n1 && !scores(1, tile + 1, false, i + 1 >= n0, i + 2 == n1)) break;
+          }
+          if (i + 1 < n) commit_if(leader, bar(sm->k_empty[(tile + 1) % kDepth]));
         }
         if (!ok) break;
-        chunk += n * kPer;
         done_item();
       }
     } else if (warp == 13) {
       // ------------------------------------------------------------- loads
-      uint32_t chunk = 0, edges = 0, items[2] = {0u, 0u};
+      // (a box costs its SM a fixed time besides its bytes: both chunks of keys, and of values, come in one)
+      uint32_t tile = 0, edges = 0, items[2] = {0u, 0u};
+      uint32_t parts = 0, freed = kRing;   // parts of tiles given back, chunks of the ring that may be written
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
       bool ok = true;
       while (next_item()) {
@@ -656,39 +701,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(b, kQk * 128u * p.group * p.tokens);
 #pragma unroll
             for (int c = 0; c < kQk; ++c)
-              tma_load_4d(q_base + (x * kQk + c) * kChunk, &tm_q, 64 * c, 0, it->head, it->q_row + x * p.tokens, b, once);
+              tma_load_5d(q_base + (x * kQk + c) * kChunk, &maps.q, 0, 0, it->q_row + x * p.tokens, c, it->head, b, once);
             return true;
           };
-          auto wait_empty = [&](uint32_t c) {
-            ok = mbar_wait(bar(sm->empty[c % kRing]), ((c / kRing) & 1) ^ 1, abort_flag, p.err);
+          // waits until the ring's first `upto` chunks of all have a place; tiles' keys and
+          // values are given back in turn
+          auto room = [&](uint32_t upto) {
+            while (ok && static_cast<int32_t>(upto - freed) > 0) {
+              const uint32_t t = parts >> 1;
+              ok = mbar_wait(bar(parts & 1 ? sm->v_empty[t % kDepth] : sm->k_empty[t % kDepth]), (t / kDepth) & 1, abort_flag, p.err);
+              freed += parts & 1 ? 2 : kQk;
+              ++parts;
+            }
             return ok;
           };
+          auto pair = [&](const CUtensorMap& both, const CUtensorMap& one, uint32_t chunk, int row, uint32_t b) {
+            const uint32_t slot = chunk % kRing;
+            mbar_arrive_expect_tx(b, 2 * kChunk);
+            if (kRing % 2 == 0 && kPer % 2 == 0) {  // (pairs never run past the ring's end)
+              tma_load_4d(ring + slot * kChunk, &both, 0, row, 0, it->head, b, keep);
+            } else if (slot + 1 < kRing) {
+              tma_load_4d(ring + slot * kChunk, &both, 0, row, 0, it->head, b, keep);
+            } else {
+              tma_load_4d(ring + slot * kChunk, &one, 0, row, 0, it->head, b, keep);
+              tma_load_4d(ring, &one, 0, row, 1, it->head, b, keep);
+            }
+          };
           ok = queries(0);
-          for (int i = 0; i < n && ok; ++i) {
+          for (int i = 0; i < n && ok; ++i, ++tile) {
             const int t = it->first + i, row = it->k_row + t * kKeys;
-            for (int c = 0; c < kQk && ok; ++c, ++chunk) {
-              if (!wait_empty(chunk)) break;
-              const uint32_t b = bar(sm->full[chunk % kRing]), to = ring + chunk % kRing * kChunk;
-              mbar_arrive_expect_tx(b, kChunk);
-              if (c < 2)
-                tma_load_3d(to, &tm_k, 64 * c, it->head, row, b, keep);
-              else
-                tma_load_3d(to, &tm_rope, 0, p.rope_per_head ? it->head : 0, row, b, keep);
+            const uint32_t c0 = tile * kPer;
+            if (!room(c0 + 2)) break;
+            pair(maps.k, maps.k1, c0, row, bar(sm->k_full[tile % kDepth]));
+            if (kHasRope) {
+              if (!room(c0 + 3)) break;
+              mbar_arrive_expect_tx(bar(sm->k_full[tile % kDepth]), kChunk);
+              tma_load_3d(ring + (c0 + 2) % kRing * kChunk, &maps.rope, 0, row, p.rope_per_head ? it->head : 0, bar(sm->k_full[tile % kDepth]), keep);
             }
-            if (ok && i == 0) ok = queries(1);
+            if (i == 0 && !queries(1)) break;
+            if (!room(c0 + kPer)) break;
+            // an edge tile's values complete on a barrier of warp 15's, which then completes the products'
             const bool edge = edge_tile(*it, t, p.causal);
-            const uint32_t e = bar(sm->edge[edges % kEdges]);
-            if (ok && edge && wait_empty(chunk) && wait_empty(chunk + 1)) {
-              mbar_arrive_expect_tx(e, 2 * kChunk);
-              ++edges;
-            }
-            for (int c = 0; c < 2 && ok; ++c, ++chunk) {
-              if (!edge && !wait_empty(chunk)) break;
-              // an edge tile's values complete on a barrier of warp 15's, which then completes the chunk's
-              const uint32_t b = edge ? e : bar(sm->full[chunk % kRing]);
-              if (!edge) mbar_arrive_expect_tx(b, kChunk);
-              tma_load_3d(ring + chunk % kRing * kChunk, &tm_v, 64 * c, it->head, row, b, keep);
-            }
+            pair(maps.v, maps.v1, c0 + kQk, row, edge ? bar(sm->edge[edges++ % kDepth]) : bar(sm->v_full[tile % kDepth]));
           }
         }
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
@@ -711,32 +765,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ------------------------------------- values that must not be multiplied
-      uint32_t chunk = 0, edges = 0;
+      uint32_t tile = 0, edges = 0;
       bool ok = true;
       while (ok && next_item()) {
         const int n = it->n[0] > it->n[1] ? it->n[0] : it->n[1];
         const int low = seen_by(*it, 0, p.causal);
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n; ++i, ++tile) {
           const int t = it->first + i;
           if (!edge_tile(*it, t, p.causal)) continue;
-          ok = mbar_wait(bar(sm->edge[edges % kEdges]), (edges / kEdges) & 1, abort_flag, p.err);
+          ok = mbar_wait(bar(sm->edge[edges % kDepth]), (edges / kDepth) & 1, abort_flag, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++edges;
-          const uint32_t s0 = (chunk + i * kPer + kQk) % kRing, s1 = (chunk + i * kPer + kQk + 1) % kRing;
+          const uint32_t c = tile * kPer + kQk;
           const int valid = it->k_len - t * kKeys < kKeys ? it->k_len - t * kKeys : kKeys;
           const int seen = low - t * kKeys > 0 ? low - t * kKeys : 0;
-          const bool odd = fix_values(ring + s0 * kChunk, ring + s1 * kChunk, seen, valid, lane);
+          const bool odd = fix_values(ring + c % kRing * kChunk, ring + (c + 1) % kRing * kChunk, seen, valid, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (odd) *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n & 1].odd) = 1u;
-            mbar_arrive(bar(sm->full[s0]));
-            mbar_arrive(bar(sm->full[s1]));
+            mbar_arrive(bar(sm->v_full[tile % kDepth]));
           }
         }
         if (!ok) break;
-        chunk += n * kPer;
         done_item();
       }
     }
