@@ -31,7 +31,10 @@ int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int
 int check_sizes(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {
   if (batch <= 0 || batch > (1 << 24) || total_q < 0 || total_q > kMaxPackedRows || total_k < 0 || total_k > kMaxPackedRows)
     return MLA_ERR_SHAPE;
+  // (the kernel counts blocks of query rows in 32 bits)
   if (h_q <= 0 || h_k <= 0 || h_q % h_k != 0 || h_q / h_k > kRows || h_q > (1 << 16) || num_sm_parts <= 0) return MLA_ERR_SHAPE;
+  const int64_t per = 2 * (kRows / (h_q / h_k));
+  if (((total_q + batch * (per - 1)) / per * h_k) > (int64_t{1} << 26)) return MLA_ERR_SHAPE;
   return MLA_OK;
 }
 
@@ -68,11 +71,11 @@ bool make_key_map(CUtensorMap* m, const void* base, int heads, int64_t tokens, i
   return make_map(m, base, 3, dims, strides, box);
 }
 
-// Position columns as [heads][tokens][64].
+// Position columns as [heads][1 chunk][tokens][64].
 bool make_rope_map(CUtensorMap* m, const void* base, int heads, int64_t tokens, int64_t head, int64_t token) {
-  const int64_t dims[2] = {tokens, heads}, strides[2] = {token, head};
-  const int box[2] = {kKeys, 1};
-  return make_map(m, base, 2, dims, strides, box);
+  const int64_t dims[3] = {tokens, 1, heads}, strides[3] = {token, 64, head};
+  const int box[3] = {kKeys, 1, 1};
+  return make_map(m, base, 3, dims, strides, box);
 }
 
 template <bool kHasRope>

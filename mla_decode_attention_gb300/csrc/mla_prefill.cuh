@@ -23,17 +23,17 @@
 //
 // Roles (512 threads):
 //   warps 0..3, 4..7 : softmax of tile 0, of tile 1: thread r = query row r = TMEM lane r
-//   warps 8..11      : outputs of both tiles (O / l -> bf16, or an fp32 partial)
-//   warp 12          : lane 0 issues every product
-//   warp 13          : lane 0 issues every TMA load
-//   warp 14          : works out the block's next item of work from the lengths
-//   warp 15          : values that must not reach a product (see fix_values)
+//   warps 8..11      : values that must not reach a product (fix_values), then outputs of
+//                      both tiles (O / l -> bf16, or an fp32 partial)
+//   warps 12, 13     : products of tile 0, of tile 1
+//   warp 14          : lane 0 issues every TMA load
+//   warp 15          : works out the block's next item of work from the lengths
 //
 // Values of keys that a row does not see have weight 0, but 0 times what is not finite
 // is NaN.  Tiles with keys that some row of the block does not see (at most three an
-// item) therefore pass through warp 15 before the products may read them: what lies behind the
+// item) therefore pass through warps 8..11 before the products may read them: what lies behind the
 // sequence's end becomes zeros, and in what some rows see and others do not, values
-// that are not finite do; the output warps then add those to the rows that see them.
+// that are not finite do; they are then added to the outputs of the rows that see them.
 //
 // Waits are bounded; after one has run out every role leaves, and the block pauses
 // before it frees TMEM and ends.
@@ -127,6 +127,24 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+// mbar_wait in few instructions: the roles' code together has to stay within the
+// instruction cache.  A wait that has run out sets *abort; the block reports it at its end.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+  uint32_t t0 = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    uint32_t now;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
+    if (t0 == 0) t0 = now | 1u;
+    if (now - t0 > static_cast<uint32_t>(kWaitTimeoutNs) && static_cast<int32_t>(now - t0) != -1) *abort = 1u;
+    if (*abort) return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void mbar_arrive_many(uint32_t bar, uint32_t count) {
+  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0], %1; }" ::"r"(bar), "r"(count) : "memory");
+}
+
 // Keys that token `at` of an item sees.
 __device__ __forceinline__ int seen_by(const Item& it, int at, int causal) {
   if (!causal) return it.k_len;
@@ -140,54 +158,50 @@ __device__ __forceinline__ bool edge_tile(const Item& it, int t, int causal) {
 }
 
 // Finds item `index` of the call (lanes of one warp together; `base`, `before`: where
-// the last search ended, sequences and items before them).  Items of a sequence lie
-// head by head, a head's blocks of query rows from the last (the most keys) to the
-// first, a block's splits beside each other.
-__device__ inline bool find_item(const Params& p, int64_t index, int& base, int64_t& before, Item& out, int lane) {
-  const int per = 2 * p.tokens, per_block = p.h_k * p.splits;
-  if (index < before) {
-    base = 0;
-    before = 0;
-  }
+// the last search ended, sequences and items before them; indexes grow).  Items of a
+// sequence lie head by head, a head's blocks of query rows from the last (the most keys)
+// to the first, a block's splits beside each other.
+__device__ __forceinline__ bool find_item(const Params& p, uint32_t index, int& base, uint32_t& before, Item& out, int lane) {
+  const int per = 2 * p.tokens;
   for (; base < p.batch; base += 32) {
     const int i = base + lane;
-    int q0 = 0, q1 = 0, blocks = 0;
+    int q0 = 0, q1 = 0;
     bool bad = false;
     if (i < p.batch) {
       q0 = p.cu_q[i];
       q1 = p.cu_q[i + 1];
       bad = q0 < 0 || q1 < q0 || q1 > p.total_q;
-      if (bad) {  // rows that exist, none twice as often as the lengths say
-        q0 = q0 < 0 ? 0 : (q0 > p.total_q ? p.total_q : q0);
-        q1 = q1 < q0 ? q0 : (q1 > p.total_q ? p.total_q : q1);
+      if (bad) {  // rows that exist
+        q0 = min(max(q0, 0), p.total_q);
+        q1 = min(max(q1, q0), p.total_q);
       }
-      blocks = (q1 - q0 + per - 1) / per;
     }
-    int64_t upto = static_cast<int64_t>(blocks) * per_block;
-    const int64_t mine = upto;
-#pragma unroll
+    const uint32_t blocks = static_cast<uint32_t>(q1 - q0 + per - 1) / per;
+    const uint32_t mine = blocks * (p.h_k * p.splits);
+    uint32_t upto = mine;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
     if (bad && p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
-    const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
-    const uint32_t hit = __ballot_sync(0xffffffffu, index < before + upto);
+    const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+    const uint32_t local = index - (before + upto - mine);  // within the lane's sequence, if below `mine`
+    const uint32_t hit = __ballot_sync(0xffffffffu, local < mine);
     if (hit == 0u) {
       before += all;
       continue;
     }
     const int who = __ffs(hit) - 1;
     if (lane == who) {
-      const int64_t local = index - before - (upto - mine);
-      const int per_head = blocks * p.splits;
-      const int head = static_cast<int>(local / per_head), rem = static_cast<int>(local % per_head);
+      const uint32_t per_head = blocks * p.splits;
+      const int head = local / per_head, rem = local % per_head;
       const int block = blocks - 1 - rem / p.splits;
       int k0 = p.cu_k[i], k1 = p.cu_k[i + 1];
       if (k0 < 0 || k1 < k0 || k1 > p.total_k) {
         if (p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
-        k0 = k0 < 0 ? 0 : (k0 > p.total_k ? p.total_k : k0);
-        k1 = k1 < k0 ? k0 : (k1 > p.total_k ? p.total_k : k1);
+        k0 = min(max(k0, 0), p.total_k);
+        k1 = min(max(k1, k0), p.total_k);
       }
       Item it;
       const int at = block * per, q_len = q1 - q0;
@@ -205,8 +219,8 @@ __device__ inline bool find_item(const Params& p, int64_t index, int& base, int6
         tiles[x] = last >= x * p.tokens ? (seen_by(it, last, p.causal) + kKeys - 1) / kKeys : 0;
       }
       const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
-      it.first = static_cast<int>(static_cast<int64_t>(most) * it.split / p.splits);
-      const int end = static_cast<int>(static_cast<int64_t>(most) * (it.split + 1) / p.splits);
+      it.first = most * it.split / p.splits;  // (2^20 tiles, 2^5 splits at most)
+      const int end = most * (it.split + 1) / p.splits;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int e = tiles[x] < end ? tiles[x] : end;
@@ -236,33 +250,32 @@ __device__ __forceinline__ uint32_t note_odd(uint32_t x, uint32_t acc) {
   return r;
 }
 
-// The value tile at `lo`, `hi` (its two chunks) before products read it: rows from
-// `valid` on become zeros; in rows `seen` .. valid - 1, which some query rows see and
-// others do not, values that are not finite do.  Returns whether there were any.
-// A row's eight 16-byte units lie swizzled within its 128 bytes, so units are taken
-// as they come.
-__device__ inline bool fix_values(uint32_t lo, uint32_t hi, int seen, int valid, int lane) {
+// The value tile at `lo`, `hi` (its two chunks) before products read it, by four warps:
+// rows from `valid` on become zeros; in rows `seen` .. valid - 1, which some query rows
+// see and others do not, values that are not finite do.  Returns whether the warp
+// found any.  A row's eight 16-byte units lie swizzled within its 128 bytes, so units
+// are taken as they come; each thread has eight of the tile's 2048.
+__device__ __forceinline__ bool fix_values(uint32_t lo, uint32_t hi, int seen, int valid, int thread) {
   bool odd = false;
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const uint32_t at = c == 0 ? lo : hi;
-    for (int u = valid * 8 + lane; u < kKeys * 8; u += 32) st_shared_v4(at + 16 * u, 0u, 0u, 0u, 0u);
-    if (seen >= valid) continue;
     uint32_t acc = 0u;
-    int u = seen * 8 + lane;
-    for (; u + 96 < valid * 8; u += 128) {
-      uint4 v[4];
+    uint4 v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(at + 16 * (u + 32 * i));
+    for (int i = 0; i < 8; ++i) v[i] = ld_shared_v4(at + 16 * (thread + 128 * i));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc = note_odd(v[i].w, note_odd(v[i].z, note_odd(v[i].y, note_odd(v[i].x, acc))));
-    }
-    for (; u < valid * 8; u += 32) {
-      const uint4 v = ld_shared_v4(at + 16 * u);
-      acc = note_odd(v.w, note_odd(v.z, note_odd(v.y, note_odd(v.x, acc))));
+    for (int i = 0; i < 8; ++i) {
+      const int u = thread + 128 * i;
+      if (u >= valid * 8)
+        st_shared_v4(at + 16 * u, 0u, 0u, 0u, 0u);
+      else
+        acc = note_odd(v[i].w, note_odd(v[i].z, note_odd(v[i].y, note_odd(v[i].x, acc))));
     }
     if (__any_sync(0xffffffffu, (acc & 0x7F807F80u) != 0u)) {  // (a sum of zeros otherwise)
-      for (int w = seen * 8 + lane; w < valid * 8; w += 32) odd |= take_out(at + 16 * w);
+#pragma unroll 1
+      for (int u = thread; u < valid * 8; u += 128)
+        if (u >= seen * 8) odd |= take_out(at + 16 * u);
     }
   }
   return __any_sync(0xffffffffu, odd);
@@ -278,6 +291,8 @@ __device__ __forceinline__ uint32_t elect_one() {
 // half of their descriptors; the upper is the same for all of them.
 constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
+// The same value in every lane, known to be so.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 // Products and commits by the lane whose `leader` is set, in code that all lanes run.
 __device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -329,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDepth; ++i) {
       mbar_init(bar(sm->k_full[i]), kHasRope ? 2 : 1);
-      mbar_init(bar(sm->k_empty[i]), 1);
-      mbar_init(bar(sm->v_full[i]), 1);
-      mbar_init(bar(sm->v_empty[i]), 1);
+      mbar_init(bar(sm->k_empty[i]), 2);
+      mbar_init(bar(sm->v_full[i]), 4);  // a load's arrival, three more; or four warps'
+      mbar_init(bar(sm->v_empty[i]), 2);
       mbar_init(bar(sm->edge[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -344,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm->sums_full[i]), 4);
       mbar_init(bar(sm->sums_free[i]), 4);
       mbar_init(bar(sm->item_full[i]), 1);
-      mbar_init(bar(sm->item_empty[i]), 15);  // warps 0..13 and 15
+      mbar_init(bar(sm->item_empty[i]), 15);  // all warps but the one that fills them
     }
     sm->abort = 0u;
     fence_mbarrier_init();
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Item* it = sm->items;
   auto next_item = [&]() -> bool {
     const uint32_t slot = it_n & 1;
-    bool ok = mbar_wait(bar(sm->item_full[slot]), (it_n >> 1) & 1, abort_flag, p.err);
+    bool ok = wait_for(bar(sm->item_full[slot]), (it_n >> 1) & 1, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
     it = &sm->items[slot];
     return it->n_tok > 0;
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = 0.f, lsum = 0.f, bsum = 0.f;
       for (int i = 0; i < n; ++i, ++tiles) {
         const int t = it->first + i;
-        ok = mbar_wait(bar(sm->s_full[x]), tiles & 1, abort_flag, p.err);
+        ok = wait_for(bar(sm->s_full[x]), tiles & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -407,64 +422,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim = seen - t * kKeys;
         float l[4][2];  // (one chain of additions would take as long as the exponentials)
         uint32_t pk[4][16];
-        for (bool again = true; again;) {
-          float s[4][32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld32(t_s + 32 * j, s[j]);
-          tmem_wait_ld();
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < 128; ++j) s[j >> 5][j & 31] = j < lim ? s[j >> 5][j & 31] : -INFINITY;
-          }
-          if (i == 0) {
-            float u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float* v = s[j >> 1] + 16 * (j & 1);
-              u[j] = fmax3(v[0], v[1], v[2]);
-#pragma unroll
-              for (int k = 3; k < 15; k += 2) u[j] = fmax3(u[j], v[k], v[k + 1]);
-              u[j] = fmaxf(u[j], v[15]);
-            }
-            const float top = fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmaxf(u[6], u[7])) * sc;
-            m = top == -INFINITY ? 0.f : top;
-          }
-          const float neg_m = -m;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) l[j][0] = l[j][1] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x0, x1;
-              asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5};"
-                  " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
-                  : "=f"(x0), "=f"(x1) : "f"(s[j][2 * k]), "f"(s[j][2 * k + 1]), "f"(sc), "f"(neg_m));
-              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-              pk[j][k] = pack_bf16x2(e0, e1);
-              asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
-                  : "+f"(l[k & 3][0]), "+f"(l[k & 3][1]) : "f"(e0), "f"(e1));
-            }
-          }
-          l[0][0] = (l[0][0] + l[0][1]) + (l[1][0] + l[1][1]) + ((l[2][0] + l[2][1]) + (l[3][0] + l[3][1]));
-          // The row maximum of a later tile is looked for only where its probabilities sum
-          // past the bound, which one of them above it needs; the warp then takes
-          // the pass again where a reference moves.
-          again = false;
-          if (__any_sync(0xffffffffu, i > 0 && !(l[0][0] <= kMoveSum))) {
+        // Scores of keys not seen become -inf in TMEM before the pass reads them, and the
+        // row maximum is taken on the way: on the tiles that have such keys, on an item's
+        // first, and on a later one only where its probabilities sum past the bound, which one of
+        // them above it needs.  Where a reference moves the warp then takes the pass again.
+        bool look = edge || i == 0, again = false;
+        while (true) {
+          if (look) {
             float top = -INFINITY;
 #pragma unroll 1
             for (int j = 0; j < 8; ++j) {
               float v[16];
               tmem_ld16(t_s + 16 * j, v);
               tmem_wait_ld();
+              if (edge) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) top = fmaxf(top, 16 * j + k < lim ? v[k] : -INFINITY);
+                for (int k = 0; k < 16; ++k) v[k] = 16 * j + k < lim ? v[k] : -INFINITY;
+                tmem_st16(t_s + 16 * j, v);
+              }
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) top = fmax3(top, v[k], v[k + 1]);
             }
+            tmem_wait_st();
             top *= sc;
-            const bool move = top > m + kRescaleLog2;
-            again = __any_sync(0xffffffffu, move);
-            if (again) {
+            if (i == 0) {
+              m = top == -INFINITY ? 0.f : top;
+            } else if (again) {
+              const bool move = top > m + kRescaleLog2;
+              if (!__any_sync(0xffffffffu, move)) break;
               // (this tile's scores were issued after the last tile's p.v and have completed: O holds every tile before)
               const float alpha = move ? fast_exp2(m - top) : 1.f;
               m = move ? top : m;
@@ -481,6 +466,31 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+          const float neg_m = -m;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) l[j][0] = l[j][1] = 0.f;
+          float s[2][32];  // 32 scores on their way while 32 are worked on
+          tmem_ld32(t_s, s[0]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j < 3) tmem_ld32(t_s + 32 * (j + 1), s[(j + 1) & 1]);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x0, x1;
+              asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5};"
+                  " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+                  : "=f"(x0), "=f"(x1) : "f"(s[j & 1][2 * k]), "f"(s[j & 1][2 * k + 1]), "f"(sc), "f"(neg_m));
+              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+              pk[j][k] = pack_bf16x2(e0, e1);
+              asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
+                  : "+f"(l[k & 3][0]), "+f"(l[k & 3][1]) : "f"(e0), "f"(e1));
+            }
+            if (j < 3) tmem_wait_ld();
+          }
+          l[0][0] = (l[0][0] + l[0][1]) + (l[1][0] + l[1][1]) + ((l[2][0] + l[2][1]) + (l[3][0] + l[3][1]));
+          if (again || i == 0 || !__any_sync(0xffffffffu, !(l[0][0] <= kMoveSum))) break;
+          look = again = true;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_st16u(t_s + 16 * j, pk[j]);
@@ -505,16 +515,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool has = !(lsum <= 0.f);  // (NaN: a key that is not finite, no empty row)
         if (row) {
           const int64_t h = static_cast<int64_t>(it->head) * p.group + my_sub, tok = it->q_row + at;
-          const float l = has ? (m + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+          const float l = has ? (m + __log2f(lsum)) * 0.69314718055994531f : -INFINITY;
           if (p.splits == 1)
             p.lse[h * p.total_q + tok] = l;
           else
             p.ws_lse[(it->split * static_cast<int64_t>(p.h_k) * p.group + h) * p.total_q + tok] = l;
         }
-        ok = mbar_wait(bar(sm->sums_free[x]), (items & 1) ^ 1, abort_flag, p.err);
+        ok = wait_for(bar(sm->sums_free[x]), (items & 1) ^ 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        sm->inv[x][r] = has ? 1.f / bsum : 0.f;
+        sm->inv[x][r] = has ? __frcp_rn(bsum) : 0.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm->sums_full[x]));
         ++items;
@@ -527,8 +537,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const int my_tok = r / p.group, my_sub = r % p.group;
     uint32_t items[2] = {0u, 0u};
+    uint32_t tile = 0, edges = 0;
     bool ok = true;
     while (ok && next_item()) {
+      // values that must not be multiplied: the item's last tiles, before its outputs
+      const int n = max(it->n[0], it->n[1]);
+      const int low = seen_by(*it, 0, p.causal);
+#pragma unroll 1
+      for (int i = max(0, low / kKeys - it->first); i < n; ++i) {
+        const int t = it->first + i;
+        ok = __all_sync(0xffffffffu, wait_for(bar(sm->edge[edges % kDepth]), (edges / kDepth) & 1, abort_flag));
+        if (!ok) break;
+        ++edges;
+        const uint32_t c = (tile + i) * kPer + kQk;
+        const bool odd = fix_values(ring + c % kRing * kChunk, ring + (c + 1) % kRing * kChunk, max(0, low - t * kKeys),
+                                    min(kKeys, it->k_len - t * kKeys), r);
+        if (odd) *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n & 1].odd) = 1u;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm->v_full[(tile + i) % kDepth]));
+      }
+      if (!ok) break;
+      tile += n;
 #pragma unroll 1
       for (int x = 0; x < 2 && ok; ++x) {
         const int at = x * p.tokens + my_tok;
@@ -541,13 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it->n[x] > 0) {
           const uint32_t par = items[x] & 1;
           ++items[x];
-          ok = mbar_wait(bar(sm->sums_full[x]), par, abort_flag, p.err);
+          ok = wait_for(bar(sm->sums_full[x]), par, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           inv = sm->inv[x][r];
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sm->sums_free[x]));
-          ok = mbar_wait(bar(sm->o_full[x]), par, abort_flag, p.err);
+          ok = wait_for(bar(sm->o_full[x]), par, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -558,43 +588,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.ws_lse[(static_cast<int64_t>(it->split) * p.h_k * p.group + h) * p.total_q + tok] = -INFINITY;
         }
         const uint32_t t_o = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO + 128 * x;
-        // values that warp 15 took out, for the rows that see them
-        const bool odd = it->n[x] > 0 && *reinterpret_cast<const volatile uint32_t*>(&it->odd) != 0u;
-        int from = 0, upto = 0;
-        if (odd) {
-          const int low = seen_by(*it, 0, p.causal), end = (it->first + it->n[x]) * kKeys, mine = seen_by(*it, at, p.causal);
-          from = low > it->first * kKeys ? low : it->first * kKeys;
-          upto = mine < end ? mine : end;
-        }
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          float o[32];
+        for (int j = 0; j < 8; ++j) {
+          float o[16];
           if (it->n[x] > 0) {
-            tmem_ld32(t_o + 32 * j, o);
+            tmem_ld16(t_o + 16 * j, o);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
-          if (odd && row && inv != 0.f) {
-            for (int t = from; t < upto; ++t) {
-              const __nv_bfloat16* v = p.v + static_cast<int64_t>(it->k_row + t) * p.v_token + it->head * p.v_head + 32 * j;
+          for (int k = 0; k < 16; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
+          if (!row) continue;
+          if (p.splits == 1) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float f = __bfloat162float(v[k]);
-                if (!(fabsf(f) < INFINITY)) o[k] += f;
-              }
-            }
-          }
-          if (row) {
-            if (p.splits == 1) {
+            for (int k = 0; k < 2; ++k)
+              dst[2 * j + k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                          pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+          } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                dst[4 * j + k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                            pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) ws[8 * j + k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            }
+            for (int k = 0; k < 4; ++k) ws[4 * j + k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
         if (it->n[x] > 0) {
@@ -602,160 +613,167 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sm->o_free[x]));
         }
+        // what was taken out, onto the rows that see it
+        if (it->n[x] > 0 && *reinterpret_cast<const volatile uint32_t*>(&it->odd) != 0u && row && inv != 0.f) {
+          const int low = seen_by(*it, 0, p.causal), end = (it->first + it->n[x]) * kKeys, mine = seen_by(*it, at, p.causal);
+          const int from = low > it->first * kKeys ? low : it->first * kKeys, upto = mine < end ? mine : end;
+#pragma unroll 1
+          for (int c = 0; c < kValue; ++c) {
+            const __nv_bfloat16* v = p.v + static_cast<int64_t>(it->k_row + from) * p.v_token + it->head * p.v_head + c;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int t = from; t < upto; ++t, v += p.v_token) {
+              const float f = __bfloat162float(*v);
+              if (!(fabsf(f) < INFINITY)) sum += f;
+            }
+            if (sum == 0.f) continue;
+            if (p.splits == 1)
+              reinterpret_cast<__nv_bfloat16*>(dst)[c] = __float2bfloat16(sum);
+            else
+              reinterpret_cast<float*>(ws)[c] = sum;
+          }
+        }
       }
       if (!ok) break;
       done_item();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 12) {
+    if (warp < 14) {
       // ---------------------------------------------------------- products
-      // All lanes walk the same path and one of them issues: descriptors stay in uniform
-      // registers (with one lane alone in the loop a product took 124 cycles to issue,
-      // twice what the tensor cores need for it).
+      // A warp for each tile of query rows: while one waits or fetches descriptors the other's
+      // products run (one warp for both left the tensor cores idle for a third of
+      // the time).  All lanes walk the same path and one of them issues, so that descriptors
+      // stay in uniform registers.  After an abort the loops run out without waiting.
+      const int x = warp - 12;
       uint32_t tile = 0;                  // key tiles of all items so far
-      uint32_t items[2] = {0u, 0u}, tiles[2] = {0u, 0u};
+      uint32_t items = 0, tiles = 0;      // of this tile of rows
       const uint32_t leader = elect_one();
-      bool ok = true;
-      auto wait = [&](uint64_t& b, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, p.err));
-        return ok;
-      };
-      while (ok && next_item()) {
-        const int n0 = __reduce_max_sync(0xffffffffu, it->n[0]), n1 = __reduce_max_sync(0xffffffffu, it->n[1]);
-        const int n = n0 > n1 ? n0 : n1;
-        // S(x) = Q(x) . K^T of tile t; `first` of the item, `fresh`: nobody has waited for the keys
-        auto scores = [&](int x, uint32_t t, bool first, bool fresh, bool last) {
-          if (first && !wait(sm->q_full[x], items[x] & 1)) return false;
-          if (fresh && !wait(sm->k_full[t % kDepth], (t / kDepth) & 1)) return false;
-          tc_fence_after();
+      const uint32_t a_q = uniform(desc_lo(q_base + x * kQk * kChunk, 16));
+      const uint32_t d_s = uniform(tmem + kColS + 128 * x), d_o = uniform(tmem + kColO + 128 * x);
+      auto wait = [&](uint64_t& b, uint32_t parity) { wait_for(bar(b), parity, abort_flag); };
+      while (next_item()) {
+        const int n = __reduce_max_sync(0xffffffffu, max(it->n[0], it->n[1])), mine = __reduce_max_sync(0xffffffffu, it->n[x]);
+#pragma unroll 1
+        for (int i = -1; i < n; ++i) {
+          // O += P . V of tile i; the chunks lie behind each other but where the ring ends
+          const uint32_t t = tile + i, o = t % kDepth;
+          if (i >= 0 && i < mine) {
+            const uint32_t s0 = (t * kPer + kQk) % kRing, b = uniform(desc_lo(ring + s0 * kChunk, kChunk));
+            if (i == 0) wait(sm->o_free[x], (items & 1) ^ 1);
+            wait(sm->v_full[o], (t / kDepth) & 1);
+            wait(sm->p_ready[x], tiles & 1);
+            ++tiles;
+            tc_fence_after();
+            if (s0 + 1 < kRing) {
 #pragma unroll
-          for (int c = 0; c < kQk; ++c) {
-            const uint32_t a = desc_lo(q_base + (x * kQk + c) * kChunk, 16), b = desc_lo(ring + (t * kPer + c) % kRing * kChunk, 16);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss_if(leader, tmem + kColS + 128 * x, a + 2 * k, b + 2 * k, kIdesc128, (c | k) != 0);
-          }
-          commit_if(leader, bar(sm->s_full[x]));
-          if (last) commit_if(leader, bar(sm->q_empty[x]));
-          return true;
-        };
-        // O(x) += P(x) . V of tile t; the chunks lie behind each other but where the ring ends
-        auto values = [&](int x, uint32_t t, bool first, bool fresh, bool last, bool done) {
-          if (first && !wait(sm->o_free[x], (items[x] & 1) ^ 1)) return false;
-          if (fresh && !wait(sm->v_full[t % kDepth], (t / kDepth) & 1)) return false;
-          if (!wait(sm->p_ready[x], tiles[x] & 1)) return false;
-          ++tiles[x];
-          tc_fence_after();
-          const uint32_t s0 = (t * kPer + kQk) % kRing, b = desc_lo(ring + s0 * kChunk, kChunk);
-          const uint32_t o = tmem + kColO + 128 * x, a = tmem + kColS + 128 * x;
-          if (s0 + 1 < kRing) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mma_ts_if(leader, o, a + 8 * k, b + 128 * k, kIdescPv, !first || k != 0);
-          } else {
-            const uint32_t b1 = desc_lo(ring, kChunk);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              mma_ts_if(leader, o, a + 8 * k, b + 128 * k, kIdescPvHalf, !first || k != 0);
-              mma_ts_if(leader, o + 64, a + 8 * k, b1 + 128 * k, kIdescPvHalf, !first || k != 0);
+              for (int k = 0; k < 8; ++k) mma_ts_if(leader, d_o, d_s + 8 * k, b + 128 * k, kIdescPv, i > 0 || k != 0);
+            } else {
+              const uint32_t b1 = uniform(desc_lo(ring, kChunk));
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) {
+                mma_ts_if(leader, d_o, d_s + 8 * k, b + 128 * k, kIdescPvHalf, i > 0 || k != 0);
+                mma_ts_if(leader, d_o + 64, d_s + 8 * k, b1 + 128 * k, kIdescPvHalf, i > 0 || k != 0);
+              }
             }
+            if (i == mine - 1) {
+              commit_if(leader, bar(sm->o_full[x]));
+              ++items;
+            }
+            commit_if(leader, bar(sm->v_empty[o]));
+          } else if (i >= 0) {
+            wait(sm->v_full[o], (t / kDepth) & 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sm->v_empty[o]));
           }
-          if (last) {
-            commit_if(leader, bar(sm->o_full[x]));
-            ++items[x];
+          // S = Q . K^T of the next, behind it (S lies where P did)
+          const uint32_t t1 = t + 1, o1 = t1 % kDepth;
+          if (i + 1 < mine) {
+            uint32_t b[kQk];
+#pragma unroll
+            for (int c = 0; c < kQk; ++c) b[c] = uniform(desc_lo(ring + (t1 * kPer + c) % kRing * kChunk, 16));
+            if (i < 0) wait(sm->q_full[x], items & 1);
+            wait(sm->k_full[o1], (t1 / kDepth) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kQk; ++c)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_ss_if(leader, d_s, a_q + c * (kChunk / 16) + 2 * k, b[c] + 2 * k, kIdesc128, (c | k) != 0);
+            commit_if(leader, bar(sm->s_full[x]));
+            if (i + 2 == mine) commit_if(leader, bar(sm->q_empty[x]));
+            commit_if(leader, bar(sm->k_empty[o1]));
+          } else if (i + 1 < n) {
+            wait(sm->k_full[o1], (t1 / kDepth) & 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sm->k_empty[o1]));
           }
-          if (done) commit_if(leader, bar(sm->v_empty[t % kDepth]));
-          return true;
-        };
-        if (n0 > 0) ok = scores(0, tile, true, true, n0 == 1);
-        if (ok && n1 > 0) ok = scores(1, tile, true, n0 == 0, n1 == 1);
-        if (ok && n > 0) commit_if(leader, bar(sm->k_empty[tile % kDepth]));
-        for (int i = 0; i < n && ok; ++i, ++tile) {
-          if (i < n0) {
-            if (!values(0, tile, i == 0, true, i == n0 - 1, i >= n1)) break;
-            if (i + 1 < n0 && !scores(0, tile + 1, false, true, i + 2 == n0)) break;
-          }
-          if (i < n1) {
-            if (!values(1, tile, i == 0, i >= n0, i == n1 - 1, true)) break;
-            if (i + 1 < n1 && !scores(1, tile + 1, false, i + 1 >= n0, i + 2 == n1)) break;
-          }
-          if (i + 1 < n) commit_if(leader, bar(sm->k_empty[(tile + 1) % kDepth]));
         }
-        if (!ok) break;
+        tile += n;
         done_item();
       }
-    } else if (warp == 13) {
+    } else if (warp == 14) {
       // ------------------------------------------------------------- loads
       // (a box costs its SM a fixed time besides its bytes: both chunks of keys, and of values, come in one)
-      uint32_t tile = 0, edges = 0, items[2] = {0u, 0u};
-      uint32_t parts = 0, freed = kRing;   // parts of tiles given back, chunks of the ring that may be written
+      uint32_t tile = 0, edges = 0, items = 0;  // items: a count of each tile of rows in 16 bits
+      uint32_t parts = 0, freed = kRing;         // parts of tiles given back, chunks of the ring that may be written
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
       bool ok = true;
       while (next_item()) {
         if (lane == 0) {
-          const int n = it->n[0] > it->n[1] ? it->n[0] : it->n[1];
-          auto queries = [&](int x) {
-            if (it->n[x] == 0) return true;
-            if (!(ok = mbar_wait(bar(sm->q_empty[x]), (items[x] & 1) ^ 1, abort_flag, p.err))) return false;
-            ++items[x];
-            const uint32_t b = bar(sm->q_full[x]);
-            mbar_arrive_expect_tx(b, kQk * 128u * p.group * p.tokens);
-#pragma unroll
-            for (int c = 0; c < kQk; ++c)
-              tma_load_5d(q_base + (x * kQk + c) * kChunk, &maps.q, 0, 0, it->q_row + x * p.tokens, c, it->head, b, once);
-            return true;
-          };
-          // waits until the ring's first `upto` chunks of all have a place; tiles' keys and
-          // values are given back in turn
-          auto room = [&](uint32_t upto) {
-            while (ok && static_cast<int32_t>(upto - freed) > 0) {
-              const uint32_t t = parts >> 1;
-              ok = mbar_wait(bar(parts & 1 ? sm->v_empty[t % kDepth] : sm->k_empty[t % kDepth]), (t / kDepth) & 1, abort_flag, p.err);
-              freed += parts & 1 ? 2 : kQk;
-              ++parts;
-            }
-            return ok;
-          };
-          auto pair = [&](const CUtensorMap& both, const CUtensorMap& one, uint32_t chunk, int row, uint32_t b) {
-            const uint32_t slot = chunk % kRing;
-            mbar_arrive_expect_tx(b, 2 * kChunk);
-            if (kRing % 2 == 0 && kPer % 2 == 0) {  // (pairs never run past the ring's end)
-              tma_load_4d(ring + slot * kChunk, &both, 0, row, 0, it->head, b, keep);
-            } else if (slot + 1 < kRing) {
-              tma_load_4d(ring + slot * kChunk, &both, 0, row, 0, it->head, b, keep);
-            } else {
-              tma_load_4d(ring + slot * kChunk, &one, 0, row, 0, it->head, b, keep);
-              tma_load_4d(ring, &one, 0, row, 1, it->head, b, keep);
-            }
-          };
-          ok = queries(0);
+          const int n = max(it->n[0], it->n[1]);
           for (int i = 0; i < n && ok; ++i, ++tile) {
-            const int t = it->first + i, row = it->k_row + t * kKeys;
-            const uint32_t c0 = tile * kPer;
-            if (!room(c0 + 2)) break;
-            pair(maps.k, maps.k1, c0, row, bar(sm->k_full[tile % kDepth]));
-            if (kHasRope) {
-              if (!room(c0 + 3)) break;
-              mbar_arrive_expect_tx(bar(sm->k_full[tile % kDepth]), kChunk);
-              tma_load_3d(ring + (c0 + 2) % kRing * kChunk, &maps.rope, 0, row, p.rope_per_head ? it->head : 0, bar(sm->k_full[tile % kDepth]), keep);
+            const int t = it->first + i;
+            // queries 0, keys, queries 1, position columns, values
+#pragma unroll 1
+            for (int step = i == 0 ? 0 : 1; step < 5 && ok; ++step) {
+              if (step == 0 || step == 2) {
+                const int x = step >> 1;
+                if (i > 0 || it->n[x] == 0) continue;
+                ok = wait_for(bar(sm->q_empty[x]), ((items >> (16 * x)) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                items += 1u << (16 * x);
+                mbar_arrive_expect_tx(bar(sm->q_full[x]), kQk * 128u * p.group * p.tokens);
+#pragma unroll 1
+                for (int c = 0; c < kQk; ++c)
+                  tma_load_5d(q_base + (x * kQk + c) * kChunk, &maps.q, 0, 0, it->q_row + x * p.tokens, c, it->head, bar(sm->q_full[x]), once);
+                continue;
+              }
+              if (!kHasRope && step == 3) continue;
+              const uint32_t c = tile * kPer + (step == 1 ? 0 : (step == 3 ? 2 : kQk)), chunks = step == 3 ? 1 : 2;
+              // the ring's chunks are given back in turn, a tile's keys, then its values
+              while (ok && static_cast<int32_t>(c + chunks - freed) > 0) {
+                const uint32_t o = (parts >> 1) % kDepth;
+                ok = wait_for(bar(parts & 1 ? sm->v_empty[o] : sm->k_empty[o]), (parts / (2 * kDepth)) & 1, abort_flag);
+                freed += parts & 1 ? 2 : kQk;
+                ++parts;
+              }
+              if (!ok) break;
+              // an edge tile's values complete on a barrier of the output warps', which then complete the products'
+              const bool edge = step == 4 && edge_tile(*it, t, p.causal);
+              const uint32_t b = bar(edge ? sm->edge[edges % kDepth] : (step == 4 ? sm->v_full[tile % kDepth] : sm->k_full[tile % kDepth]));
+              edges += edge;
+              mbar_arrive_expect_tx(b, chunks * kChunk);
+              if (step == 4 && !edge) mbar_arrive_many(b, 3);
+              const uint32_t slot = c % kRing;
+              const bool wraps = kHasRope && chunks == 2 && slot + 1 == kRing;
+              const CUtensorMap* m = step == 3 ? &maps.rope : (step == 1 ? (wraps ? &maps.k1 : &maps.k) : (wraps ? &maps.v1 : &maps.v));
+              const int row = it->k_row + t * kKeys, head = step == 3 && !p.rope_per_head ? 0 : it->head;
+              tma_load_4d(ring + slot * kChunk, m, 0, row, 0, head, b, keep);
+              if (wraps) tma_load_4d(ring, m, 0, row, 1, head, b, keep);
             }
-            if (i == 0 && !queries(1)) break;
-            if (!room(c0 + kPer)) break;
-            // an edge tile's values complete on a barrier of warp 15's, which then completes the products'
-            const bool edge = edge_tile(*it, t, p.causal);
-            pair(maps.v, maps.v1, c0 + kQk, row, edge ? bar(sm->edge[edges++ % kDepth]) : bar(sm->v_full[tile % kDepth]));
           }
         }
         ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
         if (!ok) break;
         done_item();
       }
-    } else if (warp == 14) {
+    } else {
       // ------------------------------------------------------------- items
       int cursor = 0;
-      int64_t before = 0, index = blockIdx.x;
+      uint32_t before = 0, index = blockIdx.x;
       for (uint32_t k = 0;; ++k, index += gridDim.x) {
         Item* slot = &sm->items[k & 1];
-        bool ok = mbar_wait(bar(sm->item_empty[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag, p.err);
+        bool ok = wait_for(bar(sm->item_empty[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
         const bool more = find_item(p, index, cursor, before, *slot, lane);
         if (!more && lane == 0) slot->n_tok = 0;
@@ -763,40 +781,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(sm->item_full[k & 1]));
         if (!more) break;
       }
-    } else {
-      // ------------------------------------- values that must not be multiplied
-      uint32_t tile = 0, edges = 0;
-      bool ok = true;
-      while (ok && next_item()) {
-        const int n = it->n[0] > it->n[1] ? it->n[0] : it->n[1];
-        const int low = seen_by(*it, 0, p.causal);
-        for (int i = 0; i < n; ++i, ++tile) {
-          const int t = it->first + i;
-          if (!edge_tile(*it, t, p.causal)) continue;
-          ok = mbar_wait(bar(sm->edge[edges % kDepth]), (edges / kDepth) & 1, abort_flag, p.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ++edges;
-          const uint32_t c = tile * kPer + kQk;
-          const int valid = it->k_len - t * kKeys < kKeys ? it->k_len - t * kKeys : kKeys;
-          const int seen = low - t * kKeys > 0 ? low - t * kKeys : 0;
-          const bool odd = fix_values(ring + c % kRing * kChunk, ring + (c + 1) % kRing * kChunk, seen, valid, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (odd) *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n & 1].odd) = 1u;
-            mbar_arrive(bar(sm->v_full[tile % kDepth]));
-          }
-        }
-        if (!ok) break;
-        done_item();
-      }
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag) settle_after_abort();
+  if (*abort_flag) {
+    if (threadIdx.x == 0 && p.err) atomicOr(p.err, MLA_DEVERR_TIMEOUT);
+    settle_after_abort();
+  }
   if (warp == 12) {
     tc_fence_after();
     tmem_relinquish();
