@@ -656,23 +656,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = __reduce_max_sync(0xffffffffu, max(it->n[0], it->n[1])), mine = __reduce_max_sync(0xffffffffu, it->n[x]);
 #pragma unroll 1
         for (int i = -1; i < n; ++i) {
-          // O += P . V of tile i; the chunks lie behind each other but where the ring ends
-          const uint32_t t = tile + i, o = t % kDepth;
-          if (i >= 0 && i < mine) {
-            const uint32_t s0 = (t * kPer + kQk) % kRing, b = uniform(desc_lo(ring + s0 * kChunk, kChunk));
-            if (i == 0) wait(sm->o_free[x], (items & 1) ^ 1);
-            wait(sm->v_full[o], (t / kDepth) & 1);
+          // O += P . V of tile i, and behind it S = Q . K^T of the next (S lies where P did).  All
+          // that can be known before P is there is looked up before: the products then
+          // follow one another.
+          const uint32_t t = tile + i, o = t % kDepth, t1 = t + 1, o1 = t1 % kDepth;
+          const bool pv = i >= 0 && i < mine, qk = i + 1 < mine;
+          const uint32_t s0 = (t * kPer + kQk) % kRing, b_v = uniform(desc_lo(ring + s0 * kChunk, kChunk));
+          uint32_t b_k[kQk];
+#pragma unroll
+          for (int c = 0; c < kQk; ++c) b_k[c] = uniform(desc_lo(ring + (t1 * kPer + c) % kRing * kChunk, 16));
+          if (i == 0 && pv) wait(sm->o_free[x], (items & 1) ^ 1);
+          if (i >= 0) wait(sm->v_full[o], (t / kDepth) & 1);
+          if (i < 0 && qk) wait(sm->q_full[x], items & 1);
+          if (!kHasRope && i + 1 < n) wait(sm->k_full[o1], (t1 / kDepth) & 1);
+          if (pv) {
             wait(sm->p_ready[x], tiles & 1);
             ++tiles;
             tc_fence_after();
             if (s0 + 1 < kRing) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) mma_ts_if(leader, d_o, d_s + 8 * k, b + 128 * k, kIdescPv, i > 0 || k != 0);
-            } else {
+              for (int k = 0; k < 8; ++k) mma_ts_if(leader, d_o, d_s + 8 * k, b_v + 128 * k, kIdescPv, i > 0 || k != 0);
+            } else {  // the chunks lie behind each other but where the ring ends
               const uint32_t b1 = uniform(desc_lo(ring, kChunk));
 #pragma unroll 1
               for (int k = 0; k < 8; ++k) {
-                mma_ts_if(leader, d_o, d_s + 8 * k, b + 128 * k, kIdescPvHalf, i > 0 || k != 0);
+                mma_ts_if(leader, d_o, d_s + 8 * k, b_v + 128 * k, kIdescPvHalf, i > 0 || k != 0);
                 mma_ts_if(leader, d_o + 64, d_s + 8 * k, b1 + 128 * k, kIdescPvHalf, i > 0 || k != 0);
               }
             }
@@ -681,32 +689,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++items;
             }
             commit_if(leader, bar(sm->v_empty[o]));
-          } else if (i >= 0) {
-            wait(sm->v_full[o], (t / kDepth) & 1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(sm->v_empty[o]));
           }
-          // S = Q . K^T of the next, behind it (S lies where P did)
-          const uint32_t t1 = t + 1, o1 = t1 % kDepth;
-          if (i + 1 < mine) {
-            uint32_t b[kQk];
-#pragma unroll
-            for (int c = 0; c < kQk; ++c) b[c] = uniform(desc_lo(ring + (t1 * kPer + c) % kRing * kChunk, 16));
-            if (i < 0) wait(sm->q_full[x], items & 1);
-            wait(sm->k_full[o1], (t1 / kDepth) & 1);
+          // (the ring of 192-wide keys holds 1.6 tiles: the next keys may still be on their way)
+          if (kHasRope && i + 1 < n) wait(sm->k_full[o1], (t1 / kDepth) & 1);
+          if (qk) {
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < kQk; ++c)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) mma_ss_if(leader, d_s, a_q + c * (kChunk / 16) + 2 * k, b[c] + 2 * k, kIdesc128, (c | k) != 0);
+              for (int k = 0; k < 4; ++k) mma_ss_if(leader, d_s, a_q + c * (kChunk / 16) + 2 * k, b_k[c] + 2 * k, kIdesc128, (c | k) != 0);
             commit_if(leader, bar(sm->s_full[x]));
             if (i + 2 == mine) commit_if(leader, bar(sm->q_empty[x]));
             commit_if(leader, bar(sm->k_empty[o1]));
-          } else if (i + 1 < n) {
-            wait(sm->k_full[o1], (t1 / kDepth) & 1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(sm->k_empty[o1]));
           }
+          // tiles that only the other rows have
+          __syncwarp();
+          if (lane == 0 && i >= 0 && !pv) mbar_arrive(bar(sm->v_empty[o]));
+          if (lane == 0 && i + 1 < n && !qk) mbar_arrive(bar(sm->k_empty[o1]));
         }
         tile += n;
         done_item();
