@@ -79,7 +79,7 @@ bool make_rope_map(CUtensorMap* m, const void* base, int heads, int64_t tokens, 
 }
 
 template <bool kHasRope>
-int launch_prefill(const prefill::Maps& maps, const prefill::Params& p, int blocks, cudaStream_t stream) {
+int launch_prefill(const prefill::Maps& maps, const prefill::Params& p, int64_t blocks, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};  // per instantiation
   const int rc = allow_shared_memory(prefill::mla_prefill_kernel<kHasRope>, prefill::kSmemBytes, &done,
                                      "cudaFuncSetAttribute(prefill kernel)");
@@ -183,6 +183,7 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   p.causal = causal != 0;
   p.rope_per_head = rope_per_head;
   p.splits = splits;
+  p.parts = static_cast<uint32_t>(num_sm_parts < (1 << 16) ? num_sm_parts : (1 << 16));
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.out_token = out_token;
@@ -194,8 +195,8 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   p.v_token = v_token;
   p.v_head = v_head;
   p.err = err;
-  const int64_t per = 2 * tokens, items = (total_q + batch * (per - 1)) / per * h_k * splits;
-  const int blocks = static_cast<int>(items < num_sm_parts ? items : num_sm_parts);
+  // as many blocks as items at most, whatever the lengths (a block that runs takes on further items)
+  const int64_t per = 2 * tokens, blocks = (total_q + batch * (per - 1)) / per * h_k * splits;
   const int status = k_rope ? launch_prefill<true>(maps, p, blocks, stream) : launch_prefill<false>(maps, p, blocks, stream);
   if (status != MLA_OK || splits == 1) return status;
 

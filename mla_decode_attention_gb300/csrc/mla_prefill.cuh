@@ -77,6 +77,7 @@ struct Params {
   int causal;
   int rope_per_head;     // k_rope has a head dimension
   int splits;
+  uint32_t parts;        // SMs
   float scale_log2;      // softmax_scale * log2 e
   __nv_bfloat16* out;
   int64_t out_token, out_head;  // strides in elements
@@ -109,6 +110,8 @@ struct Item {
 };
 
 struct Shared {
+  alignas(16) uint4 answer;  // of a request to cancel a block
+  uint64_t answered;
   uint64_t k_full[kDepth], k_empty[kDepth], v_full[kDepth], v_empty[kDepth];  // of a key tile's chunks
   uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], sums_full[2], sums_free[2];
   uint64_t item_full[2], item_empty[2];
@@ -157,24 +160,33 @@ __device__ __forceinline__ bool edge_tile(const Item& it, int t, int causal) {
   return (t + 1) * kKeys > seen_by(it, 0, causal);
 }
 
+// Reports sequences that do not follow each other within the tensors' rows.
+__device__ __forceinline__ void check_ranges(const Params& p, int lane) {
+  bool bad = false;
+  for (int i = lane; i < p.batch; i += 32) {
+    const int q0 = p.cu_q[i], q1 = p.cu_q[i + 1], k0 = p.cu_k[i], k1 = p.cu_k[i + 1];
+    bad = bad || q0 < 0 || q1 < q0 || q1 > p.total_q || k0 < 0 || k1 < k0 || k1 > p.total_k;
+  }
+  if (bad && p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
+}
+
 // Finds item `index` of the call (lanes of one warp together; `base`, `before`: where
-// the last search ended, sequences and items before them; indexes grow).  Items of a
-// sequence lie head by head, a head's blocks of query rows from the last (the most keys)
-// to the first, a block's splits beside each other.
+// the last search ended, sequences and items before them).  A sequence's items lie by groups
+// of heads, as many as fill the device twice (their keys and values, some 40 MB whatever the
+// length, stay in L2 meanwhile); in a group blocks of query rows come from the last, which has the
+// most keys, to the first, the heads' beside each other, and a block's splits.
 __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, int& base, uint32_t& before, Item& out, int lane) {
   const int per = 2 * p.tokens;
+  if (index < before) {
+    base = 0;
+    before = 0;
+  }
   for (; base < p.batch; base += 32) {
     const int i = base + lane;
     int q0 = 0, q1 = 0;
-    bool bad = false;
-    if (i < p.batch) {
-      q0 = p.cu_q[i];
-      q1 = p.cu_q[i + 1];
-      bad = q0 < 0 || q1 < q0 || q1 > p.total_q;
-      if (bad) {  // rows that exist
-        q0 = min(max(q0, 0), p.total_q);
-        q1 = min(max(q1, q0), p.total_q);
-      }
+    if (i < p.batch) {  // (clamped to rows that exist)
+      q0 = min(max(p.cu_q[i], 0), p.total_q);
+      q1 = min(max(p.cu_q[i + 1], q0), p.total_q);
     }
     const uint32_t blocks = static_cast<uint32_t>(q1 - q0 + per - 1) / per;
     const uint32_t mine = blocks * (p.h_k * p.splits);
@@ -184,7 +196,6 @@ __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, int& 
       const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
-    if (bad && p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
     const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
     const uint32_t local = index - (before + upto - mine);  // within the lane's sequence, if below `mine`
     const uint32_t hit = __ballot_sync(0xffffffffu, local < mine);
@@ -194,15 +205,11 @@ __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, int& 
     }
     const int who = __ffs(hit) - 1;
     if (lane == who) {
-      const uint32_t per_head = blocks * p.splits;
-      const int head = local / per_head, rem = local % per_head;
-      const int block = blocks - 1 - rem / p.splits;
-      int k0 = p.cu_k[i], k1 = p.cu_k[i + 1];
-      if (k0 < 0 || k1 < k0 || k1 > p.total_k) {
-        if (p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
-        k0 = min(max(k0, 0), p.total_k);
-        k1 = min(max(k1, k0), p.total_k);
-      }
+      const uint32_t heads = min(max(2 * p.parts / blocks, 1u), static_cast<uint32_t>(p.h_k));
+      const uint32_t first_head = local / (heads * blocks * p.splits) * heads, rem = local - first_head * blocks * p.splits;
+      const uint32_t here = min(heads, p.h_k - first_head);  // (the last group may be smaller)
+      const int split = rem % p.splits, head = first_head + rem / p.splits % here, block = blocks - 1 - rem / p.splits / here;
+      const int k0 = min(max(p.cu_k[i], 0), p.total_k), k1 = min(max(p.cu_k[i + 1], k0), p.total_k);
       Item it;
       const int at = block * per, q_len = q1 - q0;
       it.q_row = q0 + at;
@@ -211,7 +218,7 @@ __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, int& 
       it.k_len = k1 - k0;
       it.seen0 = it.k_len - q_len + at + 1;
       it.head = head;
-      it.split = rem % p.splits;
+      it.split = split;
       int tiles[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -315,6 +322,23 @@ __device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar) {
       : "memory");
 }
 
+// Asks for a block of this grid that has not begun not to begin: 16 bytes of answer at
+// `answer`, completing on `bar`.
+__device__ __forceinline__ void cancel_a_block(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer), "r"(bar)
+               : "memory");
+}
+// Whether a block was cancelled, and its index.
+__device__ __forceinline__ bool cancelled_block(uint32_t answer, uint32_t* index) {
+  uint32_t got, x;
+  asm volatile(
+      "{ .reg .pred p; .reg .b128 r; ld.shared.b128 r, [%2]; clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;"
+      " selp.u32 %1, 1, 0, p; mov.u32 %0, 0; @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r; }"
+      : "=r"(x), "=r"(got) : "r"(answer) : "memory");
+  if (got) *index = x;
+  return got != 0u;
+}
+
 // 5-D tiled load of one box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w, int32_t v,
                                             uint32_t bar, uint64_t policy) {
@@ -361,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm->item_full[i]), 1);
       mbar_init(bar(sm->item_empty[i]), 15);  // all warps but the one that fills them
     }
+    mbar_init(bar(sm->answered), 1);
     sm->abort = 0u;
     fence_mbarrier_init();
     tma_prefetch_desc(&maps.q);
@@ -768,17 +793,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ------------------------------------------------------------- items
+      // The grid has a block for every item that the lengths allow.  A block that runs takes on,
+      // when it is through with its own item, one whose block has not begun: that block is
+      // cancelled and its index comes back.  So items go to whoever is free first, without a counter
+      // in memory that calls would share.
       int cursor = 0;
-      uint32_t before = 0, index = blockIdx.x;
-      for (uint32_t k = 0;; ++k, index += gridDim.x) {
+      uint32_t before = 0, index = blockIdx.x, asked = 0;
+      bool have = true, ok = true;
+      for (uint32_t k = 0;; ++k) {
         Item* slot = &sm->items[k & 1];
-        bool ok = wait_for(bar(sm->item_empty[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const bool more = find_item(p, index, cursor, before, *slot, lane);
-        if (!more && lane == 0) slot->n_tok = 0;
+        ok = __all_sync(0xffffffffu, wait_for(bar(sm->item_empty[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag));
+        bool found = false;
+        while (ok && !found) {
+          if (!have) {
+            if (lane == 0) {
+              fence_proxy_async_smem();  // the last answer has been read
+              mbar_arrive_expect_tx(bar(sm->answered), 16);
+              cancel_a_block(smem_u32(&sm->answer), bar(sm->answered));
+            }
+            ok = __all_sync(0xffffffffu, wait_for(bar(sm->answered), asked++ & 1, abort_flag));
+            if (!ok || !cancelled_block(smem_u32(&sm->answer), &index)) break;  // (after a no, no further question)
+          }
+          have = false;
+          found = find_item(p, index, cursor, before, *slot, lane);  // (the grid may have more blocks than items)
+        }
+        if (!ok) break;
+        if (!found && lane == 0) slot->n_tok = 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm->item_full[k & 1]));
-        if (!more) break;
+        if (index == 0) check_ranges(p, lane);  // (by whoever has the first item)
+        if (!found) break;
       }
     }
   }
