@@ -579,7 +579,7 @@ int mla_prefill_workspace_size(int64_t total_q, int64_t total_k, int batch, int 
  *  h_q / h_k    a whole number of 1 .. 128.  total_q, total_k: at most 2^27 rows.
  *  num_sm_parts from mla_num_sm_parts for up to 64 heads (any value >= 1 gives the same
  *               result up to rounding).
- *  workspace    workspace_bytes bytes, at least mla_prefill_workspace_size(), 16-byte
+ *  workspace    workspace_bytes bytes, at least mla_prefill_workspace_size(), 32-byte
  *               aligned; NULL when that is 0.
  *  A query that sees no key gets out = 0, lse = -inf.  What a query does not see leaves
  *  no trace in its outputs, NaN and infinities included.  One that sees a key with a

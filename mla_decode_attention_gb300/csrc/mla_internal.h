@@ -23,6 +23,7 @@ inline int head_blocks(int h) { return (h + kHeadsPerCta - 1) / kHeadsPerCta; }
 // Most rows of a packed tensor (all its sequences together).
 constexpr int64_t kMaxPackedRows = int64_t{1} << 27;
 
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Whether rows of `width` elements, `token` apart from token to token and `head` from

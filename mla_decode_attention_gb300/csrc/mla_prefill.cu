@@ -149,7 +149,7 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   const int64_t rope_token = st(k_rope_token_stride, total_k, kRope), rope_head = rope_per_head ? k_rope_head_stride : kRope;
   const int64_t out_token = st(out_token_stride, total_q, kValue), out_head = st(out_head_stride, h_q, kValue);
   const int64_t strides = q_token | q_head | k_token | k_head | v_token | v_head | out_token | out_head | (k_rope ? rope_token | rope_head : 0);
-  if (!aligned16(q) || !aligned16(k) || !aligned16(k_rope) || !aligned16(v) || !aligned16(out) || !aligned16(workspace) ||
+  if (!aligned16(q) || !aligned16(k) || !aligned16(k_rope) || !aligned16(v) || !aligned16(out) || !aligned32(workspace) ||
       strides % 8 != 0)
     return MLA_ERR_ALIGN;
   const int splits = splits_of(total_q, total_k, batch, h_q, h_k, num_sm_parts);
@@ -188,6 +188,7 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   p.out = static_cast<__nv_bfloat16*>(out);
   p.out_token = out_token;
   p.out_head = out_head;
+  p.out_wide = reinterpret_cast<uintptr_t>(out) % 32 == 0 && (out_token | out_head) % 16 == 0;
   p.lse = lse;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_lse = splits > 1 ? p.ws_o + ws_rows * kValue : nullptr;

@@ -81,6 +81,7 @@ struct Params {
   float scale_log2;      // softmax_scale * log2 e
   __nv_bfloat16* out;
   int64_t out_token, out_head;  // strides in elements
+  int out_wide;          // rows of out begin on 32 bytes
   float* lse;            // [h_q, total_q]
   float* ws_o;           // splits > 1: [splits, total_q, h_q, 128]
   float* ws_lse;         // [splits, h_q, total_q]
@@ -250,6 +251,13 @@ __device__ __forceinline__ bool take_out(uint32_t addr) {
   return any;
 }
 
+// 32 bytes, a whole sector, by one thread.
+__device__ __forceinline__ void st_global_v8(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // x * 0 + acc for two bf16: NaN from the first value that is not finite on.
 __device__ __forceinline__ uint32_t note_odd(uint32_t x, uint32_t acc) {
   uint32_t r;
@@ -257,33 +265,32 @@ __device__ __forceinline__ uint32_t note_odd(uint32_t x, uint32_t acc) {
   return r;
 }
 
-// The value tile at `lo`, `hi` (its two chunks) before products read it, by four warps:
-// rows from `valid` on become zeros; in rows `seen` .. valid - 1, which some query rows
-// see and others do not, values that are not finite do.  Returns whether the warp
-// found any.  A row's eight 16-byte units lie swizzled within its 128 bytes, so units
-// are taken as they come; each thread has eight of the tile's 2048.
-__device__ __forceinline__ bool fix_values(uint32_t lo, uint32_t hi, int seen, int valid, int thread) {
-  bool odd = false;
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    const uint32_t at = c == 0 ? lo : hi;
-    uint32_t acc = 0u;
-    uint4 v[8];
+// One chunk of a value tile before products read it, by four warps: rows from `valid` on
+// become zeros; in rows `seen` .. valid - 1, which some query rows see and others do not,
+// values that are not finite do.  Returns whether the warp found any.  A row's eight
+// 16-byte units lie swizzled within its 128 bytes, so units are taken as they come;
+// each thread has eight of the chunk's 1024.
+__device__ __forceinline__ bool fix_values(uint32_t at, int seen, int valid, int thread) {
+  uint32_t acc[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = ld_shared_v4(at + 16 * (thread + 128 * i));
+  for (int h = 0; h < 2; ++h) {
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = thread + 128 * i;
+    for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(at + 16 * (thread + 128 * (4 * h + i)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = thread + 128 * (4 * h + i);
       if (u >= valid * 8)
         st_shared_v4(at + 16 * u, 0u, 0u, 0u, 0u);
       else
-        acc = note_odd(v[i].w, note_odd(v[i].z, note_odd(v[i].y, note_odd(v[i].x, acc))));
+        acc[i] = note_odd(v[i].w, note_odd(v[i].z, note_odd(v[i].y, note_odd(v[i].x, acc[i]))));
     }
-    if (__any_sync(0xffffffffu, (acc & 0x7F807F80u) != 0u)) {  // (a sum of zeros otherwise)
+  }
+  bool odd = false;
+  if (__any_sync(0xffffffffu, ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7F807F80u) != 0u)) {  // (sums of zeros otherwise)
 #pragma unroll 1
-      for (int u = thread; u < valid * 8; u += 128)
-        if (u >= seen * 8) odd |= take_out(at + 16 * u);
-    }
+    for (int u = thread; u < valid * 8; u += 128)
+      if (u >= seen * 8) odd |= take_out(at + 16 * u);
   }
   return __any_sync(0xffffffffu, odd);
 }
@@ -339,13 +346,29 @@ __device__ __forceinline__ bool cancelled_block(uint32_t answer, uint32_t* index
   return got != 0u;
 }
 
-// 5-D tiled load of one box into shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w, int32_t v,
-                                            uint32_t bar, uint64_t policy) {
+// Loads of one box, and the arrival that expects their bytes, by the lane whose `leader` is set.
+__device__ __forceinline__ void expect_if(uint32_t leader, uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar), "l"(policy)
+      "{ .reg .pred q; .reg .b64 st; setp.ne.b32 q, %2, 0; @q mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void load_4d_if(uint32_t leader, uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w,
+                                           uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %8, 0;"
+      " @q cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7; }" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void load_5d_if(uint32_t leader, uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w,
+                                           int32_t v, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %9, 0;"
+      " @q cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8; }" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar), "l"(policy), "r"(leader)
       : "memory");
 }
 
@@ -367,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDepth; ++i) {
-      mbar_init(bar(sm->k_full[i]), kHasRope ? 2 : 1);
+      mbar_init(bar(sm->k_full[i]), 1);
       mbar_init(bar(sm->k_empty[i]), 2);
-      mbar_init(bar(sm->v_full[i]), 4);  // a load's arrival, three more; or four warps'
+      mbar_init(bar(sm->v_full[i]), 8);  // a load's arrival and seven more, or eight warps'
       mbar_init(bar(sm->v_empty[i]), 2);
       mbar_init(bar(sm->edge[i]), 1);
     }
@@ -429,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = t_lane + kColS + 128 * x, t_o = t_lane + kColO + 128 * x;
     const int my_tok = r / p.group, my_sub = r % p.group;
     const float sc = p.scale_log2;
-    uint32_t tiles = 0, items = 0;
+    uint32_t tile = 0, edges = 0, tiles = 0, items = 0;
     bool ok = true;
     while (ok && next_item()) {
       const int n = it->n[x];
@@ -437,13 +460,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = seen_by(*it, at, p.causal);
       const bool row = my_tok < p.tokens && at < it->n_tok;
       float m = 0.f, lsum = 0.f, bsum = 0.f;
-      for (int i = 0; i < n; ++i, ++tiles) {
+      const int both = max(it->n[0], it->n[1]), low = seen_by(*it, 0, p.causal);
+      for (int i = 0; i < both; ++i, ++tile) {
         const int t = it->first + i;
-        ok = wait_for(bar(sm->s_full[x]), tiles & 1, abort_flag);
+        // (each four warps take a chunk, while the scores are on their way)
+        const bool edge = edge_tile(*it, t, p.causal);
+        if (edge) {
+          ok = __all_sync(0xffffffffu, wait_for(bar(sm->edge[edges % kDepth]), (edges / kDepth) & 1, abort_flag));
+          if (!ok) break;
+          ++edges;
+          if (fix_values(ring + (tile * kPer + kQk + x) % kRing * kChunk, max(0, low - t * kKeys), min(kKeys, it->k_len - t * kKeys), r))
+            *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n & 1].odd) = 1u;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sm->v_full[tile % kDepth]));
+        }
+        if (i >= n) continue;
+        ok = wait_for(bar(sm->s_full[x]), tiles++ & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const bool edge = edge_tile(*it, t, p.causal);
         const int lim = seen - t * kKeys;
         float l[4][2];  // (one chain of additions would take as long as the exponentials)
         uint32_t pk[4][16];
@@ -456,17 +492,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (look) {
             float top = -INFINITY;
 #pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-              float v[16];
-              tmem_ld16(t_s + 16 * j, v);
+            for (int j = 0; j < 4; ++j) {
+              float v[32];
+              tmem_ld32(t_s + 32 * j, v);
               tmem_wait_ld();
               if (edge) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = 16 * j + k < lim ? v[k] : -INFINITY;
-                tmem_st16(t_s + 16 * j, v);
+                for (int k = 0; k < 32; ++k) v[k] = k < lim - 32 * j ? v[k] : -INFINITY;
+                tmem_st32(t_s + 32 * j, v);
               }
+              float u[4];
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) top = fmax3(top, v[k], v[k + 1]);
+              for (int k = 0; k < 4; ++k) {
+                u[k] = fmax3(v[8 * k], v[8 * k + 1], v[8 * k + 2]);
+                u[k] = fmax3(u[k], v[8 * k + 3], v[8 * k + 4]);
+                u[k] = fmax3(u[k], v[8 * k + 5], v[8 * k + 6]);
+                u[k] = fmaxf(u[k], v[8 * k + 7]);
+              }
+              top = fmax3(top, fmax3(u[0], u[1], u[2]), u[3]);
             }
             tmem_wait_st();
             top *= sc;
@@ -562,28 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x & 127;
     const int my_tok = r / p.group, my_sub = r % p.group;
     uint32_t items[2] = {0u, 0u};
-    uint32_t tile = 0, edges = 0;
     bool ok = true;
     while (ok && next_item()) {
-      // values that must not be multiplied: the item's last tiles, before its outputs
-      const int n = max(it->n[0], it->n[1]);
-      const int low = seen_by(*it, 0, p.causal);
-#pragma unroll 1
-      for (int i = max(0, low / kKeys - it->first); i < n; ++i) {
-        const int t = it->first + i;
-        ok = __all_sync(0xffffffffu, wait_for(bar(sm->edge[edges % kDepth]), (edges / kDepth) & 1, abort_flag));
-        if (!ok) break;
-        ++edges;
-        const uint32_t c = (tile + i) * kPer + kQk;
-        const bool odd = fix_values(ring + c % kRing * kChunk, ring + (c + 1) % kRing * kChunk, max(0, low - t * kKeys),
-                                    min(kKeys, it->k_len - t * kKeys), r);
-        if (odd) *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n & 1].odd) = 1u;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sm->v_full[(tile + i) % kDepth]));
-      }
-      if (!ok) break;
-      tile += n;
 #pragma unroll 1
       for (int x = 0; x < 2 && ok; ++x) {
         const int at = x * p.tokens + my_tok;
@@ -623,14 +646,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
           if (!row) continue;
-          if (p.splits == 1) {
+          if (p.splits == 1 && p.out_wide) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[2 * k], o[2 * k + 1]);
+            st_global_v8(dst + 2 * j, w);
+          } else if (p.splits == 1) {
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               dst[2 * j + k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
                                           pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
           } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ws[4 * j + k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 2; ++k) st_global_v8(ws + 4 * j + 2 * k, reinterpret_cast<const uint32_t(&)[8]>(o[8 * k]));
           }
         }
         if (it->n[x] > 0) {
@@ -737,57 +765,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 14) {
       // ------------------------------------------------------------- loads
-      // (a box costs its SM a fixed time besides its bytes: both chunks of keys, and of values, come in one)
-      uint32_t tile = 0, edges = 0, items = 0;  // items: a count of each tile of rows in 16 bits
-      uint32_t parts = 0, freed = kRing;         // parts of tiles given back, chunks of the ring that may be written
+      // A box costs its SM a fixed time besides its bytes: both chunks of keys, and of values,
+      // come in one.  Like the products, in code that all lanes run.  A tile's keys take
+      // the place of values kV tiles back (and of what lies before), its values that of keys kK tiles back.
+      constexpr uint32_t kV = kHasRope ? 2 : 3, kK = kHasRope ? 1 : 2;
+      uint32_t tile = 0, edges = 0, items[2] = {0u, 0u};
       const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_first();
+      const uint32_t leader = elect_one();
       bool ok = true;
-      while (next_item()) {
-        if (lane == 0) {
-          const int n = max(it->n[0], it->n[1]);
-          for (int i = 0; i < n && ok; ++i, ++tile) {
-            const int t = it->first + i;
-            // queries 0, keys, queries 1, position columns, values
+      auto wait = [&](uint64_t& b, uint32_t parity) { return ok = __all_sync(0xffffffffu, wait_for(bar(b), parity, abort_flag)); };
+      while (ok && next_item()) {
+        const int n = __reduce_max_sync(0xffffffffu, max(it->n[0], it->n[1])), head = uniform(it->head);
+        const int rope_head = p.rope_per_head ? head : 0;
+        int row = uniform(it->k_row + it->first * kKeys);
+        auto queries = [&](int x) {
+          if (it->n[x] == 0) return;
+          if (!wait(sm->q_empty[x], (items[x]++ & 1) ^ 1)) return;
+          expect_if(leader, bar(sm->q_full[x]), kQk * 128u * p.group * p.tokens);
+          const int q_row = uniform(it->q_row + x * p.tokens);
+#pragma unroll
+          for (int c = 0; c < kQk; ++c)
+            load_5d_if(leader, q_base + (x * kQk + c) * kChunk, &maps.q, 0, 0, q_row, c, head, bar(sm->q_full[x]), once);
+        };
+        if (n > 0) queries(0);
 #pragma unroll 1
-            for (int step = i == 0 ? 0 : 1; step < 5 && ok; ++step) {
-              if (step == 0 || step == 2) {
-                const int x = step >> 1;
-                if (i > 0 || it->n[x] == 0) continue;
-                ok = wait_for(bar(sm->q_empty[x]), ((items >> (16 * x)) & 1) ^ 1, abort_flag);
-                if (!ok) break;
-                items += 1u << (16 * x);
-                mbar_arrive_expect_tx(bar(sm->q_full[x]), kQk * 128u * p.group * p.tokens);
-#pragma unroll 1
-                for (int c = 0; c < kQk; ++c)
-                  tma_load_5d(q_base + (x * kQk + c) * kChunk, &maps.q, 0, 0, it->q_row + x * p.tokens, c, it->head, bar(sm->q_full[x]), once);
-                continue;
-              }
-              if (!kHasRope && step == 3) continue;
-              const uint32_t c = tile * kPer + (step == 1 ? 0 : (step == 3 ? 2 : kQk)), chunks = step == 3 ? 1 : 2;
-              // the ring's chunks are given back in turn, a tile's keys, then its values
-              while (ok && static_cast<int32_t>(c + chunks - freed) > 0) {
-                const uint32_t o = (parts >> 1) % kDepth;
-                ok = wait_for(bar(parts & 1 ? sm->v_empty[o] : sm->k_empty[o]), (parts / (2 * kDepth)) & 1, abort_flag);
-                freed += parts & 1 ? 2 : kQk;
-                ++parts;
-              }
-              if (!ok) break;
-              // an edge tile's values complete on a barrier of the output warps', which then complete the products'
-              const bool edge = step == 4 && edge_tile(*it, t, p.causal);
-              const uint32_t b = bar(edge ? sm->edge[edges % kDepth] : (step == 4 ? sm->v_full[tile % kDepth] : sm->k_full[tile % kDepth]));
-              edges += edge;
-              mbar_arrive_expect_tx(b, chunks * kChunk);
-              if (step == 4 && !edge) mbar_arrive_many(b, 3);
-              const uint32_t slot = c % kRing;
-              const bool wraps = kHasRope && chunks == 2 && slot + 1 == kRing;
-              const CUtensorMap* m = step == 3 ? &maps.rope : (step == 1 ? (wraps ? &maps.k1 : &maps.k) : (wraps ? &maps.v1 : &maps.v));
-              const int row = it->k_row + t * kKeys, head = step == 3 && !p.rope_per_head ? 0 : it->head;
-              tma_load_4d(ring + slot * kChunk, m, 0, row, 0, head, b, keep);
-              if (wraps) tma_load_4d(ring, m, 0, row, 1, head, b, keep);
-            }
+        for (int i = 0; i < n && ok; ++i, ++tile, row += kKeys) {
+          const uint32_t c0 = uniform(tile * kPer % kRing), cv = (c0 + kQk) % kRing, o = tile % kDepth;
+          if (tile >= kV && !wait(sm->v_empty[(tile - kV) % kDepth], ((tile - kV) / kDepth) & 1)) break;
+          const uint32_t kb = uniform(bar(sm->k_full[o]));
+          expect_if(leader, kb, kQk * kChunk);
+          if (!kHasRope || c0 + 1 < kRing) {
+            load_4d_if(leader, ring + c0 * kChunk, &maps.k, 0, row, 0, head, kb, keep);
+          } else {  // (a pair that would run past the ring's end, by its chunks)
+            load_4d_if(leader, ring + c0 * kChunk, &maps.k1, 0, row, 0, head, kb, keep);
+            load_4d_if(leader, ring, &maps.k1, 0, row, 1, head, kb, keep);
+          }
+          if (kHasRope) load_4d_if(leader, ring + (c0 + 2) % kRing * kChunk, &maps.rope, 0, row, 0, rope_head, kb, keep);
+          if (i == 0) queries(1);
+          if (!ok || (tile >= kK && !wait(sm->k_empty[(tile - kK) % kDepth], ((tile - kK) / kDepth) & 1))) break;
+          // values of a tile with unseen keys complete on a barrier of the softmax warps', which then complete the products'
+          const bool edge = edge_tile(*it, it->first + i, p.causal);
+          const uint32_t vb = uniform(bar(edge ? sm->edge[edges++ % kDepth] : sm->v_full[o]));
+          expect_if(leader, vb, 2 * kChunk);
+          if (leader && !edge) mbar_arrive_many(vb, 7);
+          if (!kHasRope || cv + 1 < kRing) {
+            load_4d_if(leader, ring + cv * kChunk, &maps.v, 0, row, 0, head, vb, keep);
+          } else {
+            load_4d_if(leader, ring + cv * kChunk, &maps.v1, 0, row, 0, head, vb, keep);
+            load_4d_if(leader, ring, &maps.v1, 0, row, 1, head, vb, keep);
           }
         }
-        ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0) != 0;
         if (!ok) break;
         done_item();
       }
