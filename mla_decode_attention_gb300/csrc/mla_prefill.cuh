@@ -171,75 +171,101 @@ __device__ __forceinline__ void check_ranges(const Params& p, int lane) {
   if (bad && p.err) atomicOr(p.err, MLA_DEVERR_BAD_RANGE);
 }
 
-// Finds item `index` of the call (lanes of one warp together; `base`, `before`: where
-// the last search ended, sequences and items before them).  A sequence's items lie by groups
-// of heads, as many as fill the device twice (their keys and values, some 40 MB whatever the
-// length, stay in L2 meanwhile); in a group blocks of query rows come from the last, which has the
-// most keys, to the first, the heads' beside each other, and a block's splits.
-__device__ __forceinline__ bool find_item(const Params& p, uint32_t index, int& base, uint32_t& before, Item& out, int lane) {
-  const int per = 2 * p.tokens;
-  if (index < before) {
-    base = 0;
-    before = 0;
+// Where a search for items stands: 32 sequences, a lane each, the one with the most keys
+// first, and the items before them.
+struct Window {
+  int base;                 // the first of the sequences; -1: none looked at
+  uint32_t before, all;     // items of sequences before these, of these
+  int q0, q_len, k0, k_len; // of the lane's sequence
+  uint32_t blocks, mine, upto;  // its blocks of query rows, its items, those up to its last
+};
+
+__device__ __forceinline__ void look_at(const Params& p, Window& w, int base, uint32_t before, int lane) {
+  w.base = base;
+  w.before = before;
+  const int i = base + lane;
+  int q0 = 0, q_len = 0, k0 = 0, k_len = 0;
+  if (i < p.batch) {  // (clamped to rows that exist)
+    q0 = min(max(p.cu_q[i], 0), p.total_q);
+    q_len = min(max(p.cu_q[i + 1], q0), p.total_q) - q0;
+    k0 = min(max(p.cu_k[i], 0), p.total_k);
+    k_len = min(max(p.cu_k[i + 1], k0), p.total_k) - k0;
   }
-  for (; base < p.batch; base += 32) {
-    const int i = base + lane;
-    int q0 = 0, q1 = 0;
-    if (i < p.batch) {  // (clamped to rows that exist)
-      q0 = min(max(p.cu_q[i], 0), p.total_q);
-      q1 = min(max(p.cu_q[i + 1], q0), p.total_q);
-    }
-    const uint32_t blocks = static_cast<uint32_t>(q1 - q0 + per - 1) / per;
-    const uint32_t mine = blocks * (p.h_k * p.splits);
-    uint32_t upto = mine;
+  int rank = 0;
 #pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
-    const uint32_t local = index - (before + upto - mine);  // within the lane's sequence, if below `mine`
-    const uint32_t hit = __ballot_sync(0xffffffffu, local < mine);
-    if (hit == 0u) {
-      before += all;
-      continue;
-    }
-    const int who = __ffs(hit) - 1;
-    if (lane == who) {
-      const uint32_t heads = min(max(2 * p.parts / blocks, 1u), static_cast<uint32_t>(p.h_k));
-      const uint32_t first_head = local / (heads * blocks * p.splits) * heads, rem = local - first_head * blocks * p.splits;
-      const uint32_t here = min(heads, p.h_k - first_head);  // (the last group may be smaller)
-      const int split = rem % p.splits, head = first_head + rem / p.splits % here, block = blocks - 1 - rem / p.splits / here;
-      const int k0 = min(max(p.cu_k[i], 0), p.total_k), k1 = min(max(p.cu_k[i + 1], k0), p.total_k);
-      Item it;
-      const int at = block * per, q_len = q1 - q0;
-      it.q_row = q0 + at;
-      it.n_tok = q_len - at < per ? q_len - at : per;
-      it.k_row = k0;
-      it.k_len = k1 - k0;
-      it.seen0 = it.k_len - q_len + at + 1;
-      it.head = head;
-      it.split = split;
-      int tiles[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int last = (it.n_tok < (x + 1) * p.tokens ? it.n_tok : (x + 1) * p.tokens) - 1;  // the tile's last token
-        tiles[x] = last >= x * p.tokens ? (seen_by(it, last, p.causal) + kKeys - 1) / kKeys : 0;
-      }
-      const int most = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
-      it.first = most * it.split / p.splits;  // (2^20 tiles, 2^5 splits at most)
-      const int end = most * (it.split + 1) / p.splits;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int e = tiles[x] < end ? tiles[x] : end;
-        it.n[x] = e > it.first ? e - it.first : 0;
-      }
-      it.odd = 0u;
-      out = it;
-    }
-    return true;
+  for (int o = 0; o < 32; ++o) {
+    const int other = __shfl_sync(0xffffffffu, k_len, o);
+    rank += other > k_len || (other == k_len && o < lane);
   }
-  return false;
+  int from = 0;
+#pragma unroll 1
+  for (int o = 0; o < 32; ++o)
+    if (__shfl_sync(0xffffffffu, rank, o) == lane) from = o;
+  w.q0 = __shfl_sync(0xffffffffu, q0, from);
+  w.q_len = __shfl_sync(0xffffffffu, q_len, from);
+  w.k0 = __shfl_sync(0xffffffffu, k0, from);
+  w.k_len = __shfl_sync(0xffffffffu, k_len, from);
+  const int per = 2 * p.tokens;
+  w.blocks = static_cast<uint32_t>(w.q_len + per - 1) / per;
+  w.mine = w.upto = w.blocks * (p.h_k * p.splits);
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, w.upto, o);
+    if (lane >= o) w.upto += v;
+  }
+  w.all = __shfl_sync(0xffffffffu, w.upto, 31);
+}
+
+// Finds item `index` of the call (lanes of one warp together).  A sequence's items lie by
+// groups of heads, as many as fill the device twice (their keys and values, some 40 MB whatever
+// the length, stay in L2 meanwhile); in a group blocks of query rows come from the last, which
+// has the most keys, to the first, the heads' beside each other, and a block's splits.
+__device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Window& w, Item& out, int lane) {
+  if (w.base < 0 || index < w.before) look_at(p, w, 0, 0u, lane);
+  while (index - w.before >= w.all) {
+    if (w.base + 32 >= p.batch) return false;
+    look_at(p, w, w.base + 32, w.before + w.all, lane);
+  }
+  const uint32_t local = index - (w.before + w.upto - w.mine);  // within the lane's sequence, if below its items
+  const uint32_t hit = __ballot_sync(0xffffffffu, local < w.mine);
+  if (hit == 0u) return false;  // (sequences that overlap beyond 32 bits of items)
+  if (lane == __ffs(hit) - 1) {
+    const uint32_t blocks = w.blocks;
+    const uint32_t heads = min(max(2 * p.parts / blocks, 1u), static_cast<uint32_t>(p.h_k));
+    const uint32_t first_head = local / (heads * blocks * p.splits) * heads, rem = local - first_head * blocks * p.splits;
+    const uint32_t here = min(heads, p.h_k - first_head);  // (the last group may be smaller)
+    const int split = rem % p.splits, head = first_head + rem / p.splits % here, block = blocks - 1 - rem / p.splits / here;
+    const int per = 2 * p.tokens, at = block * per;
+    Item it;
+    it.q_row = w.q0 + at;
+    it.n_tok = min(w.q_len - at, per);
+    it.k_row = w.k0;
+    it.k_len = w.k_len;
+    it.seen0 = w.k_len - w.q_len + at + 1;
+    it.head = head;
+    it.split = split;
+    int tiles[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int last = min(it.n_tok, (x + 1) * p.tokens) - 1;  // the tile's last token
+      tiles[x] = last >= x * p.tokens ? (seen_by(it, last, p.causal) + kKeys - 1) / kKeys : 0;
+    }
+    const int most = max(tiles[0], tiles[1]);
+    it.first = most * split / p.splits;  // (2^20 tiles, 2^5 splits at most)
+    const int end = most * (split + 1) / p.splits;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) it.n[x] = max(min(tiles[x], end) - it.first, 0);
+    it.odd = 0u;
+    out = it;
+  }
+  return true;
+}
+
+// 32 bytes, a whole sector, by one thread.
+__device__ __forceinline__ void st_global_v8(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // Zeros what is not finite in a unit of eight values in shared memory; whether there was any.
@@ -249,13 +275,6 @@ __device__ __forceinline__ bool take_out(uint32_t addr) {
   const bool any = ((v.x ^ w.x) | (v.y ^ w.y) | (v.z ^ w.z) | (v.w ^ w.w)) != 0u;
   if (any) st_shared_v4(addr, w.x, w.y, w.z, w.w);
   return any;
-}
-
-// 32 bytes, a whole sector, by one thread.
-__device__ __forceinline__ void st_global_v8(void* to, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-               "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
 }
 
 // x * 0 + acc for two bf16: NaN from the first value that is not finite on.
@@ -824,8 +843,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // when it is through with its own item, one whose block has not begun: that block is
       // cancelled and its index comes back.  So items go to whoever is free first, without a counter
       // in memory that calls would share.
-      int cursor = 0;
-      uint32_t before = 0, index = blockIdx.x, asked = 0;
+      Window window;
+      window.base = -1;
+      uint32_t index = blockIdx.x, asked = 0;
       bool have = true, ok = true;
       for (uint32_t k = 0;; ++k) {
         Item* slot = &sm->items[k & 1];
@@ -842,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok || !cancelled_block(smem_u32(&sm->answer), &index)) break;  // (after a no, no further question)
           }
           have = false;
-          found = find_item(p, index, cursor, before, *slot, lane);  // (the grid may have more blocks than items)
+          found = find_item(p, index, window, *slot, lane);  // (the grid may have more blocks than items)
         }
         if (!ok) break;
         if (!found && lane == 0) slot->n_tok = 0;
