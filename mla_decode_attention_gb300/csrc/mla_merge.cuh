@@ -27,7 +27,7 @@ struct Params {
   const float* lses;
   int64_t lse_part, lse_head, lse_token;
   int n, heads, d;
-  int64_t tokens;
+  uint32_t tokens, run;  // run: set by the launch
   const int32_t* rows_from;  // optional: only tokens [*rows_from, *rows_to) are written
   const int32_t* rows_to;
   __nv_bfloat16* out;
@@ -74,56 +74,61 @@ struct Unit {
   }
 };
 
-// kLanes lanes a row, kUnits units of eight columns a lane.
-template <bool kF32, int kLanes, int kUnits>
+// kLanes lanes a row, kUnits units of eight columns a lane, kAhead parts' units in flight: the
+// first are requested before the weights are known.  (A row read for nothing, because its
+// weight turns out 0, leaves no trace.)
+template <bool kF32, int kLanes, int kUnits, int kAhead>
 __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__ Params p) {
+  static_assert(kLanes % kAhead == 0, "parts of a step have their weights in one register each");
   pdl_launch_dependents();
   pdl_wait_primary();
   const int l = threadIdx.x % kLanes;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
-  int64_t tok = row / p.heads;
-  const int head = static_cast<int>(row - tok * p.heads);
-  bool in = tok < p.tokens;
-  if (p.rows_from) in = in && tok >= *p.rows_from && tok < *p.rows_to;
-  if (!in) tok = 0;
+  const uint32_t row = (blockIdx.x * static_cast<uint32_t>(kThreads) + threadIdx.x) / kLanes;
+  // Rows of `run` neighbouring tokens of a head, then of the next head: where log-sum-exps lie token by
+  // token, a sector of them is then used by one block.
+  const uint32_t rest = row / p.run, head = rest % p.heads;
+  const uint32_t t = rest / p.heads * p.run + row % p.run;
+  bool in = t < p.tokens;
+  if (p.rows_from) in = in && static_cast<int32_t>(t) >= *p.rows_from && static_cast<int32_t>(t) < *p.rows_to;
+  const int64_t tok = in ? t : 0;
+  const int64_t at = tok * p.token_stride + head * p.head_stride + 8 * l;
+  Unit<kF32> u[kAhead][kUnits];
+  auto request = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k)
+        if (in && i0 + j < p.n && 8 * (l + kLanes * k) < p.d) u[j][k].load(p.parts, (i0 + j) * p.part_stride + at + 8 * kLanes * k);
+  };
+  request(0);
   const float* lses = p.lses + head * p.lse_head + tok * p.lse_token;
-  // the weights of up to kLanes parts at a time; first their maximum and sum
-  float top = -INFINITY;
+  // the maximum and the sum of all, a lane for each kLanes-th
+  float top = -INFINITY, first = -INFINITY;
   for (int i = l; i < p.n; i += kLanes) {
     const float v = in ? lses[i * p.lse_part] : -INFINITY;
+    if (i == l) first = v;
     top = fmaxf(top, v);
   }
   top = group_max<kLanes>(top);
   const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  for (int i = l; i < p.n; i += kLanes) sum += in ? expf(lses[i * p.lse_part] - ref) : 0.f;
+  float sum = expf(first - ref);
+  for (int i = l + kLanes; i < p.n; i += kLanes) sum += in ? expf(lses[i * p.lse_part] - ref) : 0.f;
   sum = group_sum<kLanes>(sum);
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // (NaN stays)
   float acc[kUnits][8] = {};
-  const int64_t at = tok * p.token_stride + head * p.head_stride;
-  for (int i0 = 0; i0 < p.n; i0 += kLanes) {
-    const int mine = i0 + l;
-    const float lse_i = in && mine < p.n ? lses[mine * p.lse_part] : -INFINITY;
-    const float w_mine = lse_i == -INFINITY ? 0.f : expf(lse_i - ref) * inv;
-    const int here = p.n - i0 < kLanes ? p.n - i0 : kLanes;
-    constexpr int kAhead = 4;
-    for (int j0 = 0; j0 < here; j0 += kAhead) {
-      Unit<kF32> u[kAhead][kUnits];
-      float w[kAhead];
+  float w_mine = 0.f;
+  for (int i0 = 0; i0 < p.n; i0 += kAhead) {
+    if (i0 > 0) request(i0);
+    if (i0 % kLanes == 0) {  // the next kLanes parts' weights, a lane each
+      const float v = i0 == 0 ? first : (in && i0 + l < p.n ? lses[(i0 + l) * p.lse_part] : -INFINITY);
+      w_mine = v == -INFINITY ? 0.f : expf(v - ref) * inv;
+    }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        w[j] = __shfl_sync(0xffffffffu, j0 + j < here ? w_mine : 0.f, (j0 + j) % kLanes, kLanes);
-        if (j0 + j >= here) w[j] = 0.f;
+    for (int j = 0; j < kAhead; ++j) {
+      const float w = __shfl_sync(0xffffffffu, w_mine, i0 % kLanes + j, kLanes);
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-          if (w[j] != 0.f && 8 * (l + kLanes * k) < p.d)
-            u[j][k].load(p.parts, (i0 + j0 + j) * p.part_stride + at + 8 * (l + kLanes * k));
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-          if (w[j] != 0.f && 8 * (l + kLanes * k) < p.d) u[j][k].add(w[j], acc[k]);
+      for (int k = 0; k < kUnits; ++k)
+        if (w != 0.f && 8 * (l + kLanes * k) < p.d) u[j][k].add(w, acc[k]);
     }
   }
   __syncwarp();  // every lane has read the log-sum-exps that lane 0 may write over
@@ -136,15 +141,17 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
 }
 
 template <bool kF32>
-int launch_type(const Params& p, cudaStream_t stream) {
+int launch_type(Params p, cudaStream_t stream) {
+  p.run = p.heads > 1 && p.lse_head != 1 ? 8 : 1;
   const auto go = [&](auto kernel, int lanes) {
-    const int64_t rows = p.tokens * p.heads, per = kThreads / lanes;
+    const int64_t rows = (p.tokens + p.run - 1) / p.run * p.run * p.heads, per = kThreads / lanes;
     return launch_step(kernel, p, (rows + per - 1) / per, 1, kThreads, stream, "merge kernel launch");
   };
-  if (p.d <= 64) return go(merge_kernel<kF32, 8, 1>, 8);
-  if (p.d <= 128) return go(merge_kernel<kF32, 16, 1>, 16);
-  if (p.d <= 256) return go(merge_kernel<kF32, 32, 1>, 32);
-  return go(merge_kernel<kF32, 32, 2>, 32);
+  constexpr int kMore = kF32 ? 4 : 8;
+  if (p.d <= 64) return p.n <= 2 ? go(merge_kernel<kF32, 8, 1, 2>, 8) : go(merge_kernel<kF32, 8, 1, kMore>, 8);
+  if (p.d <= 128) return p.n <= 2 ? go(merge_kernel<kF32, 16, 1, 2>, 16) : go(merge_kernel<kF32, 16, 1, kMore>, 16);
+  if (p.d <= 256) return p.n <= 2 ? go(merge_kernel<kF32, 32, 1, 2>, 32) : go(merge_kernel<kF32, 32, 1, kMore>, 32);
+  return p.n <= 2 ? go(merge_kernel<kF32, 32, 2, 2>, 32) : go(merge_kernel<kF32, 32, 2, kMore / 2>, 32);
 }
 
 }  // namespace merge

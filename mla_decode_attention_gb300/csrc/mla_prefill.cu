@@ -213,7 +213,7 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   g.n = splits;
   g.heads = h_q;
   g.d = kValue;
-  g.tokens = total_q;
+  g.tokens = static_cast<uint32_t>(total_q);
   g.rows_from = cu_seqlens_q;           // rows of no sequence stay as they were
   g.rows_to = cu_seqlens_q + batch;
   g.out = p.out;

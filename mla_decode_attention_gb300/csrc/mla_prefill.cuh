@@ -58,10 +58,11 @@ constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
 constexpr int kSmemData = 14 * kChunk;
 constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring holds parts of
-// Probabilities are taken against a reference that follows the row's maximum only
-// when that has grown by 2^8: sums and outputs stay far from fp32's limits, and O is
-// rescaled in the first few tiles alone.
-constexpr float kRescaleLog2 = 8.f, kMoveSum = 256.f;
+// Probabilities are taken against a reference: the score of the first key, and the row's
+// maximum from where a tile's probabilities sum past 2^40 on.  Sums, outputs and
+// the bf16 probabilities (8 bits of exponent) stay in range either way, and O is
+// hardly ever rescaled.
+constexpr float kRescaleLog2 = 30.f, kMoveSum = 1099511627776.f;
 constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescPv = idesc_bf16(128, 128, false, true);
 constexpr uint32_t kIdescPvHalf = idesc_bf16(128, 64, false, true);
@@ -191,15 +192,17 @@ __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, ui
     k0 = min(max(p.cu_k[i], 0), p.total_k);
     k_len = min(max(p.cu_k[i + 1], k0), p.total_k) - k0;
   }
+  const int some = min(p.batch - base, 32);
   int rank = 0;
 #pragma unroll 1
-  for (int o = 0; o < 32; ++o) {
+  for (int o = 0; o < some; ++o) {
     const int other = __shfl_sync(0xffffffffu, k_len, o);
     rank += other > k_len || (other == k_len && o < lane);
   }
-  int from = 0;
+  if (lane >= some) rank = lane;
+  int from = lane;
 #pragma unroll 1
-  for (int o = 0; o < 32; ++o)
+  for (int o = 0; o < some; ++o)
     if (__shfl_sync(0xffffffffu, rank, o) == lane) from = o;
   w.q0 = __shfl_sync(0xffffffffu, q0, from);
   w.q_len = __shfl_sync(0xffffffffu, q_len, from);
@@ -266,6 +269,13 @@ __device__ __forceinline__ void st_global_v8(void* to, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
                "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// One 32-bit column: thread i gets lane (base + i).
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr));
+  return __uint_as_float(r);
 }
 
 // Zeros what is not finite in a unit of eight values in shared memory; whether there was any.
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && next_item()) {
       const int n = it->n[x];
       const int at = x * p.tokens + my_tok;
-      const int seen = seen_by(*it, at, p.causal);
+      const int seen = seen_by(*it, min(at, it->n_tok - 1), p.causal);
       const bool row = my_tok < p.tokens && at < it->n_tok;
       float m = 0.f, lsum = 0.f, bsum = 0.f;
       const int both = max(it->n[0], it->n[1]), low = seen_by(*it, 0, p.causal);
@@ -502,63 +512,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim = seen - t * kKeys;
         float l[4][2];  // (one chain of additions would take as long as the exponentials)
         uint32_t pk[4][16];
-        // Scores of keys not seen become -inf in TMEM before the pass reads them, and the
-        // row maximum is taken on the way: on the tiles that have such keys, on an item's
-        // first, and on a later one only where its probabilities sum past the bound, which one of
-        // them above it needs.  Where a reference moves the warp then takes the pass again.
-        bool look = edge || i == 0, again = false;
-        while (true) {
-          if (look) {
+        // A tile with unseen keys: their scores become -inf in TMEM before the pass reads them,
+        // by blocks of 32 keys from the first that not all of the warp's rows see.
+        if (edge) {
+#pragma unroll 1
+          for (int j = max(__reduce_min_sync(0xffffffffu, lim), 0) / 32; j < 4; ++j) {
+            float v[32];
+            tmem_ld32(t_s + 32 * j, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = k < lim - 32 * j ? v[k] : -INFINITY;
+            tmem_st32(t_s + 32 * j, v);
+          }
+          tmem_wait_st();
+        }
+        // A piece's first key gives the reference: it need not be near the row's maximum, only so near
+        // that nothing leaves fp32's and bf16's range (their exponents are alike).
+        if (i == 0) {
+          const float u = tmem_ld1(t_s);
+          m = u == -INFINITY ? 0.f : u * sc;
+        }
+        // The row maximum is looked for only where the probabilities sum past the bound, which one of
+        // them far above the reference needs; the warp then takes the pass again.
+        bool again = false;
+#pragma unroll 1
+        do {
+          if (again) {
             float top = -INFINITY;
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-              float v[32];
-              tmem_ld32(t_s + 32 * j, v);
+            for (int j = 0; j < 8; ++j) {
+              float v[16];
+              tmem_ld16(t_s + 16 * j, v);
               tmem_wait_ld();
-              if (edge) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = k < lim - 32 * j ? v[k] : -INFINITY;
-                tmem_st32(t_s + 32 * j, v);
-              }
-              float u[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                u[k] = fmax3(v[8 * k], v[8 * k + 1], v[8 * k + 2]);
-                u[k] = fmax3(u[k], v[8 * k + 3], v[8 * k + 4]);
-                u[k] = fmax3(u[k], v[8 * k + 5], v[8 * k + 6]);
-                u[k] = fmaxf(u[k], v[8 * k + 7]);
-              }
-              top = fmax3(top, fmax3(u[0], u[1], u[2]), u[3]);
+              for (int k = 0; k < 16; k += 2) top = fmax3(top, v[k], v[k + 1]);
             }
-            tmem_wait_st();
             top *= sc;
-            if (i == 0) {
-              m = top == -INFINITY ? 0.f : top;
-            } else if (again) {
-              const bool move = top > m + kRescaleLog2;
-              if (!__any_sync(0xffffffffu, move)) break;
-              // (this tile's scores were issued after the last tile's p.v and have completed: O holds every tile before)
-              const float alpha = move ? fast_exp2(m - top) : 1.f;
-              m = move ? top : m;
-              lsum *= alpha;
-              bsum *= alpha;
+            // (this tile's scores were issued after the last tile's p.v and have completed: O holds every tile before)
+            const bool move = top > m + kRescaleLog2;
+            const float alpha = move ? fast_exp2(m - top) : 1.f;
+            m = move ? top : m;
+            lsum *= alpha;
+            bsum *= alpha;
 #pragma unroll 1
-              for (int j = 0; j < 8; ++j) {
-                float o[16];
-                tmem_ld16(t_o + 16 * j, o);
-                tmem_wait_ld();
+            for (int j = 0; j < 8 && i > 0; ++j) {
+              float o[16];
+              tmem_ld16(t_o + 16 * j, o);
+              tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= alpha;
-                tmem_st16(t_o + 16 * j, o);
-              }
+              for (int k = 0; k < 16; ++k) o[k] *= alpha;
+              tmem_st16(t_o + 16 * j, o);
             }
           }
-          const float neg_m = -m;
 #pragma unroll
           for (int j = 0; j < 4; ++j) l[j][0] = l[j][1] = 0.f;
           float s[2][32];  // 32 scores on their way while 32 are worked on
           tmem_ld32(t_s, s[0]);
           tmem_wait_ld();
+          const float neg_m = -m;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j < 3) tmem_ld32(t_s + 32 * (j + 1), s[(j + 1) & 1]);
@@ -576,9 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j < 3) tmem_wait_ld();
           }
           l[0][0] = (l[0][0] + l[0][1]) + (l[1][0] + l[1][1]) + ((l[2][0] + l[2][1]) + (l[3][0] + l[3][1]));
-          if (again || i == 0 || !__any_sync(0xffffffffu, !(l[0][0] <= kMoveSum))) break;
-          look = again = true;
-        }
+          again = !again && __any_sync(0xffffffffu, !(l[0][0] <= kMoveSum));
+        } while (again);
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_st16u(t_s + 16 * j, pk[j]);
         tmem_wait_st();
@@ -655,35 +665,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.ws_lse[(static_cast<int64_t>(it->split) * p.h_k * p.group + h) * p.total_q + tok] = -INFINITY;
         }
         const uint32_t t_o = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO + 128 * x;
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-          float o[16];
-          if (it->n[x] > 0) {
-            tmem_ld16(t_o + 16 * j, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
-          if (!row) continue;
-          if (p.splits == 1 && p.out_wide) {
-            uint32_t w[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[2 * k], o[2 * k + 1]);
-            st_global_v8(dst + 2 * j, w);
-          } else if (p.splits == 1) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              dst[2 * j + k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                          pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) st_global_v8(ws + 4 * j + 2 * k, reinterpret_cast<const uint32_t(&)[8]>(o[8 * k]));
-          }
-        }
-        if (it->n[x] > 0) {
+        auto freed = [&]() {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sm->o_free[x]));
+        };
+        if (it->n[x] > 0 && p.splits == 1) {
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            float o[32];
+            tmem_ld32(t_o + 32 * j, o);
+            tmem_wait_ld();
+            uint32_t w[2][8];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k / 8][k % 8] = inv != 0.f ? pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+            if (row && p.out_wide) {
+              st_global_v8(dst + 4 * j, w[0]);
+              st_global_v8(dst + 4 * j + 2, w[1]);
+            } else if (row) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) dst[4 * j + k] = make_uint4(w[k / 2][4 * (k & 1)], w[k / 2][4 * (k & 1) + 1], w[k / 2][4 * (k & 1) + 2], w[k / 2][4 * (k & 1) + 3]);
+            }
+          }
+          freed();
+        } else if (it->n[x] > 0) {
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j) {
+            float o[16];
+            tmem_ld16(t_o + 16 * j, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
+            if (row) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) st_global_v8(ws + 4 * j + 2 * k, reinterpret_cast<const uint32_t(&)[8]>(o[8 * k]));
+            }
+          }
+          freed();
+        } else if (row && p.splits == 1) {  // (a partial row with an lse of -inf is not read)
+#pragma unroll 1
+          for (int j = 0; j < 16; ++j) dst[j] = make_uint4(0u, 0u, 0u, 0u);
         }
         // what was taken out, onto the rows that see it
         if (it->n[x] > 0 && *reinterpret_cast<const volatile uint32_t*>(&it->odd) != 0u && row && inv != 0.f) {
