@@ -19,7 +19,7 @@
 namespace mla {
 namespace merge {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Params {
   const void* parts;                             // bf16 or fp32
@@ -27,7 +27,7 @@ struct Params {
   const float* lses;
   int64_t lse_part, lse_head, lse_token;
   int n, heads, d;
-  uint32_t tokens, run;  // run: set by the launch
+  uint32_t tokens;
   const int32_t* rows_from;  // optional: only tokens [*rows_from, *rows_to) are written
   const int32_t* rows_to;
   __nv_bfloat16* out;
@@ -74,20 +74,23 @@ struct Unit {
   }
 };
 
+// Blocks on an SM, as far as registers go: the more rows are on their way the better
+// (five states of 2048 x 128 heads x 128: 93 us with 3 blocks of 256 threads, 74 = 5.5 TB/s so;
+// 82 with half as many parts in flight and more blocks, 78 with blocks that walk several rows).
+template <bool kF32, int kUnits, int kAhead>
+constexpr int kBlocks = kUnits * kAhead * (kF32 ? 2 : 1) < 8 || !(kF32 || kUnits == 2) ? 8 : (kF32 && kUnits == 2 ? 6 : 7);
+
 // kLanes lanes a row, kUnits units of eight columns a lane, kAhead parts' units in flight: the
 // first are requested before the weights are known.  (A row read for nothing, because its
 // weight turns out 0, leaves no trace.)
 template <bool kF32, int kLanes, int kUnits, int kAhead>
-__global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocks<kF32, kUnits, kAhead>) merge_kernel(const __grid_constant__ Params p) {
   static_assert(kLanes % kAhead == 0, "parts of a step have their weights in one register each");
   pdl_launch_dependents();
   pdl_wait_primary();
   const int l = threadIdx.x % kLanes;
   const uint32_t row = (blockIdx.x * static_cast<uint32_t>(kThreads) + threadIdx.x) / kLanes;
-  // Rows of `run` neighbouring tokens of a head, then of the next head: where log-sum-exps lie token by
-  // token, a sector of them is then used by one block.
-  const uint32_t rest = row / p.run, head = rest % p.heads;
-  const uint32_t t = rest / p.heads * p.run + row % p.run;
+  const uint32_t t = row / p.heads, head = row - t * p.heads;
   bool in = t < p.tokens;
   if (p.rows_from) in = in && static_cast<int32_t>(t) >= *p.rows_from && static_cast<int32_t>(t) < *p.rows_to;
   const int64_t tok = in ? t : 0;
@@ -141,10 +144,9 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
 }
 
 template <bool kF32>
-int launch_type(Params p, cudaStream_t stream) {
-  p.run = p.heads > 1 && p.lse_head != 1 ? 8 : 1;
+int launch_type(const Params& p, cudaStream_t stream) {
   const auto go = [&](auto kernel, int lanes) {
-    const int64_t rows = (p.tokens + p.run - 1) / p.run * p.run * p.heads, per = kThreads / lanes;
+    const int64_t rows = static_cast<int64_t>(p.tokens) * p.heads, per = kThreads / lanes;
     return launch_step(kernel, p, (rows + per - 1) / per, 1, kThreads, stream, "merge kernel launch");
   };
   constexpr int kMore = kF32 ? 4 : 8;
