@@ -520,6 +520,7 @@ int mla_window_decode(const void* q, const void* kv_cache, int kv_format, int64_
  * Packed sequences, common to the first two: sequence i owns rows cu[i] .. cu[i + 1] - 1
  * of a packed tensor; cu is [batch + 1] int32 in device memory, cu[0] >= 0, no entry
  * below the one before, the last at most the tensor's rows.  Sequences may be empty.
+ * At most 2^16 sequences and 2^25 rows.
  * Rows before the first sequence and behind the last are left as they were.
  */
 
@@ -531,7 +532,7 @@ int mla_window_decode(const void* q, const void* kv_cache, int kv_format, int64_
  *               mla_append_kv.
  *  starts       optional [batch] int32 (NULL: zeros): the first token read of
  *               each request; any position, not only a page's first.
- *  rows         rows of out, at most 2^27.
+ *  rows         rows of out.
  *  out          [rows, 576] bf16 ([rows, 512] for MLA_KV_FP8_528), rows out_stride
  *               elements apart (a multiple of 8).  MLA_KV_BF16: the row as it is.
  *               MLA_KV_FP8_656: code * scale in fp32, rounded once; the position columns
@@ -576,15 +577,15 @@ int mla_prefill_workspace_size(int64_t total_q, int64_t total_k, int batch, int 
  *  cu_seqlens_q, cu_seqlens_k: packed sequences (above) of q and out, and of k, k_rope
  *               and v.  Others set MLA_DEVERR_BAD_RANGE; the rows they name are then taken as far
  *               as they exist, and outputs are unspecified.
- *  h_q / h_k    a whole number of 1 .. 128.  total_q, total_k: at most 2^27 rows.
+ *  h_q / h_k    a whole number of 1 .. 128.
  *  num_sm_parts from mla_num_sm_parts for up to 64 heads (any value >= 1 gives the same
  *               result up to rounding).
  *  workspace    workspace_bytes bytes, at least mla_prefill_workspace_size(), 32-byte
  *               aligned; NULL when that is 0.
  *  A query that sees no key gets out = 0, lse = -inf.  What a query does not see leaves
  *  no trace in its outputs, NaN and infinities included.  One that sees a key with a
- *  NaN gets NaN in its whole row and lse, one that sees a value that is not finite gets it in
- *  that column.  out must not overlap the inputs.
+ *  NaN gets NaN in its whole row and lse, one that sees a value that is not finite gets
+ *  one in that column.  out must not overlap the inputs.
  */
 int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
                 int64_t k_token_stride, int64_t k_head_stride, const void* k_rope,
@@ -606,7 +607,7 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
  *  lses         n x [h_q, tokens] fp32 by strides (mla_decode's [batch, h_q, 1] and
  *               mla_prefill's [h_q, total_q] both fit)
  *  out, lse     [tokens, h_q, d] bf16 and [h_q, tokens] fp32, by strides
- *  (tokens + 8) * h_q <= 2^31.  A part with lse_i = -inf has no weight and its row
+ *  tokens * h_q <= 2^31.  A part with lse_i = -inf has no weight and its row
  *  leaves no trace, whatever it holds; a row without any other gets out = 0, lse = -inf.  out may be one of the parts itself with
  *  the same strides, and lse its lse; otherwise outputs must not overlap inputs.  Sums are fp32,
  *  each output rounded once.

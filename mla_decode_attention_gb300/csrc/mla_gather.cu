@@ -157,7 +157,7 @@ extern "C" int mla_gather_kv(const void* kv_cache, int kv_format, int64_t num_pa
                              int64_t block_table_stride, int64_t max_pages, const int32_t* cu_seqlens, const int32_t* starts,
                              int batch, int64_t rows, void* out, int64_t out_stride, uint32_t* err, cudaStream_t stream) {
   if (kv_format != MLA_KV_BF16 && kv_format != MLA_KV_FP8_656 && kv_format != MLA_KV_FP8_528) return MLA_ERR_UNSUPPORTED;
-  if (batch <= 0 || rows < 0 || rows > kMaxPackedRows) return MLA_ERR_SHAPE;
+  if (batch <= 0 || batch > kMaxSequences || rows < 0 || rows > kMaxPackedRows) return MLA_ERR_SHAPE;
   if (num_pages <= 0 || num_pages > (int64_t{1} << 25) || max_pages <= 0 || (batch > 1 && block_table_stride < max_pages))
     return MLA_ERR_SHAPE;
   if (out_stride < (kv_format == MLA_KV_FP8_528 ? kV41HeadDim : kDqk) || out_stride > kMaxTokenStride) return MLA_ERR_SHAPE;

@@ -20,8 +20,11 @@ inline bool heads_supported(int h) {
 }
 inline int head_blocks(int h) { return (h + kHeadsPerCta - 1) / kHeadsPerCta; }
 
-// Most rows of a packed tensor (all its sequences together).
-constexpr int64_t kMaxPackedRows = int64_t{1} << 27;
+// Most rows of a packed tensor (all its sequences together), most sequences: what one
+// block works on between two signals (a sequence's keys, the search for its next
+// item) stays well below the limit of the waits.
+constexpr int64_t kMaxPackedRows = int64_t{1} << 25;
+constexpr int kMaxSequences = 1 << 16;
 
 inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -9,7 +9,7 @@ extern "C" int mla_merge_states(const void* parts, int parts_fp32, int64_t part_
                                 int64_t out_token_stride, int64_t out_head_stride, float* lse, int64_t out_lse_head_stride,
                                 int64_t out_lse_token_stride, cudaStream_t stream) {
   if (n <= 0 || h_q <= 0 || tokens < 0 || d < 8 || d > 512 || d % 8 != 0) return MLA_ERR_SHAPE;
-  if (tokens > (int64_t{1} << 31) / h_q - 8) return MLA_ERR_SHAPE;  // (rows are counted in 32 bits)
+  if (tokens > (int64_t{1} << 31) / h_q) return MLA_ERR_SHAPE;  // (rows are counted in 32 bits)
   if (tokens == 0) return MLA_OK;
   if (!parts || !lses || !out || !lse) return MLA_ERR_NULL;
   for (const int64_t s : {part_stride, token_stride, head_stride, lse_part_stride, lse_head_stride, lse_token_stride,

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kF32, kUnits, kAhead>) merge
   pdl_launch_dependents();
   pdl_wait_primary();
   const int l = threadIdx.x % kLanes;
-  const uint32_t row = (blockIdx.x * static_cast<uint32_t>(kThreads) + threadIdx.x) / kLanes;
+  const uint32_t row = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const uint32_t t = row / p.heads, head = row - t * p.heads;
   bool in = t < p.tokens;
   if (p.rows_from) in = in && static_cast<int32_t>(t) >= *p.rows_from && static_cast<int32_t>(t) < *p.rows_to;

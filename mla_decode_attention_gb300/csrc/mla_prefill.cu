@@ -33,7 +33,7 @@ int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int
 }
 
 int check_sizes(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {
-  if (batch <= 0 || batch > (1 << 24) || total_q < 0 || total_q > kMaxPackedRows || total_k < 0 || total_k > kMaxPackedRows)
+  if (batch <= 0 || batch > kMaxSequences || total_q < 0 || total_q > kMaxPackedRows || total_k < 0 || total_k > kMaxPackedRows)
     return MLA_ERR_SHAPE;
   // (the kernel counts blocks of query rows in 32 bits)
   if (h_q <= 0 || h_k <= 0 || h_q % h_k != 0 || h_q / h_k > kRows || h_q > (1 << 16) || num_sm_parts <= 0) return MLA_ERR_SHAPE;

@@ -58,11 +58,11 @@ constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
 constexpr int kSmemData = 14 * kChunk;
 constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring holds parts of
-// Probabilities are taken against a reference: the score of the first key, and the row's
-// maximum from where a tile's probabilities sum past 2^40 on.  Sums, outputs and
-// the bf16 probabilities (8 bits of exponent) stay in range either way, and O is
-// hardly ever rescaled.
-constexpr float kRescaleLog2 = 30.f, kMoveSum = 1099511627776.f;
+// Probabilities are taken against a reference 2^20 above the score of a piece's first key, and
+// above the row's maximum from where a tile's probabilities sum past 1 on.  It need not be
+// near the maximum: bf16 has fp32's exponents, so probabilities keep their precision
+// wherever they lie.  So the maximum is hardly ever looked for and O hardly ever rescaled.
+constexpr float kAbove = 20.f, kMoveSum = 1.f;
 constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescPv = idesc_bf16(128, 128, false, true);
 constexpr uint32_t kIdescPvHalf = idesc_bf16(128, 64, false, true);
@@ -526,11 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        // A piece's first key gives the reference: it need not be near the row's maximum, only so near
-        // that nothing leaves fp32's and bf16's range (their exponents are alike).
-        if (i == 0) {
+        if (i == 0) {  // (a score of -inf says nothing: any other then passes the bound)
           const float u = tmem_ld1(t_s);
-          m = u == -INFINITY ? 0.f : u * sc;
+          m = u == -INFINITY ? -1e38f : u * sc + kAbove;
         }
         // The row maximum is looked for only where the probabilities sum past the bound, which one of
         // them far above the reference needs; the warp then takes the pass again.
@@ -547,9 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 16; k += 2) top = fmax3(top, v[k], v[k + 1]);
             }
-            top *= sc;
-            // (this tile's scores were issued after the last tile's p.v and have completed: O holds every tile before)
-            const bool move = top > m + kRescaleLog2;
+            // (this tile's scores were issued after the last tile's p.v and have completed: O holds every tile
+            // before; a row moves by its own sum alone, whatever its neighbours in the warp do)
+            top = top * sc + kAbove;
+            const bool move = !(l[0][0] <= kMoveSum) && top > m;
             const float alpha = move ? fast_exp2(m - top) : 1.f;
             m = move ? top : m;
             lsum *= alpha;
@@ -587,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j < 3) tmem_wait_ld();
           }
           l[0][0] = (l[0][0] + l[0][1]) + (l[1][0] + l[1][1]) + ((l[2][0] + l[2][1]) + (l[3][0] + l[3][1]));
-          again = !again && __any_sync(0xffffffffu, !(l[0][0] <= kMoveSum));
+          again = !again && __any_sync(0xffffffffu, row && !(l[0][0] <= kMoveSum));
         } while (again);
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_st16u(t_s + 16 * j, pk[j]);

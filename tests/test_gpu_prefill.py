@@ -192,6 +192,34 @@ def test_rising_scores_move_the_reference():
     check(c, *run(c), "falling")
 
 
+@pytest.mark.parametrize("others", [0.0, -40.0, 40.0])
+def test_first_keys_that_have_no_weight(others):
+    """The first key's score is -inf, or far below the others', or far above: 40 * 2^0.5 * 128 / 128^0.5 = 640 in the exponent."""
+    for first in (-float("inf"), -3000.0, 0.0, 60.0):
+        c = case([70], [400], 2, rope="none", causal=False)
+        c["q"].fill_(2.0 ** 0.5)
+        c["k"].normal_(0, 0.05, generator=torch.Generator().manual_seed(4)).add_(others)
+        c["k"][0] = first
+        check(c, *run(c), f"{first}")
+
+
+def test_lowest_values_in_unseen_places():
+    c = case([50, 200], [90, 300], 3, before=40, behind=40)
+    clean = run(c)
+    low = torch.finfo(torch.bfloat16).min
+    for name in ("q", "k", "v", "rope"):
+        cu = c["cu_q"] if name == "q" else c["cu_k"]
+        c[name][:cu[0]] = low
+        c[name][cu[-1]:] = low
+    out, lse = run(c)
+    assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+    for name in ("k", "v", "rope"):
+        c[name][c["cu_k"][1] + 250:c["cu_k"][2]] = low       # seen by the last 50 queries only
+    out, lse = run(c)
+    seen = slice(0, c["cu_q"][2] - 50)
+    assert torch.equal(out[seen], clean[0][seen]) and torch.equal(lse[:, seen], clean[1][:, seen])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("h,h_k", [(2, 2), (6, 2)])
 def test_values_that_are_not_finite_reach_only_those_who_see_them(bad, h, h_k):

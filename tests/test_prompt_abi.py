@@ -34,7 +34,7 @@ def call(name, base, over):
 
 @pytest.mark.parametrize("over,code", [
     (dict(cache=None), -1), (dict(bt=None), -1), (dict(cu=None), -1), (dict(out=None), -1), (dict(b=0), -2), (dict(rows=-1), -2),
-    (dict(rows=(1 << 27) + 1), -2), (dict(pages=0), -2), (dict(pages=(1 << 25) + 1), -2), (dict(width=0), -2), (dict(bts=3), -2),
+    (dict(rows=(1 << 25) + 1), -2), (dict(b=(1 << 16) + 1), -2), (dict(pages=0), -2), (dict(pages=(1 << 25) + 1), -2), (dict(width=0), -2), (dict(bts=3), -2),
     (dict(stride=568), -2), (dict(stride=1 << 40), -2), (dict(fmt=2, stride=504), -2), (dict(stride=580), -3), (dict(cache=0x10008), -3),
     (dict(out=0x40002), -3), (dict(fmt=3), -6), (dict(fmt=-1), -6), (dict(rows=0, out=None, cache=None, cu=None), 0),
 ])
@@ -45,7 +45,7 @@ def test_gather_refuses(over, code):
 @pytest.mark.parametrize("over,code", [
     (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(cuq=None), -1), (dict(cuk=None), -1), (dict(out=None), -1),
     (dict(lse=None), -1), (dict(nq=1, nk=100000, parts=152, b=1, ws=None), -1), (dict(nq=1, nk=100000, parts=152, b=1, wsb=1000), -2),
-    (dict(b=0), -2), (dict(b=(1 << 24) + 1), -2), (dict(nq=-1), -2), (dict(nk=-1), -2), (dict(nq=(1 << 27) + 1), -2), (dict(nk=1 << 28), -2),
+    (dict(b=0), -2), (dict(b=(1 << 16) + 1), -2), (dict(nq=-1), -2), (dict(nk=-1), -2), (dict(nq=(1 << 25) + 1), -2), (dict(nk=1 << 26), -2),
     (dict(h=0), -2), (dict(hk=0), -2), (dict(h=3), -2), (dict(h=130, hk=1), -2), (dict(parts=0), -2), (dict(scale=0.0), -2),
     (dict(scale=-1.0), -2), (dict(scale=NAN), -2), (dict(scale=float("inf")), -2), (dict(qh=184), -2), (dict(qt=184), -2),
     (dict(kh=120), -2), (dict(kt=0), -2), (dict(vh=0), -2), (dict(vt=120), -2), (dict(rt=56), -2), (dict(rh=56), -2), (dict(ot=128), -2),
