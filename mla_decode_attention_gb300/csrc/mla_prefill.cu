@@ -181,9 +181,10 @@ extern "C" int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head
   p.batch = batch;
   p.total_q = static_cast<int>(total_q);
   p.total_k = static_cast<int>(total_k);
-  p.h_k = h_k;
+  p.h_k = static_cast<uint32_t>(h_k);
   p.group = group;
   p.tokens = tokens;
+  p.per_inverse = ((uint64_t{1} << 38) + 2 * tokens - 1) / (2 * tokens);
   p.causal = causal != 0;
   p.rope_per_head = rope_per_head;
   p.splits = splits;

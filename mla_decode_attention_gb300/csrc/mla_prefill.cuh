@@ -57,6 +57,7 @@ constexpr int kKeys = 128;    // keys of a tile
 constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
 constexpr int kSmemData = 14 * kChunk;
+constexpr int kItems = 2;     // the one that is worked on, and the next
 constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring holds parts of
 // Probabilities are taken against a reference 2^20 above the score of a piece's first key, and
 // above the row's maximum from where a tile's probabilities sum past 1 on.  It need not be
@@ -73,8 +74,10 @@ struct Params {
   const int32_t* cu_q;   // [batch + 1]
   const int32_t* cu_k;
   int batch, total_q, total_k;
-  int h_k, group;        // key heads, query heads of each
+  uint32_t h_k;          // key heads
+  int group;             // query heads of each
   int tokens;            // tokens of a tile: 128 / group
+  uint64_t per_inverse;  // 2^38 / (2 * tokens), rounded up: quotients of up to 2^26 by it
   int causal;
   int rope_per_head;     // k_rope has a head dimension
   int splits;
@@ -108,6 +111,7 @@ struct Item {
   int32_t split;
   int32_t first;      // first key tile
   int32_t n[2];       // key tiles of each tile of query rows
+  int32_t off[2];     // each one's first token (n_tok or more: it has none)
   uint32_t odd;       // a value that is not finite was taken out
 };
 
@@ -116,9 +120,9 @@ struct Shared {
   uint64_t answered;
   uint64_t k_full[kDepth], k_empty[kDepth], v_full[kDepth], v_empty[kDepth];  // of a key tile's chunks
   uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], sums_full[2], sums_free[2];
-  uint64_t item_full[2], item_empty[2];
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t edge[kDepth];
-  Item items[2];
+  Item items[kItems];
   uint32_t tmem;
   uint32_t abort;
   float inv[2][kRows];  // 1 / (sum of a row's probabilities); 0 for a row that sees no key
@@ -179,6 +183,7 @@ struct Window {
   uint32_t before, all;     // items of sequences before these, of these
   int q0, q_len, k0, k_len; // of the lane's sequence
   uint32_t blocks, mine, upto;  // its blocks of query rows, its items, those up to its last
+  uint32_t heads;           // of a group of its
 };
 
 __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, uint32_t before, int lane) {
@@ -209,8 +214,9 @@ __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, ui
   w.k0 = __shfl_sync(0xffffffffu, k0, from);
   w.k_len = __shfl_sync(0xffffffffu, k_len, from);
   const int per = 2 * p.tokens;
-  w.blocks = static_cast<uint32_t>(w.q_len + per - 1) / per;
+  w.blocks = static_cast<uint32_t>(static_cast<uint64_t>(w.q_len + per - 1) * p.per_inverse >> 38);
   w.mine = w.upto = w.blocks * (p.h_k * p.splits);
+  w.heads = w.blocks * p.h_k <= 2 * p.parts ? p.h_k : max(2 * p.parts / w.blocks, 1u);
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(0xffffffffu, w.upto, o);
@@ -222,8 +228,10 @@ __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, ui
 // Finds item `index` of the call (lanes of one warp together).  A sequence's items lie by
 // groups of heads, as many as fill the device twice (their keys and values, some 40 MB whatever
 // the length, stay in L2 meanwhile); in a group blocks of query rows come from the last, which
-// has the most keys, to the first, the heads' beside each other, and a block's splits.
-__device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Window& w, Item& out, int lane) {
+// has the most keys, to the first, the heads' beside each other, and a block's splits.  Rows of an
+// item that fill one tile only are tile 0 or 1 by turns: the next item's products and softmax then
+// run beside it.
+__device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Window& w, Item& out, uint32_t turn, int lane) {
   if (w.base < 0 || index < w.before) look_at(p, w, 0, 0u, lane);
   while (index - w.before >= w.all) {
     if (w.base + 32 >= p.batch) return false;
@@ -234,10 +242,12 @@ __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Windo
   if (hit == 0u) return false;  // (sequences that overlap beyond 32 bits of items)
   if (lane == __ffs(hit) - 1) {
     const uint32_t blocks = w.blocks;
-    const uint32_t heads = min(max(2 * p.parts / blocks, 1u), static_cast<uint32_t>(p.h_k));
-    const uint32_t first_head = local / (heads * blocks * p.splits) * heads, rem = local - first_head * blocks * p.splits;
-    const uint32_t here = min(heads, p.h_k - first_head);  // (the last group may be smaller)
-    const int split = rem % p.splits, head = first_head + rem / p.splits % here, block = blocks - 1 - rem / p.splits / here;
+    // (most calls have a group or a piece; divisions take as long as a load)
+    const uint32_t first_head = w.heads >= p.h_k ? 0u : local / (w.heads * blocks * p.splits) * w.heads;
+    const uint32_t here = min(w.heads, p.h_k - first_head);  // (the last group may be smaller)
+    const uint32_t rem = local - first_head * blocks * p.splits, by_split = p.splits == 1 ? rem : rem / p.splits;
+    const uint32_t row = by_split / here;
+    const int split = rem - by_split * p.splits, head = first_head + by_split - row * here, block = blocks - 1 - row;
     const int per = 2 * p.tokens, at = block * per;
     Item it;
     it.q_row = w.q0 + at;
@@ -247,15 +257,17 @@ __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Windo
     it.seen0 = w.k_len - w.q_len + at + 1;
     it.head = head;
     it.split = split;
+    it.off[0] = it.n_tok <= p.tokens && turn != 0 ? p.tokens : 0;
+    it.off[1] = it.n_tok <= p.tokens && turn != 0 ? 0 : p.tokens;
     int tiles[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int last = min(it.n_tok, (x + 1) * p.tokens) - 1;  // the tile's last token
-      tiles[x] = last >= x * p.tokens ? (seen_by(it, last, p.causal) + kKeys - 1) / kKeys : 0;
+      const int last = min(it.n_tok, it.off[x] + p.tokens) - 1;  // the tile's last token
+      tiles[x] = last >= it.off[x] ? (seen_by(it, last, p.causal) + kKeys - 1) / kKeys : 0;
     }
     const int most = max(tiles[0], tiles[1]);
-    it.first = most * split / p.splits;  // (2^20 tiles, 2^5 splits at most)
-    const int end = most * (split + 1) / p.splits;
+    it.first = p.splits == 1 ? 0 : most * split / p.splits;  // (2^18 tiles, 2^5 splits at most)
+    const int end = p.splits == 1 ? most : most * (split + 1) / p.splits;
 #pragma unroll
     for (int x = 0; x < 2; ++x) it.n[x] = max(min(tiles[x], end) - it.first, 0);
     it.odd = 0u;
@@ -434,6 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm->o_free[i]), 4);
       mbar_init(bar(sm->sums_full[i]), 4);
       mbar_init(bar(sm->sums_free[i]), 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
       mbar_init(bar(sm->item_full[i]), 1);
       mbar_init(bar(sm->item_empty[i]), 15);  // all warps but the one that fills them
     }
@@ -461,15 +475,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t it_n = 0;
   const Item* it = sm->items;
   auto next_item = [&]() -> bool {
-    const uint32_t slot = it_n & 1;
-    bool ok = wait_for(bar(sm->item_full[slot]), (it_n >> 1) & 1, abort_flag);
+    const uint32_t slot = it_n % kItems;
+    bool ok = wait_for(bar(sm->item_full[slot]), (it_n / kItems) & 1, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) return false;
     it = &sm->items[slot];
     return it->n_tok > 0;
   };
   auto done_item = [&]() {
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(sm->item_empty[it_n & 1]));
+    if (lane == 0) mbar_arrive(bar(sm->item_empty[it_n % kItems]));
     ++it_n;
   };
 
@@ -485,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && next_item()) {
       const int n = it->n[x];
-      const int at = x * p.tokens + my_tok;
+      const int at = it->off[x] + my_tok;
       const int seen = seen_by(*it, min(at, it->n_tok - 1), p.causal);
       const bool row = my_tok < p.tokens && at < it->n_tok;
       float m = 0.f, lsum = 0.f, bsum = 0.f;
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++edges;
           if (fix_values(ring + (tile * kPer + kQk + x) % kRing * kChunk, max(0, low - t * kKeys), min(kKeys, it->k_len - t * kKeys), r))
-            *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n & 1].odd) = 1u;
+            *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n % kItems].odd) = 1u;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sm->v_full[tile % kDepth]));
@@ -637,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && next_item()) {
 #pragma unroll 1
       for (int x = 0; x < 2 && ok; ++x) {
-        const int at = x * p.tokens + my_tok;
+        const int at = it->off[x] + my_tok;
         const bool row = my_tok < p.tokens && at < it->n_tok;
         const int64_t h = static_cast<int64_t>(it->head) * p.group + my_sub, tok = it->q_row + at;
         const int64_t part = (static_cast<int64_t>(it->split) * p.total_q + tok) * p.h_k * p.group + h;
@@ -821,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (it->n[x] == 0) return;
           if (!wait(sm->q_empty[x], (items[x]++ & 1) ^ 1)) return;
           expect_if(leader, bar(sm->q_full[x]), kQk * 128u * p.group * p.tokens);
-          const int q_row = uniform(it->q_row + x * p.tokens);
+          const int q_row = uniform(it->q_row + it->off[x]);
 #pragma unroll
           for (int c = 0; c < kQk; ++c)
             load_5d_if(leader, q_base + (x * kQk + c) * kChunk, &maps.q, 0, 0, q_row, c, head, bar(sm->q_full[x]), once);
@@ -868,8 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t index = blockIdx.x, asked = 0;
       bool have = true, ok = true;
       for (uint32_t k = 0;; ++k) {
-        Item* slot = &sm->items[k & 1];
-        ok = __all_sync(0xffffffffu, wait_for(bar(sm->item_empty[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag));
+        Item* slot = &sm->items[k % kItems];
+        ok = __all_sync(0xffffffffu, wait_for(bar(sm->item_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort_flag));
         bool found = false;
         while (ok && !found) {
           if (!have) {
@@ -882,12 +896,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok || !cancelled_block(smem_u32(&sm->answer), &index)) break;  // (after a no, no further question)
           }
           have = false;
-          found = find_item(p, index, window, *slot, lane);  // (the grid may have more blocks than items)
+          found = find_item(p, index, window, *slot, k & 1, lane);  // (the grid may have more blocks than items)
         }
         if (!ok) break;
         if (!found && lane == 0) slot->n_tok = 0;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sm->item_full[k & 1]));
+        if (lane == 0) mbar_arrive(bar(sm->item_full[k % kItems]));
         if (index == 0) check_ranges(p, lane);  // (by whoever has the first item)
         if (!found) break;
       }
