@@ -17,11 +17,14 @@ using prefill::kValue;
 
 // Pieces that each block of query rows' keys are cut into: a piece for every SM where
 // blocks are few, each at least kLeastTiles key tiles on average (a piece costs its query
-// rows, its fp32 rows and their merge).  Several sequences differ in length: then up to
-// three pieces an SM, of twice as many tiles, which go to whoever is free (3 sequences over 8000 to 16384
-// keys, 16 heads: 73 us with one an SM, 65 so, 70 with four; one sequence over 12000: 35, 39,
-// 44).  Known without the lengths, so that a workspace fits whatever they are.
-constexpr int kLeastTiles = 4, kMostSplits = 32;
+// rows, its fp32 rows and their merge, together about as much as two tiles; 10 tokens of 16
+// heads over 1500 keys: 16.3 us with four tiles at least, 13.7 with three, 13.0 with two; 1000
+// tokens of 16 heads, causal, 22.9, 24.8, 25.1).  Several sequences differ in length:
+// then up to three pieces an SM, of twice as many tiles, which go to whoever is free (3 sequences
+// over 8000 to 16384 keys, 16 heads: 73 us with one an SM, 65 so, 70 with four; one
+// sequence over 12000: 35, 39, 44).  Known without the lengths, so that a workspace fits
+// whatever they are.
+constexpr int kLeastTiles = 2, kMostSplits = 32;
 int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {
   const int64_t per = 2 * (kRows / (h_q / h_k));
   const int64_t blocks = (total_q + batch * (per - 1)) / per * h_k;
