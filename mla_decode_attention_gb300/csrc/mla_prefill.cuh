@@ -197,32 +197,35 @@ __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, ui
     k0 = min(max(p.cu_k[i], 0), p.total_k);
     k_len = min(max(p.cu_k[i + 1], k0), p.total_k) - k0;
   }
-  const int some = min(p.batch - base, 32);
-  int rank = 0;
-#pragma unroll 1
-  for (int o = 0; o < some; ++o) {
-    const int other = __shfl_sync(0xffffffffu, k_len, o);
-    rank += other > k_len || (other == k_len && o < lane);
-  }
-  if (lane >= some) rank = lane;
+  const int per = 2 * p.tokens;
+  w.blocks = static_cast<uint32_t>(static_cast<uint64_t>(q_len + per - 1) * p.per_inverse >> 38);
+  w.all = __reduce_add_sync(0xffffffffu, w.blocks) * (p.h_k * p.splits);
+  // the order counts where items wait for an SM and differ in length
+  const uint32_t tiles = static_cast<uint32_t>(k_len + kKeys - 1) / kKeys;
   int from = lane;
+  if (w.all > p.parts && __reduce_max_sync(0xffffffffu, w.blocks > 0 ? tiles : 0u) != __reduce_min_sync(0xffffffffu, w.blocks > 0 ? tiles : ~0u)) {
+    int rank = 0;
 #pragma unroll 1
-  for (int o = 0; o < some; ++o)
-    if (__shfl_sync(0xffffffffu, rank, o) == lane) from = o;
+    for (int o = 0; o < 32; ++o) {
+      const int other = __shfl_sync(0xffffffffu, k_len, o);
+      rank += other > k_len || (other == k_len && o < lane);
+    }
+#pragma unroll 1
+    for (int o = 0; o < 32; ++o)
+      if (__shfl_sync(0xffffffffu, rank, o) == lane) from = o;
+  }
   w.q0 = __shfl_sync(0xffffffffu, q0, from);
   w.q_len = __shfl_sync(0xffffffffu, q_len, from);
   w.k0 = __shfl_sync(0xffffffffu, k0, from);
   w.k_len = __shfl_sync(0xffffffffu, k_len, from);
-  const int per = 2 * p.tokens;
-  w.blocks = static_cast<uint32_t>(static_cast<uint64_t>(w.q_len + per - 1) * p.per_inverse >> 38);
+  w.blocks = __shfl_sync(0xffffffffu, w.blocks, from);
   w.mine = w.upto = w.blocks * (p.h_k * p.splits);
-  w.heads = w.blocks * p.h_k <= 2 * p.parts ? p.h_k : max(2 * p.parts / w.blocks, 1u);
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(0xffffffffu, w.upto, o);
     if (lane >= o) w.upto += v;
   }
-  w.all = __shfl_sync(0xffffffffu, w.upto, 31);
+  w.heads = w.blocks * p.h_k <= 2 * p.parts ? p.h_k : max(2 * p.parts / w.blocks, 1u);
 }
 
 // Finds item `index` of the call (lanes of one warp together).  A sequence's items lie by
