@@ -13,27 +13,43 @@
 // token, so the heads that share keys fill a tile together.  TMEM holds S0, S1 (the
 // tiles' scores, overwritten by their probabilities in bf16) and O0, O1: all 512
 // columns.  While the softmax warps of one tile turn S into P, the tensor cores work on the
-// other tile's products; per key tile they need 2 * (768 + 512) cycles (192 columns of
-// q.k, 128 of p.v), the exponentials about half of that.
+// other tile's products.  One pass over S with a reference that hardly ever moves: the
+// probabilities' fp32 sum divides O (dividing by the sum of the rounded ones instead, as the
+// decode kernels do, would take the rounding of a weight that dominates its row, 2^-9 at most, out of
+// the output, and costs 5 to 8 % here: softmax is on the products' way).
 //
-// The query rows stay in shared memory (96 KB); keys and values come through one ring of
-// 16 KB chunks [128 tokens x 64 columns] in the order K(0), V(0), K(1), V(1), ..., a
-// chunk of position columns shared by all heads being loaded by each block as K's
-// third.
+// The query rows stay in shared memory (96 KB, 64 KB without position columns); keys and
+// values come through one ring of 16 KB chunks [128 tokens x 64 columns] in the order
+// K(0), V(0), K(1), V(1), ... (1.6 key tiles, or 2.5), the position columns that the heads share as
+// the third chunk of each block's keys.
 //
-// Roles (512 threads):
+// Roles (512 threads; registers dealt out by setmaxnreg, 176, 72 and 88 a thread):
 //   warps 0..3, 4..7 : softmax of tile 0, of tile 1: thread r = query row r = TMEM lane r
-//   warps 8..11      : values that must not reach a product (fix_values), then outputs of
-//                      both tiles (O / l -> bf16, or an fp32 partial)
+//   warps 8..11      : outputs of both tiles (O / l -> bf16, or an fp32 partial)
 //   warps 12, 13     : products of tile 0, of tile 1
-//   warp 14          : lane 0 issues every TMA load
-//   warp 15          : works out the block's next item of work from the lengths
+//   warp 14          : TMA loads
+//   warp 15          : the block's next item of work (up to two tiles of query rows of one
+//                      sequence and key head), found from the lengths
 //
 // Values of keys that a row does not see have weight 0, but 0 times what is not finite
 // is NaN.  Tiles with keys that some row of the block does not see (at most three an
-// item) therefore pass through warps 8..11 before the products may read them: what lies behind the
-// sequence's end becomes zeros, and in what some rows see and others do not, values
-// that are not finite do; they are then added to the outputs of the rows that see them.
+// item) therefore pass through the softmax warps, while their scores are on the way, before
+// products may read them: what lies behind the sequence's end becomes zeros, and in what some
+// rows see and others do not, values that are not finite do; they are then added to
+// the outputs of the rows that see them.
+//
+// What bounds it.  A tile's chain: scores complete, softmax 0.55 us, p.v and the next q.k issued
+// behind it, 1280 (192 columns) or 1024 cycles, and three signals of 0.1 us.  The two tiles'
+// chains overlap, so that the tensor cores are busy 75 to 85 % of the time on long
+// items; an item's start and end cost about 2 us (first loads, both chains in step).
+// Measured: 76 heads of 4096 tokens over 4096 keys, no mask, 467 us = 1.75 PFLOP/s (92 % of the
+// matrix rate); one causal prompt of 16 heads of 16384 tokens 895 us = 1.53; two of 128 heads of 2048 and
+// 4096 551 us = 1.56; 61 of 1 to 601 tokens, 64 heads, 290 us = 4.7 TB/s; a single tile 6.5 us.
+// On the way here (16384 tokens): one lane walking the products' loop 1841 us, all lanes 1476,
+// whole boxes for two chunks and no row maxima 1288, a warp for each tile's products and code that fits
+// the instruction cache 1132, loads and descriptors off the way 997 and 865 to 935, without the
+// second sum 895.  Not kept: P handed over by halves (930), rolled halves, Q towards L2 ahead of its item,
+// both tiles on one tile's rows where rows are few.
 //
 // Waits are bounded; after one has run out every role leaves, and the block pauses
 // before it frees TMEM and ends.
@@ -59,11 +75,11 @@ constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
 constexpr int kSmemData = 14 * kChunk;
 constexpr int kItems = 2;     // the one that is worked on, and the next
 constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring holds parts of
-// Probabilities are taken against a reference 2^20 above the score of a piece's first key, and
+// Probabilities are taken against a reference 2^24 above the score of a piece's first key, and
 // above the row's maximum from where a tile's probabilities sum past 1 on.  It need not be
 // near the maximum: bf16 has fp32's exponents, so probabilities keep their precision
 // wherever they lie.  So the maximum is hardly ever looked for and O hardly ever rescaled.
-constexpr float kAbove = 20.f, kMoveSum = 1.f;
+constexpr float kAbove = 24.f, kMoveSum = 1.f;
 constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescPv = idesc_bf16(128, 128, false, true);
 constexpr uint32_t kIdescPvHalf = idesc_bf16(128, 64, false, true);
@@ -505,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = it->off[x] + my_tok;
       const int seen = seen_by(*it, min(at, it->n_tok - 1), p.causal);
       const bool row = my_tok < p.tokens && at < it->n_tok;
-      float m = 0.f, lsum = 0.f, bsum = 0.f;
+      float m = 0.f, lsum = 0.f;
       const int both = max(it->n[0], it->n[1]), low = seen_by(*it, 0, p.causal);
       for (int i = 0; i < both; ++i, ++tile) {
         const int t = it->first + i;
@@ -522,9 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar(sm->v_full[tile % kDepth]));
         }
         if (i >= n) continue;
-        ok = wait_for(bar(sm->s_full[x]), tiles++ & 1, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        wait_for(bar(sm->s_full[x]), tiles++ & 1, abort_flag);  // (after an abort the item runs out without waiting)
+        __syncwarp();
         tc_fence_after();
         const int lim = seen - t * kKeys;
         float l[4][2];  // (one chain of additions would take as long as the exponentials)
@@ -569,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float alpha = move ? fast_exp2(m - top) : 1.f;
             m = move ? top : m;
             lsum *= alpha;
-            bsum *= alpha;
 #pragma unroll 1
             for (int j = 0; j < 8 && i > 0; ++j) {
               float o[16];
@@ -611,17 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm->p_ready[x]));
-        // the rounded probabilities' sum, by which O is divided: off the products' way
-        float b[4][2] = {};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            asm("{ .reg .b64 a, b, c; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 c, a, b; mov.b64 {%0, %1}, c; }"
-                : "+f"(b[k & 3][0]), "+f"(b[k & 3][1])
-                : "f"(__uint_as_float(pk[j][k] << 16)), "f"(__uint_as_float(pk[j][k] & 0xFFFF0000u)));
         lsum += l[0][0];
-        bsum += (b[0][0] + b[0][1]) + (b[1][0] + b[1][1]) + ((b[2][0] + b[2][1]) + (b[3][0] + b[3][1]));
       }
       if (!ok) break;
       if (n > 0) {
@@ -637,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_for(bar(sm->sums_free[x]), (items & 1) ^ 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        sm->inv[x][r] = has ? __frcp_rn(bsum) : 0.f;
+        sm->inv[x][r] = has ? __frcp_rn(lsum) : 0.f;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm->sums_full[x]));
         ++items;
