@@ -74,6 +74,7 @@ constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
 constexpr int kSmemData = 14 * kChunk;
 constexpr int kItems = 2;     // the one that is worked on, and the next
+constexpr int kLead = 2;      // key tiles of an item still to be loaded when the next is looked for
 constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring holds parts of
 // Probabilities are taken against a reference 2^24 above the score of a piece's first key, and
 // above the row's maximum from where a tile's probabilities sum past 1 on.  It need not be
@@ -136,7 +137,7 @@ struct Shared {
   uint64_t answered;
   uint64_t k_full[kDepth], k_empty[kDepth], v_full[kDepth], v_empty[kDepth];  // of a key tile's chunks
   uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], o_free[2], sums_full[2], sums_free[2];
-  uint64_t item_full[kItems], item_empty[kItems];
+  uint64_t item_full[kItems], item_empty[kItems], item_ahead;
   uint64_t edge[kDepth];
   Item items[kItems];
   uint32_t tmem;
@@ -471,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(sm->item_empty[i]), 15);  // all warps but the one that fills them
     }
     mbar_init(bar(sm->answered), 1);
+    mbar_init(bar(sm->item_ahead), 1);
     sm->abort = 0u;
     fence_mbarrier_init();
     tma_prefetch_desc(&maps.q);
@@ -838,6 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = __reduce_max_sync(0xffffffffu, max(it->n[0], it->n[1])), head = uniform(it->head);
         const int rope_head = p.rope_per_head ? head : 0;
         int row = uniform(it->k_row + it->first * kKeys);
+        if (n <= kLead && lane == 0) mbar_arrive(bar(sm->item_ahead));
         auto queries = [&](int x) {
           if (it->n[x] == 0) return;
           if (!wait(sm->q_empty[x], (items[x]++ & 1) ^ 1)) return;
@@ -852,6 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n && ok; ++i, ++tile, row += kKeys) {
           const uint32_t c0 = uniform(tile * kPer % kRing), cv = (c0 + kQk) % kRing, o = tile % kDepth;
           if (tile >= kV && !wait(sm->v_empty[(tile - kV) % kDepth], ((tile - kV) / kDepth) & 1)) break;
+          if (i + kLead == n && i > 0 && lane == 0) mbar_arrive(bar(sm->item_ahead));
           const uint32_t kb = uniform(bar(sm->k_full[o]));
           expect_if(leader, kb, kQk * kChunk);
           if (!kHasRope || c0 + 1 < kRing) {
@@ -891,6 +895,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t k = 0;; ++k) {
         Item* slot = &sm->items[k % kItems];
         ok = __all_sync(0xffffffffu, wait_for(bar(sm->item_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort_flag));
+        // The next item is taken on when the last loads of the one before are due: early enough
+        // for its own, and so late that nobody sits on work that others could begin (64 on 8
+        // heads, three prompts: 134 us with an item in hand all the time, 125 so).
+        if (k > 0) ok = ok && __all_sync(0xffffffffu, wait_for(bar(sm->item_ahead), (k - 1) & 1, abort_flag));
         bool found = false;
         while (ok && !found) {
           if (!have) {
