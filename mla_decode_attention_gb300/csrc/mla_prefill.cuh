@@ -129,6 +129,7 @@ struct Item {
   int32_t first;      // first key tile
   int32_t n[2];       // key tiles of each tile of query rows
   int32_t off[2];     // each one's first token (n_tok or more: it has none)
+  int32_t ahead;      // the block of rows with the most keys: it sends for them first
   uint32_t odd;       // a value that is not finite was taken out
 };
 
@@ -290,6 +291,7 @@ __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Windo
     const int end = p.splits == 1 ? most : most * (split + 1) / p.splits;
 #pragma unroll
     for (int x = 0; x < 2; ++x) it.n[x] = max(min(tiles[x], end) - it.first, 0);
+    it.ahead = row == 0 && p.splits == 1;
     it.odd = 0u;
     out = it;
   }
@@ -388,6 +390,13 @@ __device__ __forceinline__ void commit_if(uint32_t leader, uint32_t bar) {
       "{ .reg .pred q; setp.ne.b32 q, %1, 0;"
       " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(leader)
       : "memory");
+}
+
+// A box towards L2.
+__device__ __forceinline__ void prefetch_4d_if(uint32_t leader, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile("{ .reg .pred q; setp.ne.b32 q, %5, 0; @q cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}]; }" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(leader)
+               : "memory");
 }
 
 // Asks for a block of this grid that has not begun not to begin: 16 bytes of answer at
@@ -869,6 +878,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok || (tile >= kK && !wait(sm->k_empty[(tile - kK) % kDepth], ((tile - kK) / kDepth) & 1))) break;
           // values of a tile with unseen keys complete on a barrier of the softmax warps', which then complete the products'
           const bool edge = edge_tile(*it, it->first + i, p.causal);
+          // the ring is short of a load's way from memory; of blocks on the same keys the longest sends
+          // for them (chunks of 512 tokens over 1000 to 7500 keys 286 -> 274 us, one prompt of 16384
+          // 855 -> 820; pieces of a few rows' keys are slower with it, 64 -> 67)
+          if (it->ahead && i + 2 < n) {
+            prefetch_4d_if(leader, &maps.k, 0, row + 2 * kKeys, 0, head);
+            prefetch_4d_if(leader, &maps.v, 0, row + 1 * kKeys, 0, head);
+          }
           const uint32_t vb = uniform(bar(edge ? sm->edge[edges++ % kDepth] : sm->v_full[o]));
           expect_if(leader, vb, 2 * kChunk);
           if (leader && !edge) mbar_arrive_many(vb, 7);
