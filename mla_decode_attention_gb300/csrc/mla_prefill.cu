@@ -29,7 +29,7 @@ int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int
   const int64_t per = 2 * (kRows / (h_q / h_k));
   const int64_t blocks = (total_q + batch * (per - 1)) / per * h_k;
   if (blocks == 0) return 1;
-  const int64_t tiles = total_k / batch / kKeys, sms = num_sm_parts;
+  const int64_t tiles = total_k / batch / kKeys, sms = std::min(num_sm_parts, 1 << 16);
   int64_t s = std::min(sms / blocks, tiles / kLeastTiles);
   if (batch > 1) s = std::max(s, std::min(3 * sms / blocks, tiles / (2 * kLeastTiles)));
   return static_cast<int>(std::clamp<int64_t>(s, 1, kMostSplits));

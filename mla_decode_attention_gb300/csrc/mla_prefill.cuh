@@ -733,11 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           freed();
-        } else if (row && p.splits == 1) {  // (a partial row with an lse of -inf is not read)
+        } else if (row && p.splits == 1) {  // (a partial row with an lse of -inf has no weight, whatever it holds)
 #pragma unroll 1
           for (int j = 0; j < 16; ++j) dst[j] = make_uint4(0u, 0u, 0u, 0u);
         }
-        // what was taken out, onto the rows that see it
+        // what was taken out, onto the rows that see it (infinities and NaN: a sum of them, whatever their weights)
         if (it->n[x] > 0 && *reinterpret_cast<const volatile uint32_t*>(&it->odd) != 0u && row && inv != 0.f) {
           const int low = seen_by(*it, 0, p.causal), end = (it->first + it->n[x]) * kKeys, mine = seen_by(*it, at, p.causal);
           const int from = low > it->first * kKeys ? low : it->first * kKeys, upto = mine < end ? mine : end;
@@ -751,10 +751,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(fabsf(f) < INFINITY)) sum += f;
             }
             if (sum == 0.f) continue;
-            if (p.splits == 1)
-              reinterpret_cast<__nv_bfloat16*>(dst)[c] = __float2bfloat16(sum);
-            else
-              reinterpret_cast<float*>(ws)[c] = sum;
+            if (p.splits == 1) {
+              __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(dst) + c;
+              *o = __float2bfloat16(__bfloat162float(*o) + sum);
+            } else {
+              reinterpret_cast<float*>(ws)[c] += sum;
+            }
           }
         }
       }

@@ -237,6 +237,19 @@ def test_values_that_are_not_finite_reach_only_those_who_see_them(bad, h, h_k):
         assert bool((out[rows].isnan() if bad != bad else out[rows] == bad).all())
 
 
+def test_what_is_not_finite_adds_up():
+    """inf and -inf in one column, one seen by all and one by some; a NaN key and an infinite value."""
+    c = case([20, 390, 33], [20, 390, 33], 2)
+    c["v"][20 + 3, 1, 5] = float("inf")           # in the first tile: seen by queries 3 .. of the sequence
+    c["v"][20 + 200, 1, 5] = -float("inf")
+    c["k"][20 + 300, 1, 9] = float("nan")
+    c["v"][20 + 310, 1, 7] = float("inf")
+    out, lse = run(c)
+    o = out[20:410, 1]
+    assert bool(o[:3].isfinite().all()) and bool((o[3:200, 5] == float("inf")).all()) and bool(o[200:, 5].isnan().all())
+    assert bool(o[300:].isnan().all()) and bool(o[:300, 7].isfinite().all()) and bool(lse[1, 320:410].isnan().all())
+
+
 def test_keys_that_are_not_finite_reach_only_those_who_see_them():
     for key in (0, 150, 389):
         for name in ("k", "rope"):
