@@ -575,8 +575,8 @@ int mla_prefill_workspace_size(int64_t total_q, int64_t total_k, int batch, int 
  *  lie beside each other in a projection's output, and the position columns in rows
  *  of mla_gather_kv.
  *  cu_seqlens_q, cu_seqlens_k: packed sequences (above) of q and out, and of k, k_rope
- *               and v.  Others set MLA_DEVERR_BAD_RANGE; the rows they name are then taken as far
- *               as they exist, and outputs are unspecified.
+ *               and v.  Others set MLA_DEVERR_BAD_RANGE; the rows they name are then
+ *               taken as far as they exist, and outputs are unspecified.
  *  h_q / h_k    a whole number of 1 .. 128.
  *  num_sm_parts from mla_num_sm_parts for up to 64 heads (any value >= 1 gives the same
  *               result up to rounding).
@@ -607,10 +607,10 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
  *  lses         n x [h_q, tokens] fp32 by strides (mla_decode's [batch, h_q, 1] and
  *               mla_prefill's [h_q, total_q] both fit)
  *  out, lse     [tokens, h_q, d] bf16 and [h_q, tokens] fp32, by strides
- *  tokens * h_q <= 2^31.  A part with lse_i = -inf has no weight and its row
- *  leaves no trace, whatever it holds; a row without any other gets out = 0, lse = -inf.  out may be one of the parts itself with
- *  the same strides, and lse its lse; otherwise outputs must not overlap inputs.  Sums are fp32,
- *  each output rounded once.
+ *  tokens * h_q <= 2^31.  A part with lse_i = -inf has no weight and its row leaves no
+ *  trace, whatever it holds; a row without any other gets out = 0, lse = -inf.  out may
+ *  be one of the parts itself with the same strides, and lse its lse; otherwise
+ *  outputs must not overlap inputs.  Sums are fp32, each output rounded once.
  */
 int mla_merge_states(const void* parts, int parts_fp32, int64_t part_stride, int64_t token_stride,
                      int64_t head_stride, const float* lses, int64_t lse_part_stride,

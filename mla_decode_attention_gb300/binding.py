@@ -460,7 +460,7 @@ def mla_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q:
 def mla_merge_states(parts: torch.Tensor, lses: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, stream=None) -> None:
     """Joins attention outputs over disjoint sets of keys: parts [n, tokens, h_q, d] bf16 or float32 (unit column
     stride), lses [n, h_q, tokens] float32 -> out [tokens, h_q, d] bf16, lse [h_q, tokens] float32.  out and lse may be
-    parts[i] and lses[i] themselves.  A part whose lse is -inf is not read."""
+    parts[i] and lses[i] themselves.  A part whose lse is -inf has no weight, whatever it holds."""
     status = (_step or _load_step()).merge_states(parts, lses, out, lse, stream)
     if status != 0:
         raise MlaError("mla_merge_states", status)

@@ -42,14 +42,16 @@
 // behind it, 1280 (192 columns) or 1024 cycles, and three signals of 0.1 us.  The two tiles'
 // chains overlap, so that the tensor cores are busy 75 to 85 % of the time on long
 // items; an item's start and end cost about 2 us (first loads, both chains in step).
-// Measured: 76 heads of 4096 tokens over 4096 keys, no mask, 467 us = 1.75 PFLOP/s (92 % of the
-// matrix rate); one causal prompt of 16 heads of 16384 tokens 895 us = 1.53; two of 128 heads of 2048 and
-// 4096 551 us = 1.56; 61 of 1 to 601 tokens, 64 heads, 290 us = 4.7 TB/s; a single tile 6.5 us.
+// Measured: 76 heads of 4096 tokens over 4096 keys, no mask, 464 us = 1.76 PFLOP/s (92 % of the
+// matrix rate); one causal prompt of 16 heads of 16384 tokens 820 us = 1.67; two of 128 heads of 2048 and
+// 4096 532 us = 1.61; 61 of 1 to 601 tokens, 64 heads, 283 us = 4.8 TB/s; a single tile 6.3 us.
 // On the way here (16384 tokens): one lane walking the products' loop 1841 us, all lanes 1476,
 // whole boxes for two chunks and no row maxima 1288, a warp for each tile's products and code that fits
-// the instruction cache 1132, loads and descriptors off the way 997 and 865 to 935, without the
-// second sum 895.  Not kept: P handed over by halves (930), rolled halves, Q towards L2 ahead of its item,
-// both tiles on one tile's rows where rows are few.
+// the instruction cache 1132, loads and descriptors off the way 997 and 935, without the
+// second sum 868, keys and values towards L2 820.  Not kept: P handed over by halves (930 where it was 895; the
+// ragged 61 and chunks of a prompt gained 3 %), the rounded probabilities' sum (5 to 8 % more everywhere), queries
+// and first keys towards L2 ahead of their item, both tiles on one tile's rows where rows are few, the
+// products' loop flattened across items (grouped heads 125 -> 155), four items in hand (137 -> 144).
 //
 // Waits are bounded; after one has run out every role leaves, and the block pauses
 // before it frees TMEM and ends.
@@ -97,7 +99,7 @@ struct Params {
   uint64_t per_inverse;  // 2^38 / (2 * tokens), rounded up: quotients of up to 2^26 by it
   int causal;
   int rope_per_head;     // k_rope has a head dimension
-  int splits;
+  int splits;            // pieces that a row's keys are cut into, at most
   uint32_t parts;        // SMs
   float scale_log2;      // softmax_scale * log2 e
   __nv_bfloat16* out;
