@@ -76,6 +76,7 @@ constexpr int kNope = 128, kRope = 64, kValue = 128;
 constexpr int kChunk = 16384; // [128 tokens x 64 columns] bf16
 constexpr int kSmemData = 14 * kChunk;
 constexpr int kItems = 2;     // the one that is worked on, and the next
+constexpr uint32_t kBeside = 8;  // blocks of a head's query rows whose items follow each other
 constexpr int kLead = 2;      // key tiles of an item still to be loaded when the next is looked for
 constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring holds parts of
 // Probabilities are taken against a reference 2^24 above the score of a piece's first key, and
@@ -251,7 +252,9 @@ __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, ui
 // Finds item `index` of the call (lanes of one warp together).  A sequence's items lie by
 // groups of heads, as many as fill the device twice (their keys and values, some 40 MB whatever
 // the length, stay in L2 meanwhile); in a group blocks of query rows come from the last, which
-// has the most keys, to the first, the heads' beside each other, and a block's splits.  Rows of an
+// has the most keys, to the first, eight of a head beside each other, and a block's splits.  (With a
+// head's blocks apart, all heads' between them, each read its keys from memory: 2 requests of 1024 tokens over 4000
+// and 8000 keys, 128 heads, 766 us, by twos 732, fours 661, eights 658, sixteens 657.)  Rows of an
 // item that fill one tile only are tile 0 or 1 by turns: the next item's products and softmax then
 // run beside it.
 __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Window& w, Item& out, uint32_t turn, int lane) {
@@ -269,8 +272,9 @@ __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Windo
     const uint32_t first_head = w.heads >= p.h_k ? 0u : local / (w.heads * blocks * p.splits) * w.heads;
     const uint32_t here = min(w.heads, p.h_k - first_head);  // (the last group may be smaller)
     const uint32_t rem = local - first_head * blocks * p.splits, by_split = p.splits == 1 ? rem : rem / p.splits;
-    const uint32_t row = by_split / here;
-    const int split = rem - by_split * p.splits, head = first_head + by_split - row * here, block = blocks - 1 - row;
+    const uint32_t from = blocks <= kBeside ? 0u : by_split / (here * kBeside) * kBeside;
+    const uint32_t in = by_split - here * from, beside = min(blocks - from, kBeside), hd = in / beside, row = from + in - hd * beside;
+    const int split = rem - by_split * p.splits, head = first_head + hd, block = blocks - 1 - row;
     const int per = 2 * p.tokens, at = block * per;
     Item it;
     it.q_row = w.q0 + at;
@@ -883,8 +887,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // values of a tile with unseen keys complete on a barrier of the softmax warps', which then complete the products'
           const bool edge = edge_tile(*it, it->first + i, p.causal);
           // the ring is short of a load's way from memory; of blocks on the same keys the longest sends
-          // for them (chunks of 512 tokens over 1000 to 7500 keys 286 -> 274 us, one prompt of 16384
-          // 855 -> 820; pieces of a few rows' keys are slower with it, 64 -> 67)
+          // for them (one prompt of 16384 tokens 855 -> 820 us; pieces of a few rows' keys are
+          // slower with it, 64 -> 67)
           if (it->ahead && i + 2 < n) {
             prefetch_4d_if(leader, &maps.k, 0, row + 2 * kKeys, 0, head);
             prefetch_4d_if(leader, &maps.v, 0, row + 1 * kKeys, 0, head);

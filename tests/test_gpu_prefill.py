@@ -1,8 +1,8 @@
 """GPU parity of mla_prefill against the fp64 definition.
 
 Tolerances.  A weight is rounded to bf16 once (half a step, 2^-8 relative) and the sum that
-divides is of the rounded ones (2^-8 again), so an output is off by at most
-2^-7 sum w |v|, by its own rounding, 2^-8 |out|, and by what the scores' fp32 arithmetic
+divides is fp32, of the unrounded ones, so an output is off by at most
+2^-8 sum w |v|, by its own rounding, 2^-8 |out|, and by what the scores' fp32 arithmetic
 leaves: 192 products and their sum, 192 * 2^-23 of sum |q k| * scale, here below 20 * 192 * 2^-23 =
 5e-4 in a score and a weight; 2^-10 of sum w |v| covers it.  The rounding errors are
 independent, so over a whole call their root mean square is far lower: rel-L2
@@ -84,7 +84,7 @@ def check(c, out, lse, what="", rel=OUT_REL_L2):
     assert np.all(np.isfinite(o)), what
     assert np.all(o.transpose(1, 0, 2)[none] == 0.0), what
     assert not none.size or np.max(np.abs(np.where(none, 0.0, l) - np.where(none, 0.0, want_lse)), initial=0.0) <= LSE_ABS, what
-    off = np.abs(o - want) - (2.0 ** -8 * np.abs(want) + (2.0 ** -7 + 2.0 ** -10) * size)
+    off = np.abs(o - want) - (2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -10) * size)
     assert np.max(off, initial=-1.0) <= 0.0, f"{what}: {np.max(off)} at {np.unravel_index(np.argmax(off), off.shape)}"
     norm = np.linalg.norm(want)
     if norm > 0:
@@ -113,6 +113,13 @@ def test_queries_and_keys_of_different_number(q_lens, k_lens, causal):
 @pytest.mark.parametrize("rope", ["shared", "own", "none"])
 def test_grouped_heads(h, h_k, rope):
     c = case([37, 150, 1], [37, 200, 90], h, h_k, rope, seed=h + h_k)
+    check(c, *run(c))
+
+
+@pytest.mark.parametrize("q_lens,k_lens,h,h_k", [([300, 7], [300, 7], 320, 40), ([2900], [2900], 2, 2), ([500, 1000], [1500, 1000], 44, 11)])
+def test_blocks_beside_each_other(q_lens, k_lens, h, h_k):
+    """More blocks of a head's rows than run side by side, heads in more than one group, both with a remainder."""
+    c = case(q_lens, k_lens, h, h_k, seed=h)
     check(c, *run(c))
 
 
