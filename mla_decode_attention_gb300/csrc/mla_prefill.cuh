@@ -25,18 +25,20 @@
 //
 // Roles (512 threads; registers dealt out by setmaxnreg, 176, 72 and 88 a thread):
 //   warps 0..3, 4..7 : softmax of tile 0, of tile 1: thread r = query row r = TMEM lane r
-//   warps 8..11      : outputs of both tiles (O / l -> bf16, or an fp32 partial)
+//   warps 8..11      : outputs of both tiles (O / l -> bf16, or an fp32 partial); values that
+//                      must not be multiplied as they are
 //   warps 12, 13     : products of tile 0, of tile 1
 //   warp 14          : TMA loads
 //   warp 15          : the block's next item of work (up to two tiles of query rows of one
 //                      sequence and key head), found from the lengths
 //
 // Values of keys that a row does not see have weight 0, but 0 times what is not finite
-// is NaN.  Tiles with keys that some row of the block does not see (at most three an
-// item) therefore pass through the softmax warps, while their scores are on the way, before
-// products may read them: what lies behind the sequence's end becomes zeros, and in what some
-// rows see and others do not, values that are not finite do; they are then added to
-// the outputs of the rows that see them.
+// is NaN.  Tiles with keys that some row of the block does not see (an item's last, at most
+// three) therefore pass through the output warps before products may read them: what
+// lies behind the sequence's end becomes zeros, and in what some rows see and others do not, values
+// that are not finite do; they are then added to the outputs of the rows that see
+// them.  (By the softmax warps, beside their scores: each tile's products then wait for both
+// tiles' softmax there; 61 short prompts 283 us, by the output warps 275.)
 //
 // What bounds it.  A tile's chain: scores complete, softmax 0.55 us, p.v and the next q.k issued
 // behind it, 1280 (192 columns) or 1024 cycles, and three signals of 0.1 us.  The two tiles'
@@ -44,7 +46,7 @@
 // items; an item's start and end cost about 2 us (first loads, both chains in step).
 // Measured: 76 heads of 4096 tokens over 4096 keys, no mask, 464 us = 1.76 PFLOP/s (92 % of the
 // matrix rate); one causal prompt of 16 heads of 16384 tokens 820 us = 1.67; two of 128 heads of 2048 and
-// 4096 532 us = 1.61; 61 of 1 to 601 tokens, 64 heads, 283 us = 4.8 TB/s; a single tile 6.3 us.
+// 4096 525 us = 1.63; 61 of 1 to 601 tokens, 64 heads, 275 us = 5.0 TB/s; a single tile 6.3 us.
 // On the way here (16384 tokens): one lane walking the products' loop 1841 us, all lanes 1476,
 // whole boxes for two chunks and no row maxima 1288, a warp for each tile's products and code that fits
 // the instruction cache 1132, loads and descriptors off the way 997 and 935, without the
@@ -258,7 +260,11 @@ __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, ui
 // item that fill one tile only are tile 0 or 1 by turns: the next item's products and softmax then
 // run beside it.
 __device__ __forceinline__ bool find_item(const Params& p, uint32_t index, Window& w, Item& out, uint32_t turn, int lane) {
-  if (w.base < 0 || index < w.before) look_at(p, w, 0, 0u, lane);
+  if (w.base < 0 || index < w.before) {
+    w.base = -32;
+    w.before = w.all = 0u;
+  }
+#pragma unroll 1
   while (index - w.before >= w.all) {
     if (w.base + 32 >= p.batch) return false;
     look_at(p, w, w.base + 32, w.before + w.all, lane);
@@ -341,7 +347,7 @@ __device__ __forceinline__ uint32_t note_odd(uint32_t x, uint32_t acc) {
 // each thread has eight of the chunk's 1024.
 __device__ __forceinline__ bool fix_values(uint32_t at, int seen, int valid, int thread) {
   uint32_t acc[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     uint4 v[4];
 #pragma unroll
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kDepth; ++i) {
       mbar_init(bar(sm->k_full[i]), 1);
       mbar_init(bar(sm->k_empty[i]), 2);
-      mbar_init(bar(sm->v_full[i]), 8);  // a load's arrival and seven more, or eight warps'
+      mbar_init(bar(sm->v_full[i]), 4);  // a load's arrival and three more, or four warps'
       mbar_init(bar(sm->v_empty[i]), 2);
       mbar_init(bar(sm->edge[i]), 1);
     }
@@ -531,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = t_lane + kColS + 128 * x, t_o = t_lane + kColO + 128 * x;
     const int my_tok = r / p.group, my_sub = r % p.group;
     const float sc = p.scale_log2;
-    uint32_t tile = 0, edges = 0, tiles = 0, items = 0;
+    uint32_t tiles = 0, items = 0;
     bool ok = true;
     while (ok && next_item()) {
       const int n = it->n[x];
@@ -539,22 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = seen_by(*it, min(at, it->n_tok - 1), p.causal);
       const bool row = my_tok < p.tokens && at < it->n_tok;
       float m = 0.f, lsum = 0.f;
-      const int both = max(it->n[0], it->n[1]), low = seen_by(*it, 0, p.causal);
-      for (int i = 0; i < both; ++i, ++tile) {
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
         const int t = it->first + i;
-        // (each four warps take a chunk, while the scores are on their way)
         const bool edge = edge_tile(*it, t, p.causal);
-        if (edge) {
-          ok = __all_sync(0xffffffffu, wait_for(bar(sm->edge[edges % kDepth]), (edges / kDepth) & 1, abort_flag));
-          if (!ok) break;
-          ++edges;
-          if (fix_values(ring + (tile * kPer + kQk + x) % kRing * kChunk, max(0, low - t * kKeys), min(kKeys, it->k_len - t * kKeys), r))
-            *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n % kItems].odd) = 1u;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(sm->v_full[tile % kDepth]));
-        }
-        if (i >= n) continue;
         wait_for(bar(sm->s_full[x]), tiles++ & 1, abort_flag);  // (after an abort the item runs out without waiting)
         __syncwarp();
         tc_fence_after();
@@ -644,7 +638,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(sm->p_ready[x]));
         lsum += l[0][0];
       }
-      if (!ok) break;
       if (n > 0) {
         const bool has = !(lsum <= 0.f);  // (NaN: a key that is not finite, no empty row)
         if (row) {
@@ -670,9 +663,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ outputs
     const int r = threadIdx.x & 127;
     const int my_tok = r / p.group, my_sub = r % p.group;
-    uint32_t items[2] = {0u, 0u};
+    uint32_t items[2] = {0u, 0u}, tile = 0, edges = 0;
     bool ok = true;
     while (ok && next_item()) {
+      // The item's tiles with unseen keys, which are its last; then its rows.
+      const int n = max(it->n[0], it->n[1]), low = seen_by(*it, 0, p.causal);
+#pragma unroll 1
+      for (int i = max(low / kKeys - it->first, 0); i < n; ++i, ++edges) {
+        ok = __all_sync(0xffffffffu, wait_for(bar(sm->edge[edges % kDepth]), (edges / kDepth) & 1, abort_flag));
+        if (!ok) break;
+        const int from = (it->first + i) * kKeys, seen = max(0, low - from), valid = min(kKeys, it->k_len - from);
+        bool odd = false;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) odd |= fix_values(ring + ((tile + i) * kPer + kQk + c) % kRing * kChunk, seen, valid, r);
+        if (odd) *reinterpret_cast<volatile uint32_t*>(&sm->items[it_n % kItems].odd) = 1u;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm->v_full[(tile + i) % kDepth]));
+      }
+      tile += n;
 #pragma unroll 1
       for (int x = 0; x < 2 && ok; ++x) {
         const int at = it->off[x] + my_tok;
@@ -884,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kHasRope) load_4d_if(leader, ring + (c0 + 2) % kRing * kChunk, &maps.rope, 0, row, 0, rope_head, kb, keep);
           if (i == 0) queries(1);
           if (!ok || (tile >= kK && !wait(sm->k_empty[(tile - kK) % kDepth], ((tile - kK) / kDepth) & 1))) break;
-          // values of a tile with unseen keys complete on a barrier of the softmax warps', which then complete the products'
+          // values of a tile with unseen keys complete on a barrier of the output warps', which then complete the products'
           const bool edge = edge_tile(*it, it->first + i, p.causal);
           // the ring is short of a load's way from memory; of blocks on the same keys the longest sends
           // for them (one prompt of 16384 tokens 855 -> 820 us; pieces of a few rows' keys are
@@ -895,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t vb = uniform(bar(edge ? sm->edge[edges++ % kDepth] : sm->v_full[o]));
           expect_if(leader, vb, 2 * kChunk);
-          if (leader && !edge) mbar_arrive_many(vb, 7);
+          if (leader && !edge) mbar_arrive_many(vb, 3);
           if (!kHasRope || cv + 1 < kRing) {
             load_4d_if(leader, ring + cv * kChunk, &maps.v, 0, row, 0, head, vb, keep);
           } else {
