@@ -44,16 +44,19 @@
 // behind it, 1280 (192 columns) or 1024 cycles, and three signals of 0.1 us.  The two tiles'
 // chains overlap, so that the tensor cores are busy 75 to 85 % of the time on long
 // items; an item's start and end cost about 2 us (first loads, both chains in step).
-// Measured: 76 heads of 4096 tokens over 4096 keys, no mask, 464 us = 1.76 PFLOP/s (92 % of the
-// matrix rate); one causal prompt of 16 heads of 16384 tokens 820 us = 1.67; two of 128 heads of 2048 and
-// 4096 525 us = 1.63; 61 of 1 to 601 tokens, 64 heads, 275 us = 5.0 TB/s; a single tile 6.3 us.
+// Measured: 76 heads of 4096 tokens over 4096 keys, no mask, 456 us = 1.79 PFLOP/s (94 % of the
+// matrix rate); one causal prompt of 16 heads of 16384 tokens 790 us = 1.74; two of 128 heads of 2048 and
+// 4096 520 us = 1.65; 61 of 1 to 601 tokens, 64 heads, 274 us = 5.0 TB/s; a single tile 6.0 us.
 // On the way here (16384 tokens): one lane walking the products' loop 1841 us, all lanes 1476,
 // whole boxes for two chunks and no row maxima 1288, a warp for each tile's products and code that fits
 // the instruction cache 1132, loads and descriptors off the way 997 and 935, without the
 // second sum 868, keys and values towards L2 820.  Not kept: P handed over by halves (930 where it was 895; the
-// ragged 61 and chunks of a prompt gained 3 %), the rounded probabilities' sum (5 to 8 % more everywhere), queries
-// and first keys towards L2 ahead of their item, both tiles on one tile's rows where rows are few, the
-// products' loop flattened across items (grouped heads 125 -> 155), four items in hand (137 -> 144).
+// ragged 61 and chunks of a prompt gained 3 %), the rounded probabilities' sum (5 to 8 % more everywhere), queries,
+// first keys and values towards L2 ahead of their item (61 short prompts 274 -> 276 to 281), both tiles on one
+// tile's rows where rows are few, the products' loop flattened across items (64 on 8 heads 125 -> 155), four
+// items in hand (137 -> 144), a third tile of queries instead of half a tile of ring for 128 columns (76 heads
+// 405 -> 390, but 32 on 8 heads, causal, 331 -> 340), boxes of 64 tokens where a tile's last half is not
+// needed (61 short prompts 274 -> 291, whose surplus of 190 MB read they would have halved).
 //
 // Waits are bounded; after one has run out every role leaves, and the block pauses
 // before it frees TMEM and ends.
@@ -201,7 +204,7 @@ __device__ __forceinline__ void check_ranges(const Params& p, int lane) {
 }
 
 // Where a search for items stands: 32 sequences, a lane each, the one with the most keys
-// first, and the items before them.
+// first where the order counts, and the items before them.
 struct Window {
   int base;                 // the first of the sequences; -1: none looked at
   uint32_t before, all;     // items of sequences before these, of these
@@ -224,10 +227,15 @@ __device__ __forceinline__ void look_at(const Params& p, Window& w, int base, ui
   const int per = 2 * p.tokens;
   w.blocks = static_cast<uint32_t>(static_cast<uint64_t>(q_len + per - 1) * p.per_inverse >> 38);
   w.all = __reduce_add_sync(0xffffffffu, w.blocks) * (p.h_k * p.splits);
-  // the order counts where items wait for an SM and differ in length
+  // The order counts where items wait for an SM, differ in length, and the longest takes more than a
+  // sixteenth of the call.  Otherwise sequences come as they lie: what boxes hold of the next
+  // sequence's rows is then still in L2 when its turn comes (100 of 1 to 300 tokens, 128 heads, 483 us
+  // sorted, 469 so; with an eighth 8 of 300 to 3000, 32 heads, 213 -> 225).
   const uint32_t tiles = static_cast<uint32_t>(k_len + kKeys - 1) / kKeys;
   int from = lane;
-  if (w.all > p.parts && __reduce_max_sync(0xffffffffu, w.blocks > 0 ? tiles : 0u) != __reduce_min_sync(0xffffffffu, w.blocks > 0 ? tiles : ~0u)) {
+  const uint32_t most = __reduce_max_sync(0xffffffffu, w.blocks > 0 ? tiles : 0u);
+  if (w.all > p.parts && most != __reduce_min_sync(0xffffffffu, w.blocks > 0 ? tiles : ~0u) &&
+      static_cast<float>(most) * p.parts * 16.f > static_cast<float>(p.h_k) * __reduce_add_sync(0xffffffffu, w.blocks * tiles)) {
     int rank = 0;
 #pragma unroll 1
     for (int o = 0; o < 32; ++o) {
