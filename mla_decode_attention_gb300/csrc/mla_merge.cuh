@@ -1,6 +1,5 @@
 // Attention outputs over several sets of keys joined by their log-sum-exps:
-//   lse = ln sum_i e^lse_i,   out = sum_i e^(lse_i - lse) out_i
-// (DeepGEMM & FlashMLA article, section 7 merge formula).
+//   lse = ln sum_i e^lse_i,   out = sum_i e^(lse_i - lse) out_i.
 //
 // Bound by memory: n rows in, one out, nothing read twice.  A group of lanes owns a
 // row of one token and head, eight columns a lane and step, so a row moves in whole

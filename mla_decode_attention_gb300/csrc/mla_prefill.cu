@@ -15,24 +15,45 @@ using prefill::kRope;
 using prefill::kRows;
 using prefill::kValue;
 
-// Pieces that each block of query rows' keys are cut into: a piece for every SM where
-// blocks are few, each at least kLeastTiles key tiles on average (a piece costs its query
-// rows, its fp32 rows and their merge, together about as much as two tiles; 10 tokens of 16
-// heads over 1500 keys: 16.3 us with four tiles at least, 13.7 with three, 13.0 with two; 1000
-// tokens of 16 heads, causal, 22.9, 24.8, 25.1).  Several sequences differ in length:
-// then up to three pieces an SM, of twice as many tiles, which go to whoever is free (3 sequences
-// over 8000 to 16384 keys, 16 heads: 73 us with one an SM, 65 so, 70 with four; one
-// sequence over 12000: 35, 39, 44).  Known without the lengths, so that a workspace fits
-// whatever they are.
+// Pieces that each block of query rows' keys are cut into.  Known without the lengths, so that a
+// workspace fits whatever they are, and of kLeastTiles key tiles at least on average.
+//
+// Several sequences differ in length.  Where their blocks are fewer than SMs: up to three pieces an SM, which go
+// to whoever is free (3 sequences over 8000 to 16384 keys, 16 heads: 73 us with one an SM, 65
+// so, 70 with four).
+//
+// Otherwise what costs least by this count in key tiles: a piece costs its share of the keys and, cut, its
+// query rows, its fp32 rows and their merge, 1.5 tiles with few rows and 5 with all 256; a merge's launch costs 2.  Pieces
+// of one sequence end together, so they run in whole rounds; those of several fill
+// the gaps but for half of a long one at the end.  (us for 1, 2, 3, 4, 6, 8 pieces, 40 heads of 1024 over 9024 keys: 260,
+// 215, 197, 192, 197, 207; 200 heads of 100 over 12100: 287, 229, 220, 241, 236, 247; 128 heads of 512 over 16512:
+// 535, 572, 563, 529, 537, 549; 20 heads of 2048 over themselves: 42, 51, 57, 64; 2 sequences of 300
+// over 16300, 40 heads: 448, 305, 289, 275, 271, 275.)
 constexpr int kLeastTiles = 2, kMostSplits = 32;
 int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {
   const int64_t per = 2 * (kRows / (h_q / h_k));
   const int64_t blocks = (total_q + batch * (per - 1)) / per * h_k;
   if (blocks == 0) return 1;
   const int64_t tiles = total_k / batch / kKeys, sms = std::min(num_sm_parts, 1 << 16);
-  int64_t s = std::min(sms / blocks, tiles / kLeastTiles);
-  if (batch > 1) s = std::max(s, std::min(3 * sms / blocks, tiles / (2 * kLeastTiles)));
-  return static_cast<int>(std::clamp<int64_t>(s, 1, kMostSplits));
+  if (batch > 1 && blocks <= sms) {
+    const int64_t s = std::max(std::min(sms / blocks, tiles / kLeastTiles), std::min(3 * sms / blocks, tiles / (2 * kLeastTiles)));
+    return static_cast<int>(std::clamp<int64_t>(s, 1, kMostSplits));
+  }
+  // (a causal call's mean; without a mask rows have up to twice as many)
+  const double mean = static_cast<double>(std::max(total_k - total_q / 2, total_k / 2)) / batch / kKeys;
+  const double piece = 1.5 + 3.5 * static_cast<double>(total_q * h_q) / static_cast<double>(blocks * 2 * kRows);
+  int best = 1;
+  double least = 0.;
+  for (int s = 1; s <= std::clamp<int64_t>(tiles / kLeastTiles, 1, kMostSplits); ++s) {
+    const double each = s == 1 ? mean + 1. : mean / s + piece, launch = s == 1 ? 0. : 2.;
+    const int64_t rounds = (blocks * s + sms - 1) / sms;
+    const double cost = launch + (batch == 1 ? rounds * each : each * s * blocks / sms + 0.75 * mean / s);
+    if (s == 1 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 int check_sizes(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {

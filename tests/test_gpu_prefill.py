@@ -161,6 +161,14 @@ def test_few_rows_are_split_over_their_keys(q_lens, k_lens, h, causal, rope):
         check(c, *run(c, parts=parts), f"{parts} parts")
 
 
+@pytest.mark.parametrize("q_lens,k_lens,h,parts", [([40], [2000], 5, 4), ([40, 3], [4000, 3800], 5, 8), ([300], [4300], 3, 4)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_blocks_than_parts_are_cut_where_rounds_would_stay_part_full(q_lens, k_lens, h, parts, causal):
+    c = case(q_lens, k_lens, h, causal=causal, seed=parts)
+    assert binding.mla_prefill_workspace_size(sum(q_lens), sum(k_lens), len(q_lens), h, h, parts) > 0
+    check(c, *run(c, parts=parts))
+
+
 def test_results_do_not_depend_on_timing():
     c = case([700, 90, 333], [900, 90, 1000], 6, 2)
     first = run(c)
