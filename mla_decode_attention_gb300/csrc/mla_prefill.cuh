@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // for its own, and so late that nobody sits on work that others could begin (64 on 8
         // heads, three prompts: 134 us with an item in hand all the time, 125 so).
         if (k > 0) ok = ok && __all_sync(0xffffffffu, wait_for(bar(sm->item_ahead), (k - 1) & 1, abort_flag));
-        bool found = false;
+        bool found = false, first = false;
         while (ok && !found) {
           if (!have) {
             if (lane == 0) {
@@ -971,13 +971,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok || !cancelled_block(smem_u32(&sm->answer), &index)) break;  // (after a no, no further question)
           }
           have = false;
+          first = first || index == 0u;  // (whether there is an item behind it or not)
           found = find_item(p, index, window, *slot, k & 1, lane);  // (the grid may have more blocks than items)
         }
         if (!ok) break;
         if (!found && lane == 0) slot->n_tok = 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sm->item_full[k % kItems]));
-        if (index == 0) check_ranges(p, lane);  // (by whoever has the first item)
+        if (first) check_ranges(p, lane);  // (by whoever has the first block, behind its item)
         if (!found) break;
       }
     }
