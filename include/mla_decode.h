@@ -585,7 +585,7 @@ int mla_prefill_workspace_size(int64_t total_q, int64_t total_k, int batch, int 
  *  A query that sees no key gets out = 0, lse = -inf.  What a query does not see leaves
  *  no trace in its outputs, NaN and infinities included.  One that sees a key with a
  *  NaN gets NaN in its whole row and lse, one that sees a value that is not finite gets
- *  one in that column.  out must not overlap the inputs.
+ *  one in that column.  Scores of any size that fp32 holds.  out must not overlap the inputs.
  */
 int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
                 int64_t k_token_stride, int64_t k_head_stride, const void* k_rope,

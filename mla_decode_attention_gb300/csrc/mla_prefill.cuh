@@ -88,7 +88,11 @@ constexpr int kDepth = 4;     // barriers of each kind: more tiles than the ring
 // above the row's maximum from where a tile's probabilities sum past 1 on.  It need not be
 // near the maximum: bf16 has fp32's exponents, so probabilities keep their precision
 // wherever they lie.  So the maximum is hardly ever looked for and O hardly ever rescaled.
-constexpr float kAbove = 24.f, kMoveSum = 1.f;
+// r * sc + 24 is rounded to fp32, past kFar by more than 1: the weights of a row's largest scores could then
+// leave fp32 at either end.  A row whose reference lies past kFar (a far row; no trained model has such
+// scores) keeps r itself, in the scores' units: each tile's maximum goes into it, and it is subtracted from the tile's
+// scores in TMEM before they are scaled.
+constexpr float kAbove = 24.f, kMoveSum = 1.f, kFar = 16777216.f;
 constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdescPv = idesc_bf16(128, 128, false, true);
 constexpr uint32_t kIdescPvHalf = idesc_bf16(128, 64, false, true);
@@ -555,6 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = seen_by(*it, min(at, it->n_tok - 1), p.causal);
       const bool row = my_tok < p.tokens && at < it->n_tok;
       float m = 0.f, lsum = 0.f;
+      bool far = false, any_far = false;  // this row, some row of the warp
+      float far_ref = -INFINITY;
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const int t = it->first + i;
@@ -579,16 +585,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        if (i == 0) {  // (a score of -inf says nothing: any other then passes the bound)
+        if (i == 0) {  // (a row that does not see the piece's first key sees none of it)
           const float u = tmem_ld1(t_s);
           m = u == -INFINITY ? -1e38f : u * sc + kAbove;
+          far = row && lim > 0 && !(fabsf(m) <= kFar);
+          m = far ? kAbove : m;
+          any_far = __any_sync(0xffffffffu, far);
         }
         // The row maximum is looked for only where the probabilities sum past the bound, which one of
         // them far above the reference needs; the warp then takes the pass again.
         bool again = false;
 #pragma unroll 1
         do {
-          if (again) {
+          if (again || any_far) {
             float top = -INFINITY;
 #pragma unroll 1
             for (int j = 0; j < 8; ++j) {
@@ -600,10 +609,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (this tile's scores were issued after the last tile's p.v and have completed: O holds every tile
             // before; a row moves by its own sum alone, whatever its neighbours in the warp do)
-            top = top * sc + kAbove;
-            const bool move = !(l[0][0] <= kMoveSum) && top > m;
-            const float alpha = move ? fast_exp2(m - top) : 1.f;
-            m = move ? top : m;
+            float alpha = 1.f, less = 0.f;  // less: to be subtracted from the row's scores
+            if (far && !again) {
+              if (top > far_ref) {
+                alpha = fast_exp2((far_ref - top) * sc);
+                far_ref = top;
+              }
+              less = far_ref == -INFINITY ? 0.f : far_ref;
+            } else if (!far && again) {
+              const float up = top * sc + kAbove;
+              if (!(l[0][0] <= kMoveSum) && up > m) {
+                far = row && up > kFar;
+                if (far) far_ref = less = top;
+                alpha = fast_exp2(far ? __fmaf_rn(-top, sc, m) - kAbove : m - up);
+                m = far ? kAbove : up;
+              }
+            }
             lsum *= alpha;
 #pragma unroll 1
             for (int j = 0; j < 8 && i > 0; ++j) {
@@ -613,6 +634,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[k] *= alpha;
               tmem_st16(t_o + 16 * j, o);
+            }
+            any_far = __any_sync(0xffffffffu, far);
+            if (any_far) {
+#pragma unroll 1
+              for (int j = 0; j < 8; ++j) {
+                float v[16];
+                tmem_ld16(t_s + 16 * j, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] -= less;
+                tmem_st16(t_s + 16 * j, v);
+              }
+              tmem_wait_st();
             }
           }
 #pragma unroll
@@ -652,7 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool has = !(lsum <= 0.f);  // (NaN: a key that is not finite, no empty row)
         if (row) {
           const int64_t h = static_cast<int64_t>(it->head) * p.group + my_sub, tok = it->q_row + at;
-          const float l = has ? (m + __log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+          constexpr float kLn2 = 0.69314718055994531f;
+          const float l2 = (m + __log2f(lsum)) * kLn2, l = !has ? -INFINITY : (far ? __fmaf_rn(far_ref, sc * kLn2, l2) : l2);
           if (p.splits == 1)
             p.lse[h * p.total_q + tok] = l;
           else
