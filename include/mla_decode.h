@@ -608,7 +608,8 @@ int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, co
  *               mla_prefill's [h_q, total_q] both fit)
  *  out, lse     [tokens, h_q, d] bf16 and [h_q, tokens] fp32, by strides
  *  tokens * h_q <= 2^31.  A part with lse_i = -inf has no weight and its row leaves no
- *  trace, whatever it holds; a row without any other gets out = 0, lse = -inf.  out may
+ *  trace, whatever it holds (any other part's does: what is not finite stays so, however
+ *  small the weight); a row without any other gets out = 0, lse = -inf.  out may
  *  be one of the parts itself with the same strides, and lse its lse; otherwise
  *  outputs must not overlap inputs.  Sums are fp32, each output rounded once.
  */

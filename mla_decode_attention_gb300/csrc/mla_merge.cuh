@@ -80,8 +80,9 @@ template <bool kF32, int kUnits, int kAhead>
 constexpr int kBlocks = kUnits * kAhead * (kF32 ? 2 : 1) < 8 || !(kF32 || kUnits == 2) ? 8 : (kF32 && kUnits == 2 ? 6 : 7);
 
 // kLanes lanes a row, kUnits units of eight columns a lane, kAhead parts' units in flight: the
-// first are requested before the weights are known.  (A row read for nothing, because its
-// weight turns out 0, leaves no trace.)
+// first are requested before the weights are known.  (A row read for nothing, because its part
+// has no key, leaves no trace.  One whose weight is so small that it rounds to 0 is added all the same: what is
+// not finite in it belongs to the sum.)
 template <bool kF32, int kLanes, int kUnits, int kAhead>
 __global__ void __launch_bounds__(kThreads, kBlocks<kF32, kUnits, kAhead>) merge_kernel(const __grid_constant__ Params p) {
   static_assert(kLanes % kAhead == 0, "parts of a step have their weights in one register each");
@@ -118,19 +119,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks<kF32, kUnits, kAhead>) merge
   sum = group_sum<kLanes>(sum);
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // (NaN stays)
   float acc[kUnits][8] = {};
-  float w_mine = 0.f;
+  float w_mine = -1.f;  // (no part)
   for (int i0 = 0; i0 < p.n; i0 += kAhead) {
     if (i0 > 0) request(i0);
     if (i0 % kLanes == 0) {  // the next kLanes parts' weights, a lane each
       const float v = i0 == 0 ? first : (in && i0 + l < p.n ? lses[(i0 + l) * p.lse_part] : -INFINITY);
-      w_mine = v == -INFINITY ? 0.f : expf(v - ref) * inv;
+      w_mine = v == -INFINITY ? -1.f : expf(v - ref) * inv;
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const float w = __shfl_sync(0xffffffffu, w_mine, i0 % kLanes + j, kLanes);
 #pragma unroll
       for (int k = 0; k < kUnits; ++k)
-        if (w != 0.f && 8 * (l + kLanes * k) < p.d) u[j][k].add(w, acc[k]);
+        if (!(w < 0.f) && 8 * (l + kLanes * k) < p.d) u[j][k].add(w, acc[k]);
     }
   }
   __syncwarp();  // every lane has read the log-sum-exps that lane 0 may write over
