@@ -19,8 +19,13 @@ using prefill::kValue;
 // workspace fits whatever they are, and of kLeastTiles key tiles at least on average.
 //
 // Several sequences differ in length.  Where their blocks are fewer than SMs: up to three pieces an SM, which go
-// to whoever is free (3 sequences over 8000 to 16384 keys, 16 heads: 73 us with one an SM, 65
-// so, 70 with four).
+// to whoever is free (3 sequences over 8000 to 16384 keys, 16 heads: 69 us with one an SM, 64
+// so, 67 with four), or none: whole, the call takes as long as its longest block; cut, as its pieces on
+// all SMs and a quarter of the longest at the end.  In key tiles, a piece costs 1.5 with few rows and 3.5 with all 256,
+// a launch 4, the merge 2.  (us whole and in 2, 3, 4 pieces, causal: 2 of 2048 tokens, 8 heads, 41, 45, 47, 53; 2 of
+// 1024, 16 heads, 24, 35, 40, 46; over 2048 keys 42, 50, 53, 58; 2 of 4096, 4 heads, 75, 58, 57, 63; 16 tokens over
+// 1000 keys each, 4 heads, 16.8, 14.7, 17.6, 17.2; over 4000, 8 heads, 53, 57, 58, 58; 2 of 100 over 1500, 8 heads, 22,
+// 17, 14, 13.)
 //
 // Otherwise what costs least by this count in key tiles: a piece costs its share of the keys and, cut, its
 // query rows, its fp32 rows and their merge, 1.5 tiles with few rows and 5 with all 256; a merge's launch costs 2.  Pieces
@@ -35,13 +40,17 @@ int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int
   const int64_t blocks = (total_q + batch * (per - 1)) / per * h_k;
   if (blocks == 0) return 1;
   const int64_t tiles = total_k / batch / kKeys, sms = std::min(num_sm_parts, 1 << 16);
-  if (batch > 1 && blocks <= sms) {
-    const int64_t s = std::max(std::min(sms / blocks, tiles / kLeastTiles), std::min(3 * sms / blocks, tiles / (2 * kLeastTiles)));
-    return static_cast<int>(std::clamp<int64_t>(s, 1, kMostSplits));
-  }
   // (a causal call's mean; without a mask rows have up to twice as many)
   const double mean = static_cast<double>(std::max(total_k - total_q / 2, total_k / 2)) / batch / kKeys;
-  const double piece = 1.5 + 3.5 * static_cast<double>(total_q * h_q) / static_cast<double>(blocks * 2 * kRows);
+  const double full = static_cast<double>(total_q * h_q) / static_cast<double>(blocks * 2 * kRows);
+  if (batch > 1 && blocks <= sms) {
+    const int64_t up_to = std::max(std::min(sms / blocks, tiles / kLeastTiles), std::min(3 * sms / blocks, tiles / (2 * kLeastTiles)));
+    const int s = static_cast<int>(std::clamp<int64_t>(up_to, 1, kMostSplits));
+    const double piece = 1.5 + 2. * full, length = static_cast<double>(total_k) / batch / kKeys, longest = length / s + piece;
+    const double cut = 6. + std::max(longest, (mean / s + piece) * s * blocks / sms + 0.25 * longest);
+    return cut < 5. + length ? s : 1;
+  }
+  const double piece = 1.5 + 3.5 * full;
   int best = 1;
   double least = 0.;
   for (int s = 1; s <= std::clamp<int64_t>(tiles / kLeastTiles, 1, kMostSplits); ++s) {
