@@ -550,8 +550,9 @@ int mla_gather_kv(const void* kv_cache, int kv_format, int64_t num_pages, const 
 
 /*
  * Size in bytes of mla_prefill's workspace for these arguments: 0, or fp32 partial
- * outputs and LSEs when few blocks of query rows are cut along their keys to fill the
- * device.  One workspace serves one call at a time.
+ * outputs and LSEs where cutting blocks of query rows along their keys saves time
+ * worth it (blocks that do not fill the device, or fill rounds of its SMs and a bit); at most
+ * 2048 * 516 bytes for each of num_sm_parts.  One workspace serves one call at a time.
  */
 int mla_prefill_workspace_size(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k,
                                int num_sm_parts, size_t* bytes);

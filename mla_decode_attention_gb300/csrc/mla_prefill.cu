@@ -34,31 +34,38 @@ using prefill::kValue;
 // 215, 197, 192, 197, 207; 200 heads of 100 over 12100: 287, 229, 220, 241, 236, 247; 128 heads of 512 over 16512:
 // 535, 572, 563, 529, 537, 549; 20 heads of 2048 over themselves: 42, 51, 57, 64; 2 sequences of 300
 // over 16300, 40 heads: 448, 305, 289, 275, 271, 275.)
+//
+// Pieces take a workspace: 516 bytes for each of their rows.  So they are made only where they save a thirtieth by
+// this count (the saving of thousands of blocks is less than its error: 8192 tokens of 128 heads over 262144 keys, two
+// sequences, two pieces for 0.5 % and 1.1 GB), and their rows are those of eight full blocks an SM at most, 160 MB on 152.
 constexpr int kLeastTiles = 2, kMostSplits = 32;
+constexpr int64_t kMostPartialRows = 8 * 2 * kRows;  // for each SM
+constexpr double kWorth = 29. / 30.;
 int splits_of(int64_t total_q, int64_t total_k, int batch, int h_q, int h_k, int num_sm_parts) {
   const int64_t per = 2 * (kRows / (h_q / h_k));
   const int64_t blocks = (total_q + batch * (per - 1)) / per * h_k;
-  if (blocks == 0) return 1;
+  if (total_q == 0) return 1;
   const int64_t tiles = total_k / batch / kKeys, sms = std::min(num_sm_parts, 1 << 16);
+  const int64_t most = std::clamp<int64_t>(sms * kMostPartialRows / (total_q * h_q), 1, kMostSplits);
   // (a causal call's mean; without a mask rows have up to twice as many)
   const double mean = static_cast<double>(std::max(total_k - total_q / 2, total_k / 2)) / batch / kKeys;
   const double full = static_cast<double>(total_q * h_q) / static_cast<double>(blocks * 2 * kRows);
   if (batch > 1 && blocks <= sms) {
     const int64_t up_to = std::max(std::min(sms / blocks, tiles / kLeastTiles), std::min(3 * sms / blocks, tiles / (2 * kLeastTiles)));
-    const int s = static_cast<int>(std::clamp<int64_t>(up_to, 1, kMostSplits));
+    const int s = static_cast<int>(std::clamp<int64_t>(up_to, 1, most));
     const double piece = 1.5 + 2. * full, length = static_cast<double>(total_k) / batch / kKeys, longest = length / s + piece;
     const double cut = 6. + std::max(longest, (mean / s + piece) * s * blocks / sms + 0.25 * longest);
-    return cut < 5. + length ? s : 1;
+    return cut < kWorth * (5. + length) ? s : 1;
   }
   const double piece = 1.5 + 3.5 * full;
   int best = 1;
   double least = 0.;
-  for (int s = 1; s <= std::clamp<int64_t>(tiles / kLeastTiles, 1, kMostSplits); ++s) {
+  for (int s = 1; s <= std::clamp<int64_t>(tiles / kLeastTiles, 1, most); ++s) {
     const double each = s == 1 ? mean + 1. : mean / s + piece, launch = s == 1 ? 0. : 2.;
     const int64_t rounds = (blocks * s + sms - 1) / sms;
     const double cost = launch + (batch == 1 ? rounds * each : each * s * blocks / sms + 0.75 * mean / s);
     if (s == 1 || cost < least) {
-      least = cost;
+      least = s == 1 ? kWorth * cost : cost;
       best = s;
     }
   }
