@@ -585,12 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        if (i == 0) {  // (a row that does not see the piece's first key sees none of it)
-          const float u = tmem_ld1(t_s);
-          m = u == -INFINITY ? -1e38f : u * sc + kAbove;
-          far = row && lim > 0 && !(fabsf(m) <= kFar);
-          m = far ? kAbove : m;
-          any_far = __any_sync(0xffffffffu, far);
+        // (a row that does not see the piece's first key sees none of it; where that key's score is no reference, the
+        // sum is NaN and the pass taken again)
+        if (i == 0) {
+          m = tmem_ld1(t_s) * sc + kAbove;
+          m = lim <= 0 ? 0.f : (fabsf(m) <= kFar ? m : NAN);
         }
         // The row maximum is looked for only where the probabilities sum past the bound, which one of
         // them far above the reference needs; the warp then takes the pass again.
@@ -618,11 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               less = far_ref == -INFINITY ? 0.f : far_ref;
             } else if (!far && again) {
               const float up = top * sc + kAbove;
-              if (!(l[0][0] <= kMoveSum) && up > m) {
-                far = row && up > kFar;
-                if (far) far_ref = less = top;
-                alpha = fast_exp2(far ? __fmaf_rn(-top, sc, m) - kAbove : m - up);
+              if (!(l[0][0] <= kMoveSum) && !(up <= m)) {
+                far = row && !(fabsf(up) <= kFar);
+                if (i > 0) alpha = fast_exp2(far ? __fmaf_rn(-top, sc, m) - kAbove : m - up);
                 m = far ? kAbove : up;
+                if (far) far_ref = top;
+                if (far && top != -INFINITY) less = top;
               }
             }
             lsum *= alpha;
