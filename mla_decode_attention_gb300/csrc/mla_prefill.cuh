@@ -44,9 +44,11 @@
 // behind it, 1280 (192 columns) or 1024 cycles, and three signals of 0.1 us.  The two tiles'
 // chains overlap, so that the tensor cores are busy 75 to 85 % of the time on long
 // items; an item's start and end cost about 2 us (first loads, both chains in step).
-// Measured: 76 heads of 4096 tokens over 4096 keys, no mask, 456 us = 1.79 PFLOP/s (94 % of the
-// matrix rate); one causal prompt of 16 heads of 16384 tokens 790 us = 1.74; two of 128 heads of 2048 and
-// 4096 520 us = 1.65; 61 of 1 to 601 tokens, 64 heads, 274 us = 5.0 TB/s; a single tile 6.0 us.
+// Measured in the first 0.1 s of calls, and after a second of them, when the power limit has lowered the
+// clock: 76 heads of 4096 tokens over 4096 keys, no mask, 461 and 501 us = 1.77 and 1.63 PFLOP/s (93 % of the
+// burst matrix rate, 97 % of the sustained one); one causal prompt of 16 heads of 16384 tokens 774 and 825 us =
+// 1.78 and 1.67; two of 128 heads of 2048 and 4096 532 and 594 us = 1.62 and 1.45; 61 of 1 to 601 tokens, 64 heads, 278
+// and 296 us = 4.9 and 4.6 TB/s; a single tile 6.2 us.
 // On the way here (16384 tokens): one lane walking the products' loop 1841 us, all lanes 1476,
 // whole boxes for two chunks and no row maxima 1288, a warp for each tile's products and code that fits
 // the instruction cache 1132, loads and descriptors off the way 997 and 935, without the
